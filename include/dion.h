@@ -378,6 +378,101 @@ int dion_apply_batched(const float* const* Q, const void* const* X, void* const*
                        int32_t batch, int32_t dtype, int32_t precision, void* workspace, size_t workspace_bytes,
                        void* stream);
 
+/* ---- Operators of a training step around the optimizer ------------------
+ * What a distillation step needs beside it: a teacher that runs in 8 bits
+ * (norm with 8-bit output, 8-bit product), the student's norm with its
+ * gradient, and the loss on the teacher's top logits with its gradient.
+ *
+ * Conventions (beside those above): matrices are row-major single device
+ * pointers with a row stride in elements (ld >= the row length; any
+ * alignment of at least one element); vectors are dense.  rows may be 0 (the
+ * call then writes nothing but dweight).  Pointers to elements of matrices
+ * without rows may be NULL.  Outputs must not overlap inputs or each other,
+ * except where a matrix is said to be allowed in place (the same pointer and
+ * stride).  Sums, norms and softmax statistics are held in fp32 and every
+ * result is rounded to its type once (to nearest even); no result depends on
+ * an order of atomics: equal calls give equal bits.  Each call is one
+ * profiled phase.  Workspaces as above (256-byte aligned; the size functions
+ * return 0 on invalid arguments). */
+
+/* RMS norm of rows with the residual's addition:
+ *   s = x + residual (residual may be NULL)   h = s rounded to x's type
+ *   rstd = 1 / sqrt(mean(s^2) + eps)          y = s * rstd * weight
+ *   x, residual, h, y   rows x cols of `dtype`; h may be NULL (not kept) and
+ *                       may be x or residual in place
+ *   weight              cols values of weight_dtype: `dtype` or DION_FP32
+ *   rstd                rows floats (dion_rmsnorm_backward reads them)
+ *   cols                1 .. 65536 (DION_E_UNSUPPORTED above)
+ * dion_rmsnorm_int8 writes y as 8-bit codes q with a scale for each row,
+ * for dion_int8_linear: scale = max|y| / 127, q = rint(y * (127 / max|y|)).
+ * A row with max|y| below 2^-119 has scale 0 and codes 0; a row in which an
+ * infinity or a NaN is left has scale NaN (and codes 0).  dion_int8_quantize
+ * does the same to rows of x as they are; dion_int8_dequantize reads codes
+ * back: y = q * scale. */
+int dion_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight, void* h,
+                 int64_t ldh, void* y, int64_t ldy, float* rstd, int64_t rows, int32_t cols, int32_t dtype,
+                 int32_t weight_dtype, float eps, void* stream);
+int dion_rmsnorm_int8(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight, void* h,
+                      int64_t ldh, int8_t* q, int64_t ldq, float* scale, int64_t rows, int32_t cols, int32_t dtype,
+                      int32_t weight_dtype, float eps, void* stream);
+int dion_int8_quantize(const void* x, int64_t ldx, int8_t* q, int64_t ldq, float* scale, int64_t rows, int32_t cols,
+                       int32_t dtype, void* stream);
+int dion_int8_dequantize(const int8_t* q, int64_t ldq, const float* scale, void* y, int64_t ldy, int64_t rows,
+                         int32_t cols, int32_t dtype, void* stream);
+
+/* Gradient of dion_rmsnorm.  With g = dy * weight and c = mean(g h) rstd^2:
+ *   dx = rstd * (g - h c) + dh     dweight_j = sum over rows of dy_j h_j rstd
+ * h and rstd are the forward's (h = x without a residual); dh, the gradient
+ * that reaches h itself along the residual stream, may be NULL.  dx is the
+ * gradient of x and of the residual alike; it may be dy or dh in place.
+ * dweight (cols values of weight_dtype) is summed in a fixed order. */
+size_t dion_rmsnorm_backward_workspace_size(int64_t rows, int32_t cols);
+int dion_rmsnorm_backward(const void* dy, int64_t lddy, const void* h, int64_t ldh, const void* weight,
+                          const float* rstd, const void* dh, int64_t lddh, void* dx, int64_t lddx, void* dweight,
+                          int64_t rows, int32_t cols, int32_t dtype, int32_t weight_dtype, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* Product of 8-bit integers with a scale for each token and channel:
+ *   out[i][j] = (sum_l a[i][l] b[j][l]) * a_scale[i] * b_scale[j] + bias[j]
+ * a: m x k activations, b: n x k weights (output channels as rows), both any
+ * int8 values; the sum is exact in 32 bits, k < 2^17 (DION_E_UNSUPPORTED
+ * above).  bias: n values of bias_dtype, or NULL.  out: m x n of out_dtype. */
+size_t dion_int8_linear_workspace_size(int64_t m, int64_t n, int32_t k);
+int dion_int8_linear(const int8_t* a, int64_t lda, const float* a_scale, const int8_t* b, int64_t ldb,
+                     const float* b_scale, const void* bias, int32_t bias_dtype, void* out, int64_t ldo, int64_t m,
+                     int64_t n, int32_t k, int32_t out_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Distillation from a teacher's top logits.  For each row, with student
+ * logits z (vocab values of `dtype`), k teacher logits t of teacher_dtype at
+ * the indices i (idx_bytes 4 or 8; dense rows x k) and temperature T > 0:
+ *   p = softmax of t / T over the present entries: those with an index in
+ *       [0, vocab) and a logit above -infinity
+ *   q = softmax(z / T)
+ *   loss = T^2 * sum_k p_k (log p_k - log q_{i_k})   (0 where p_k = 0)
+ *   d loss / d z_j = T * (q_j - sum over k with i_k = j of p_k)
+ * An index that appears twice counts twice.  A row with no present entry has
+ * loss 0 and gradient 0 whatever its logits hold (NaN included), and so has
+ * the gradient of a row whose grad_loss is 0.  k = 0 .. 1024.
+ *   loss       rows floats
+ *   stats      rows x 2 floats (8-byte aligned) that the backward call reads:
+ *              the largest z and log(sum exp((z - largest) / T))
+ *   grad_loss  rows floats: the gradient that reaches each row's loss; NULL = 1
+ *   dlogits    rows x vocab of `dtype`; may be the logits in place
+ * dion_distill_topk_step computes the loss and the gradient in one call, for
+ * a grad_loss known ahead of it. */
+size_t dion_distill_topk_workspace_size(int64_t rows, int32_t vocab);
+int dion_distill_topk(const void* logits, int64_t ldz, const void* teacher, const void* teacher_idx, float* loss,
+                      float* stats, int64_t rows, int32_t vocab, int32_t k, int32_t dtype, int32_t teacher_dtype,
+                      int32_t idx_bytes, float temperature, void* workspace, size_t workspace_bytes, void* stream);
+int dion_distill_topk_backward(const float* grad_loss, const void* logits, int64_t ldz, const float* stats,
+                               const void* teacher, const void* teacher_idx, void* dlogits, int64_t ldd, int64_t rows,
+                               int32_t vocab, int32_t k, int32_t dtype, int32_t teacher_dtype, int32_t idx_bytes,
+                               float temperature, void* stream);
+int dion_distill_topk_step(const void* logits, int64_t ldz, const void* teacher, const void* teacher_idx,
+                           const float* grad_loss, float* loss, void* dlogits, int64_t ldd, int64_t rows,
+                           int32_t vocab, int32_t k, int32_t dtype, int32_t teacher_dtype, int32_t idx_bytes,
+                           float temperature, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Useful floating-point operations of one dion_orth_batched call on this
  * batch, in the executed formulation, symmetric products counted once:
  * per matrix and restart segment of length L,

@@ -14,7 +14,9 @@ from ._lib import DION_BF16, DION_FP16, DION_FP32, PHASE, PREC, DionError, DionP
 __all__ = ["orth_batched", "rowsubset_step", "workspace_size", "useful_flops", "Orthogonalizer",
            "DionError", "QUINTIC", "profile_enable", "profile_records", "rowkeys_topk", "syrk", "sympoly",
            "apply", "rowsubset_step_update", "Dion3", "restart_points", "lowrank_step",
-           "lowrank_workspace_size", "orth_batched_noalloc", "NOALLOC_SCRATCH_BYTES"]
+           "lowrank_workspace_size", "orth_batched_noalloc", "NOALLOC_SCRATCH_BYTES",
+           "rmsnorm", "rmsnorm_int8", "rmsnorm_backward", "int8_quantize", "int8_dequantize", "int8_linear",
+           "distill_topk", "distill_topk_backward", "distill_topk_step", "rms_norm", "distill_loss"]
 
 QUINTIC = (3.4445, -4.7750, 2.0315)
 
@@ -487,3 +489,5 @@ def profile_records():
 
 
 from .optim import Dion3  # noqa: E402
+from .train_ops import (distill_loss, distill_topk, distill_topk_backward, distill_topk_step, int8_dequantize,  # noqa: E402
+                        int8_linear, int8_quantize, rms_norm, rmsnorm, rmsnorm_backward, rmsnorm_int8)

@@ -45,6 +45,10 @@ EXPORTS = (
     "dion_sympoly_batched", "dion_apply_batched", "dion_rowsubset_step_update", "dion_restart_points",
     "dion_lowrank_workspace_size", "dion_lowrank_step", "dion_orth_batched_noalloc", "dion_workspace_size_capped",
     "dion_profile_get_algorithmic",
+    "dion_rmsnorm", "dion_rmsnorm_int8", "dion_int8_quantize", "dion_int8_dequantize",
+    "dion_rmsnorm_backward_workspace_size", "dion_rmsnorm_backward", "dion_int8_linear_workspace_size",
+    "dion_int8_linear", "dion_distill_topk_workspace_size", "dion_distill_topk", "dion_distill_topk_backward",
+    "dion_distill_topk_step",
 )
 
 
@@ -122,6 +126,32 @@ def _load():
     lib.dion_rowsubset_step_update.argtypes = [pp, pp, pp, shp, i32, i32, i32, ctypes.c_float, fp, ctypes.c_float,
                                                prm, vp, vp, sz, vp]
     lib.dion_rowsubset_step_update.restype = ctypes.c_int
+    i64, f32 = ctypes.c_int64, ctypes.c_float
+    mat = [vp, i64]   # a device matrix and its row stride
+    lib.dion_rmsnorm.argtypes = mat + mat + [vp] + mat + mat + [vp, i64, i32, i32, i32, f32, vp]
+    lib.dion_rmsnorm.restype = ctypes.c_int
+    lib.dion_rmsnorm_int8.argtypes = lib.dion_rmsnorm.argtypes
+    lib.dion_rmsnorm_int8.restype = ctypes.c_int
+    lib.dion_int8_quantize.argtypes = mat + mat + [vp, i64, i32, i32, vp]
+    lib.dion_int8_quantize.restype = ctypes.c_int
+    lib.dion_int8_dequantize.argtypes = mat + [vp] + mat + [i64, i32, i32, vp]
+    lib.dion_int8_dequantize.restype = ctypes.c_int
+    lib.dion_rmsnorm_backward_workspace_size.argtypes = [i64, i32]
+    lib.dion_rmsnorm_backward_workspace_size.restype = sz
+    lib.dion_rmsnorm_backward.argtypes = mat + mat + [vp, vp] + mat + mat + [vp, i64, i32, i32, i32, vp, sz, vp]
+    lib.dion_rmsnorm_backward.restype = ctypes.c_int
+    lib.dion_int8_linear_workspace_size.argtypes = [i64, i64, i32]
+    lib.dion_int8_linear_workspace_size.restype = sz
+    lib.dion_int8_linear.argtypes = mat + [vp] + mat + [vp, vp, i32] + mat + [i64, i64, i32, i32, vp, sz, vp]
+    lib.dion_int8_linear.restype = ctypes.c_int
+    lib.dion_distill_topk_workspace_size.argtypes = [i64, i32]
+    lib.dion_distill_topk_workspace_size.restype = sz
+    lib.dion_distill_topk.argtypes = mat + [vp, vp, vp, vp, i64, i32, i32, i32, i32, i32, f32, vp, sz, vp]
+    lib.dion_distill_topk.restype = ctypes.c_int
+    lib.dion_distill_topk_backward.argtypes = [vp] + mat + [vp, vp, vp] + mat + [i64, i32, i32, i32, i32, i32, f32, vp]
+    lib.dion_distill_topk_backward.restype = ctypes.c_int
+    lib.dion_distill_topk_step.argtypes = mat + [vp, vp, vp, vp] + mat + [i64, i32, i32, i32, i32, i32, f32, vp, sz, vp]
+    lib.dion_distill_topk_step.restype = ctypes.c_int
     return lib
 
 

@@ -27,7 +27,11 @@ SOURCES = [
     ("lowrank_kernels.hip", ["-ffp-contract=off"]),
     ("lowrank_gemm.hip", []),
     ("tiny_kernels.hip", []),
+    ("norm_kernels.hip", []),
+    ("int8_gemm.hip", []),
+    ("distill_kernels.hip", []),
     ("dion_api.cpp", []),
+    ("train_api.cpp", []),
 ]
 
 BASE_FLAGS = [

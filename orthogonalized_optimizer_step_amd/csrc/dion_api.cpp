@@ -23,6 +23,7 @@
 #include "../../include/dion.h"
 #include "dion_internal.h"
 #include "lowrank_internal.h"
+#include "train_internal.h"
 
 namespace dion {
 // launchers (gemm_kernels.hip, stream_kernels.hip)
@@ -2010,6 +2011,31 @@ int scratch_address(void** out) {
 }
 
 }  // namespace
+
+namespace dion {
+
+int set_error(int code, const std::string& msg) { return fail(code, msg); }
+
+int run_phase(const char* name, const char* kernel, double flops, double bytes, hipStream_t stream,
+              const std::function<void()>& launch) {
+  ProfRec rec{name, kernel, nullptr, nullptr, flops, flops, bytes, flops};
+  if (g_prof.on) {
+    rec.a = g_prof.get();
+    rec.b = g_prof.get();
+    if (!rec.a || !rec.b || hipEventRecord(rec.a, stream) != hipSuccess)
+      return fail(DION_E_HIP, "profiling event failed");
+  }
+  launch();
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return hip_fail("kernel launch", e);
+  if (g_prof.on) {
+    if (hipEventRecord(rec.b, stream) != hipSuccess) return fail(DION_E_HIP, "profiling event failed");
+    g_prof.recs.push_back(rec);
+  }
+  return DION_OK;
+}
+
+}  // namespace dion
 
 extern "C" {
 
