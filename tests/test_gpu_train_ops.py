@@ -192,7 +192,7 @@ def test_quantize_codes_are_the_definition(dion, rows, cols, dtype, pad):
 LINEAR = [(1, 1, 1), (1, 5, 0), (2, 3, 17), (1, 64, 64), (1, 1000, 333), (3, 257, 128), (5, 31, 4096), (16, 96, 640),
           (17, 100, 300), (24, 520, 1024), (33, 129, 65), (64, 256, 2048), (65, 300, 511), (100, 64, 14336),
           (128, 128, 128), (129, 257, 200), (200, 1000, 777), (256, 512, 1024), (300, 270, 130), (515, 777, 640),
-          (1030, 260, 384)]
+          (1030, 260, 384), (70, 90, 48), (300, 140, 208), (1500, 1300, 1040), (4100, 4200, 400)]
 
 
 @pytest.mark.parametrize("m,n,k", LINEAR)
