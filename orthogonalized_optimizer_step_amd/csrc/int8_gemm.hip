@@ -9,6 +9,8 @@
 // 8 (e / 4) + 4 (l / 32) + e % 4 of the first operand and row l % 32 of the
 // second.  b goes first, so that a lane holds four consecutive channels of one
 // token.
+#include <algorithm>
+
 #include "train_device.h"
 #include "train_internal.h"
 
@@ -24,8 +26,8 @@ typedef intx4 intx4u __attribute__((aligned(1)));
 constexpr int BK = 128;   // bytes of k in a stage: one cache line of each row
 
 // Position of 16-byte chunk c of row r in its 128-byte LDS row: any 8
-// consecutive rows reading one chunk touch all 128 bytes, any 16 touch both
-// halves of 256, so the fragment reads meet no bank twice.
+// consecutive rows reading one chunk touch all 128 bytes, any 16 both halves
+// of 256, so the fragment reads meet no bank twice.
 __device__ __forceinline__ int swz(int r, int c) { return c ^ ((r ^ ((r >> 3) & 1)) & 7); }
 
 // One 16-byte copy per lane from global memory straight into LDS: lane l's
@@ -64,6 +66,13 @@ __device__ __forceinline__ intx4 load_chunk(const int8_t* row, int k, int ks) {
   return v;
 }
 
+// an output before its rounding
+__device__ __forceinline__ float scaled(const Int8Args& g, int64_t row, int64_t col, int sum) {
+  float v = (float)sum * g.sa[row] * g.sb[col];
+  if (g.bias) v += load_fmt(g.bias, col, g.bias_fmt);
+  return v;
+}
+
 template <typename O> struct OutVec;   // 16 bytes of output elements
 template <> struct OutVec<float> { static constexpr int N = 4; };
 template <> struct OutVec<bf16_t> { static constexpr int N = 8; };
@@ -89,15 +98,22 @@ __device__ __forceinline__ void tile_of_block(int TM, int TN, int& ti, int& tj) 
 // bytes are read from LDS while the present ones are multiplied, across the
 // stage's end too.
 template <int BM, int BN, int WM, int WN, int S, bool DMA, typename O>
-__global__ __launch_bounds__(64 * WM * WN) void k_int8_mma(Int8Args g) {
+__global__ __launch_bounds__(64 * WM * WN) void k_int8_mma(Int8Args g, int* partial) {
   constexpr int W = WM * WN, NT = 64 * W;
   constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32;   // wave tile, its fragments
   constexpr int STAGE = (BM + BN) * BK;
-  constexpr int NP = STAGE / 1024 / W;            // 1 KB pieces (8 rows) of a stage per wave
+  constexpr int NP = STAGE / 1024 / W;            // 1 KB pieces of a stage per wave
+  constexpr int PR = 1024 / BK, CR = BK / 16;     // rows of a piece, chunks of a row
   constexpr int OV = OutVec<O>::N, SROW = TN + OV;   // staged output row
   constexpr int STAGED = W * 32 * SROW * (int)sizeof(O);
   constexpr int LDS = S * STAGE > STAGED ? S * STAGE : STAGED;
-  static_assert(NP * W * 1024 == STAGE && BM % 8 == 0, "whole pieces");
+  // Copies of the stage S - 1 ahead: all at once after the turn, or (the
+  // largest tile, with one block per CU) spread over the products of two steps.
+  constexpr int KS = BK / 32, AHEAD = DMA ? S - 1 : 1;
+  constexpr bool SPREAD = DMA && BM * BN >= 256 * 256;
+  constexpr int PW = NP / 2, EVERY = SPREAD ? FM * FN / PW : 1;
+  static_assert(!SPREAD || (PW * 2 == NP && EVERY * PW == FM * FN), "the copies divide the products");
+  static_assert(S <= 4 && NP * W * 1024 == STAGE && BM % PR == 0, "whole pieces");
   __shared__ __attribute__((aligned(1024))) int8_t smem[LDS];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
@@ -107,11 +123,14 @@ __global__ __launch_bounds__(64 * WM * WN) void k_int8_mma(Int8Args g) {
   const int rm = (int)min((int64_t)BM, g.m - m0), rn = (int)min((int64_t)BN, g.n - n0);   // valid rows of the tile
   const int8_t* A = g.a + m0 * g.lda;
   const int8_t* B = g.b + n0 * g.ldb;
-  const int nk = (g.k + BK - 1) / BK;
+  // this split's stages
+  const int all = (g.k + BK - 1) / BK;
+  const int kt0 = (int)((int64_t)all * blockIdx.y / gridDim.y);
+  const int nk = (int)((int64_t)all * (blockIdx.y + 1) / gridDim.y) - kt0;
   const uint32_t lds0 = (uint32_t)(uintptr_t)((__attribute__((address_space(3))) int8_t*)smem);
 
-  // piece q = wave + i W of a stage: rows 8 q .. 8 q + 7 (a's, then b's), lane
-  // l row l / 8 and the chunk whose place is l % 8
+  // piece q = wave + i W of a stage: rows PR q .. of a, then of b; lane l has
+  // row l / CR and the chunk whose place is l % CR
   uint32_t voff[NP];
   int vk[NP];
   const intx4 ra = raw_buffer(A, (uint32_t)((rm - 1) * g.lda + g.k)), rb = raw_buffer(B, (uint32_t)((rn - 1) * g.ldb + g.k));
@@ -119,26 +138,22 @@ __global__ __launch_bounds__(64 * WM * WN) void k_int8_mma(Int8Args g) {
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
     const int q = wave + i * W;
-    const bool isa = q < BM / 8;
-    const int r = (isa ? q : q - BM / 8) * 8 + (lane >> 3);
-    vk[i] = swz(r, lane & 7) * 16;
+    const bool isa = q < BM / PR;
+    const int r = (isa ? q : q - BM / PR) * PR + lane / CR;
+    vk[i] = swz(r, lane % CR) * 16;
     voff[i] = r < (isa ? rm : rn) ? (uint32_t)(r * (isa ? g.lda : g.ldb)) + vk[i] : OUT_OF_RANGE;
   }
-  auto issue = [&](int kt) {
-    const int k0 = kt * BK;
-    const bool whole = k0 + BK <= g.k;
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      const int q = wave + i * W;
-      const bool isa = q < BM / 8;
-      if (DMA) {
-        const uint32_t v = whole || k0 + vk[i] < g.k ? voff[i] : OUT_OF_RANGE;
-        dma16(v, isa ? ra : rb, (uint32_t)k0,
-              (uint32_t)__builtin_amdgcn_readfirstlane(lds0 + (kt % S) * STAGE + q * 1024));
-      } else {
-        const int8_t* p = (isa ? A : B) + (int64_t)((isa ? q : q - BM / 8) * 8 + (lane >> 3)) * (isa ? g.lda : g.ldb);
-        reg[i] = voff[i] != OUT_OF_RANGE ? load_chunk(p, k0 + vk[i], g.k) : intx4{0, 0, 0, 0};
-      }
+  // piece i of stage kt: into LDS, or into registers
+  auto issue = [&](int kt, int i) {
+    const int k0 = (kt0 + kt) * BK, q = wave + i * W;
+    const bool isa = q < BM / PR;
+    if (DMA) {
+      const uint32_t v = k0 + vk[i] < g.k ? voff[i] : OUT_OF_RANGE;
+      dma16(v, isa ? ra : rb, (uint32_t)k0,
+            (uint32_t)__builtin_amdgcn_readfirstlane(lds0 + (kt % S) * STAGE + q * 1024));
+    } else {
+      const int8_t* p = (isa ? A : B) + (int64_t)((isa ? q : q - BM / PR) * PR + lane / CR) * (isa ? g.lda : g.ldb);
+      reg[i] = voff[i] != OUT_OF_RANGE ? load_chunk(p, k0 + vk[i], g.k) : intx4{0, 0, 0, 0};
     }
   };
   auto store = [&](int kt) {   // registers to LDS
@@ -167,38 +182,78 @@ __global__ __launch_bounds__(64 * WM * WN) void k_int8_mma(Int8Args g) {
       store(kt);
     }
     lds_barrier();
-    if (DMA) {
-      if (kt + S - 1 < nk) issue(kt + S - 1);
-    } else {
-      if (kt + 1 < nk) issue(kt + 1);
+    if (!SPREAD && kt + AHEAD < nk) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) issue(kt + AHEAD, i);
     }
   };
   if (nk > 0) {
     if (DMA) {
 #pragma unroll
-      for (int i = 0; i < S - 1; ++i)
-        if (i < nk) issue(i);
+      for (int t = 0; t < S - 1; ++t)
+        if (t < nk) {
+#pragma unroll
+          for (int i = 0; i < NP; ++i) issue(t, i);
+        }
     } else {
-      issue(0);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) issue(0, i);
     }
     turn(0);
+    if (SPREAD && S - 1 < nk) {
+#pragma unroll
+      for (int i = 0; i < PW; ++i) issue(S - 1, i);
+    }
     fetch(0, 0, 0);
     for (int kt = 0; kt < nk; ++kt) {
 #pragma unroll
-      for (int ks = 0; ks < BK / 32; ++ks) {
-        if (ks + 1 < BK / 32) {
+      for (int ks = 0; ks < KS; ++ks) {
+        if (ks + 1 < KS) {
           fetch(kt, ks + 1, (ks + 1) & 1);
         } else if (kt + 1 < nk) {
           turn(kt + 1);
           fetch(kt + 1, 0, 0);
         }
+        __builtin_amdgcn_sched_barrier(0);   // the reads above go out before the products, not beside their use
+        // the copies of step ks, one after every EVERY products: half of a
+        // stage's right after its turn, half beside the next step's products
+        const int w = (ks + 1) % KS, st = ks + 1 < KS ? kt + S - 1 : kt + S;
 #pragma unroll
         for (int i = 0; i < FM; ++i)
 #pragma unroll
-          for (int j = 0; j < FN; ++j)
+          for (int j = 0; j < FN; ++j) {
             acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[ks & 1][j], fa[ks & 1][i], acc[i][j], 0, 0, 0);
+            const int t = i * FN + j;
+            if (SPREAD && w < 2 && t % EVERY == EVERY - 1) {
+              __builtin_amdgcn_sched_barrier(0);
+              if (st < nk) issue(st, w * PW + t / EVERY);
+              __builtin_amdgcn_sched_barrier(0);
+            }
+          }
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
+  }
+  if (partial) {   // several splits: the sums as they are, for k_int8_join
+    int* out = partial + (int64_t)blockIdx.y * g.m * g.n;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int64_t row = m0 + wm * TM + i * 32 + r;
+      if (row >= g.m) continue;
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int64_t col = n0 + wn * TN + j * 32 + q * 8 + (lane >> 5) * 4;
+          int* o = out + row * g.n + col;
+          const intx4 v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+          if (col + 4 <= g.n) *(intx4u*)o = v;
+          else
+            for (int e = 0; e < 4; ++e)
+              if (col + e < g.n) o[e] = v[e];
+        }
+    }
+    return;
   }
   __syncthreads();   // the stages are free: each wave stages 32 rows of its output at a time
 
@@ -243,27 +298,157 @@ __global__ __launch_bounds__(64 * WM * WN) void k_int8_mma(Int8Args g) {
   }
 }
 
+// The splits' sums, scaled.
+template <typename O> __global__ __launch_bounds__(256) void k_int8_join(Int8Args g, const int* partial, int splits) {
+  const int64_t row = blockIdx.y, col = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (col >= g.n) return;
+  int v = 0;
+  for (int s = 0; s < splits; ++s) v += partial[((int64_t)s * g.m + row) * g.n + col];
+  ((O*)g.out)[row * g.ldo + col] = from_f<O>(scaled(g, row, col, v));
+}
+
+void launch_join(const Int8Args& a, int splits, hipStream_t s) {
+  const dim3 grid((unsigned)((a.n + 255) / 256), (unsigned)a.m);
+  if (a.out_fmt == 1) hipLaunchKernelGGL((k_int8_join<float>), grid, dim3(256), 0, s, a, a.partial, splits);
+  else if (a.out_fmt == 0) hipLaunchKernelGGL((k_int8_join<bf16_t>), grid, dim3(256), 0, s, a, a.partial, splits);
+  else hipLaunchKernelGGL((k_int8_join<fp16_t>), grid, dim3(256), 0, s, a, a.partial, splits);
+}
+
 template <int BM, int BN, int WM, int WN, int S, bool DMA>
-void launch_mma(const Int8Args& a, hipStream_t s) {
+void launch_mma(const Int8Args& a, int splits, hipStream_t s) {
   const int64_t tiles = (a.m + BM - 1) / BM * ((a.n + BN - 1) / BN);
-  const dim3 grid((unsigned)tiles), block(64 * WM * WN);
-  if (a.out_fmt == 1) hipLaunchKernelGGL((k_int8_mma<BM, BN, WM, WN, S, DMA, float>), grid, block, 0, s, a);
-  else if (a.out_fmt == 0) hipLaunchKernelGGL((k_int8_mma<BM, BN, WM, WN, S, DMA, bf16_t>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((k_int8_mma<BM, BN, WM, WN, S, DMA, fp16_t>), grid, block, 0, s, a);
+  const dim3 grid((unsigned)tiles, splits), block(64 * WM * WN);
+  int* part = splits > 1 ? a.partial : nullptr;
+  if (a.out_fmt == 1) hipLaunchKernelGGL((k_int8_mma<BM, BN, WM, WN, S, DMA, float>), grid, block, 0, s, a, part);
+  else if (a.out_fmt == 0) hipLaunchKernelGGL((k_int8_mma<BM, BN, WM, WN, S, DMA, bf16_t>), grid, block, 0, s, a, part);
+  else hipLaunchKernelGGL((k_int8_mma<BM, BN, WM, WN, S, DMA, fp16_t>), grid, block, 0, s, a, part);
+  if (part) launch_join(a, splits, s);
+}
+
+// Up to 16 tokens: the block takes 16 NW channels; its waves take 16 of them
+// and every KW-th 128-byte piece of the split's share of k each, and the sums
+// of the KW meet in LDS.  Fragments go from global memory to registers
+// (v_mfma_i32_16x16x64_i8: lane l holds 16 consecutive k of row l % 16, k
+// block l / 16; result element e of lane l is row 4 (l / 16) + e of the first
+// operand and row l % 16 of the second), at any alignment.  Rows past the end
+// repeat the last one and are not written.
+template <int NW, int KW, typename O>
+__global__ __launch_bounds__(64 * NW * KW) void k_int8_rows(Int8Args g, int* partial) {
+  __shared__ __attribute__((aligned(16))) int sum[KW * NW * 256];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int nw = wave % NW, kw = wave / NW;
+  const int64_t n0 = (int64_t)blockIdx.x * (16 * NW);
+  const int r = lane & 15, kc = (lane >> 4) * 16;
+  const int8_t* b = g.b + min(n0 + nw * 16 + r, g.n - 1) * g.ldb;
+  const int8_t* a = g.a + min((int64_t)r, g.m - 1) * g.lda;
+  intx4 acc = {0, 0, 0, 0};
+  const int pieces = (g.k + 127) / 128;
+  const int p0 = (int)((int64_t)pieces * blockIdx.y / gridDim.y);
+  const int kend = min(g.k, (int)((int64_t)pieces * (blockIdx.y + 1) / gridDim.y) * 128);
+  int k0 = (p0 + kw) * 128;
+#pragma unroll 4
+  for (; k0 + 128 <= kend; k0 += KW * 128) {
+#pragma unroll
+    for (int h = 0; h < 128; h += 64)
+      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(*(const intx4u*)(b + k0 + kc + h), *(const intx4u*)(a + k0 + kc + h),
+                                                  acc, 0, 0, 0);
+  }
+  if (k0 < kend) {   // the last piece, in part
+    for (int h = 0; h < 128; h += 64)
+      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(load_chunk(b, k0 + kc + h, kend), load_chunk(a, k0 + kc + h, kend),
+                                                  acc, 0, 0, 0);
+  }
+  // [kw][token][channel of the block]
+  *(intx4*)(sum + (kw * 16 + r) * (16 * NW) + nw * 16 + (lane >> 4) * 4) = acc;
+  __syncthreads();
+  for (int i = tid; i < NW * 256; i += 64 * NW * KW) {
+    int v = 0;
+#pragma unroll
+    for (int w = 0; w < KW; ++w) v += sum[w * NW * 256 + i];
+    const int64_t row = i / (16 * NW), col = n0 + i % (16 * NW);
+    if (row < g.m && col < g.n) {
+      if (partial) partial[((int64_t)blockIdx.y * g.m + row) * g.n + col] = v;
+      else ((O*)g.out)[row * g.ldo + col] = from_f<O>(scaled(g, row, col, v));
+    }
+  }
+}
+
+template <int NW, int KW>
+void launch_rows(const Int8Args& a, int splits, hipStream_t s) {
+  const dim3 grid((unsigned)((a.n + 16 * NW - 1) / (16 * NW)), splits), block(64 * NW * KW);
+  int* part = splits > 1 ? a.partial : nullptr;
+  if (a.out_fmt == 1) hipLaunchKernelGGL((k_int8_rows<NW, KW, float>), grid, block, 0, s, a, part);
+  else if (a.out_fmt == 0) hipLaunchKernelGGL((k_int8_rows<NW, KW, bf16_t>), grid, block, 0, s, a, part);
+  else hipLaunchKernelGGL((k_int8_rows<NW, KW, fp16_t>), grid, block, 0, s, a, part);
+  if (part) launch_join(a, splits, s);
 }
 
 }  // namespace
+
+// Which kernel takes a product, by its sizes alone (us on an MI355X, one
+// bf16 output).
+//  - Up to 16 tokens the rows kernel: its traffic is the weights', read once.
+//    Four channel groups to a block where that leaves most CUs a block (1 x
+//    14336 x 4096: 11.4 against 13.0 with one, and 5.0 TB/s); one where it
+//    would not (1 x 4096 x 4096: 6.2 against 11.2), and k split over blocks
+//    when there are few channels and each wave would have more than seven
+//    pieces of k (8 x 512 x 14336: 7.5 against 12.0).  Beyond 16 tokens its
+//    fragments of a cost more than they save (20 x 14336 x 4096: 20.7 against
+//    the 64 x 64 tile's 13.8).
+//  - Otherwise the tile whose rounds over the 256 CUs are shortest, from the
+//    time of one stage (128 bytes of k) and a tile's fixed cost: 256 x 256 one
+//    block per CU (8192 x 14336 x 4096: 490, 128 x 128: 590), 128 x 128
+//    (2048 x 4096 x 4096: 43, 256 x 256: 54) and 64 x 64 (512 x 4096 x 4096:
+//    18, 128 x 128: 28) two, at about half the time for a block alone.  Fewer
+//    than 128 tiles of 64 split k so that up to 256 blocks run, of eight
+//    stages at least (24 x 4096 x 14336: 14.3 against 35.3).
+struct Int8Plan {
+  enum { ROWS1, ROWS4, TILE64, TILE128, TILE256 } kind;
+  int splits;
+};
+
+static Int8Plan int8_plan(int64_t m, int64_t n, int k) {
+  const auto tiles = [&](int64_t t) { return (m + t - 1) / t * ((n + t - 1) / t); };
+  const int stages = (k + 127) / 128;
+  const auto split = [&](int64_t blocks, int least) {
+    return (int)std::max<int64_t>(1, std::min<int64_t>(256 / std::max<int64_t>(1, blocks), stages / least));
+  };
+  if (m <= 16) {
+    if (n >= 64 * 208) return {Int8Plan::ROWS4, 1};
+    return {Int8Plan::ROWS1, split((n + 15) / 16, 28)};
+  }
+  const int64_t t64 = tiles(64), t128 = tiles(128), t256 = tiles(256);
+  const int s64 = split(t64, 8);
+  const double c64 = (t64 * s64 <= 256 ? 0.30 : 0.55 * (double)((t64 * s64 + 511) / 512)) * stages / s64 +
+                     (s64 > 1 ? 5.0 : 3.0);
+  const double c128 = (t128 <= 256 ? 0.70 : 1.28 * (double)((t128 + 511) / 512)) * stages + 5.0;
+  const double c256 = 1.31 * (double)((t256 + 255) / 256) * stages + 9.0;
+  if (c256 <= c128 && c256 <= c64) return {Int8Plan::TILE256, 1};
+  if (c128 <= c64) return {Int8Plan::TILE128, 1};
+  return {Int8Plan::TILE64, s64};
+}
+
+size_t int8_linear_scratch(int64_t m, int64_t n, int k) {
+  const int splits = int8_plan(m, n, k).splits;
+  return splits > 1 ? (size_t)splits * m * n * 4 : 0;
+}
 
 void launch_int8_linear(const Int8Args& a, hipStream_t s) {
   // copies straight into LDS need rows at multiples of 16 bytes, whole 16-byte
   // chunks and 31-bit offsets inside a tile
   const bool dma = ((uintptr_t)a.a | (uintptr_t)a.b | (uint64_t)a.lda | (uint64_t)a.ldb | (uint64_t)a.k) % 16 == 0 &&
                    a.lda < (1 << 22) && a.ldb < (1 << 22);
-  const auto tiles = [&](int64_t t) { return (a.m + t - 1) / t * ((a.n + t - 1) / t); };
-  if (!dma) launch_mma<128, 128, 2, 2, 2, false>(a, s);
-  else if (tiles(256) >= 256) launch_mma<256, 256, 2, 2, 2, true>(a, s);
-  else if (tiles(128) >= 128) launch_mma<128, 128, 2, 2, 2, true>(a, s);
-  else launch_mma<64, 64, 2, 2, 4, true>(a, s);
+  const Int8Plan p = int8_plan(a.m, a.n, a.k);
+  switch (p.kind) {
+    case Int8Plan::ROWS1: return launch_rows<1, 4>(a, p.splits, s);
+    case Int8Plan::ROWS4: return launch_rows<4, 4>(a, p.splits, s);
+    case Int8Plan::TILE64:
+      return dma ? launch_mma<64, 64, 2, 2, 4, true>(a, p.splits, s) : launch_mma<64, 64, 2, 2, 2, false>(a, p.splits, s);
+    case Int8Plan::TILE128:
+      return dma ? launch_mma<128, 128, 2, 2, 2, true>(a, 1, s) : launch_mma<128, 128, 2, 2, 2, false>(a, 1, s);
+    case Int8Plan::TILE256:
+      return dma ? launch_mma<256, 256, 2, 4, 2, true>(a, 1, s) : launch_mma<128, 128, 2, 2, 2, false>(a, 1, s);
+  }
 }
 
 }  // namespace dion

@@ -2,6 +2,7 @@
 // checks, workspace sizes, and the launches as profiled phases.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <exception>
 #include <string>
@@ -226,7 +227,7 @@ size_t dion_int8_linear_workspace_size(int64_t m, int64_t n, int32_t k) {
     (void)guarded([&]() { return set_error(DION_E_INVAL, "m, n and k must not be negative"); });
     return 0;
   }
-  return 256;
+  return std::max<size_t>(256, align256(int8_linear_scratch(m, n, k)));
 }
 
 int dion_int8_linear(const int8_t* a, int64_t lda, const float* a_scale, const int8_t* b, int64_t ldb,
@@ -253,7 +254,8 @@ int dion_int8_linear(const int8_t* a, int64_t lda, const float* a_scale, const i
     }
     if (c.code != DION_OK || m == 0 || n == 0) return c.done();
     const hipStream_t st = (hipStream_t)stream;
-    const Int8Args g{a, b, a_scale, b_scale, bias, out, lda, ldb, ldo, m, n, k, bias_dtype, out_dtype};
+    const Int8Args g{a, b, a_scale, b_scale, bias, out, lda, ldb, ldo, m, n, k, bias_dtype, out_dtype,
+                     (int*)workspace};
     return run_phase("int8_linear", "dion::k_int8", 2.0 * m * n * k,
                      (double)m * k + (double)n * k + (double)m * n * esize(out_dtype), st,
                      [&]() { launch_int8_linear(g, st); });
