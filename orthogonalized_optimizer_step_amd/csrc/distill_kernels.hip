@@ -3,12 +3,16 @@
 // Row by row, with student logits z (vocab values), teacher logits t_k at
 // indices i_k and temperature T:
 //   p = softmax of t / T over the present entries (index inside the
-//   vocabulary, t_k > -inf);  log q_j = (z_j - m) / T - ls with m = max z and
-//   ls = log sum exp((z - m) / T)
+//   vocabulary, t_k > -inf);  q_j = exp((z_j - m) / T) / s with m = max z and
+//   s = sum exp((z - m) / T)
 //   loss = T^2 sum_k p_k (log p_k - log q_{i_k})   (terms with p_k = 0 are 0)
 //   dz_j = gl T (q_j - sum over k with i_k = j of p_k)
 // A row with no present entry has loss 0 and gradient 0, whatever z holds; a
 // row whose loss has gradient gl = 0 has gradient 0.
+//
+// Exponents are formed as (z - m) (log2(e) / T), subtraction first: exact
+// enough for the whole range of the types (z - m is 0 for the largest however
+// low the mask value that it may be), and one v_exp_f32 each.
 #include "train_device.h"
 #include "train_internal.h"
 
@@ -16,126 +20,318 @@ namespace dion {
 
 namespace {
 
-constexpr int NT = 256;
+constexpr float NEG = -__builtin_inff();
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
-// The teacher's distribution of one row in LDS.
-struct Teacher {
-  float logp[kDistillMaxK];   // log p_k, -inf where p_k = 0 or the entry is absent
-  int idx[kDistillMaxK];      // -1 where absent
-  float red[NT / 64];
+// 16 bytes of logits at element alignment
+typedef uint32_t uintx4 __attribute__((ext_vector_type(4)));
+typedef uintx4 uintx4u __attribute__((aligned(2)));
+
+template <typename Z> struct Chunk {
+  static constexpr int N = 16 / (int)sizeof(Z);
+  static __device__ __forceinline__ void unpack(const uintx4& v, float* f) {
+    union { uintx4 u; Z z[N]; } c;
+    c.u = v;
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = to_f(c.z[i]);
+  }
+  static __device__ __forceinline__ uintx4 pack(const float* f) {
+    union { uintx4 u; Z z[N]; } c;
+#pragma unroll
+    for (int i = 0; i < N; ++i) c.z[i] = from_f<Z>(f[i]);
+    return c.u;
+  }
+  // elements [j, j + N) of a row of n, -inf past its end
+  static __device__ __forceinline__ uintx4 load(const Z* row, int j, int n) {
+    if (j + N <= n) return *(const uintx4u*)(row + j);
+    float f[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = j + i < n ? to_f(row[j + i]) : NEG;
+    return pack(f);
+  }
+  static __device__ __forceinline__ void store(Z* row, int j, int n, const float* f) {
+    if (j + N <= n) {
+      *(uintx4u*)(row + j) = pack(f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (j + i < n) row[j + i] = from_f<Z>(f[i]);
+    }
+  }
 };
 
-__device__ __forceinline__ int64_t teacher_index(const DistillArgs& a, int64_t i) {
-  return a.idx64 ? ((const int64_t*)a.idx)[i] : (int64_t)((const int32_t*)a.idx)[i];
-}
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// Fills T for `row`; returns whether any entry is present.
-__device__ bool teacher_row(const DistillArgs& a, int64_t row, Teacher& T) {
-  float top = -__builtin_inff();
-  for (int k = threadIdx.x; k < a.k; k += NT) {
-    const int64_t i = teacher_index(a, row * a.k + k);
-    const float t = load_fmt(a.t, row * a.k + k, a.t_fmt);
-    const bool ok = i >= 0 && i < a.vocab && t != -__builtin_inff();
-    T.idx[k] = ok ? (int)i : -1;
-    T.logp[k] = t;
-    if (ok) top = max_nan(top, t);
-  }
-  top = block_max<NT>(top, T.red);
-  if (top == -__builtin_inff()) return false;
-  float s = 0.f;
-  for (int k = threadIdx.x; k < a.k; k += NT) {
-    const float u = T.idx[k] >= 0 ? (T.logp[k] - top) / a.temp : -__builtin_inff();
-    T.logp[k] = u;
-    s += expf(u);
-  }
-  const float ls = logf(block_sum<NT>(s, T.red));
-  for (int k = threadIdx.x; k < a.k; k += NT) {
-    const float lp = T.logp[k] - ls;
-    T.logp[k] = expf(lp) == 0.f ? -__builtin_inff() : lp;
-  }
-  __syncthreads();
-  return true;
-}
+// A barrier for LDS alone: loads and stores of global memory stay in flight.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory"); }
 
-template <typename Z> __global__ __launch_bounds__(NT) void k_distill_forward(DistillArgs a) {
-  __shared__ Teacher T;
-  const int64_t row = blockIdx.x;
-  const Z* z = (const Z*)a.z + row * a.ldz;
-  if (!teacher_row(a, row, T)) {
-    if (threadIdx.x == 0) {
-      if (a.loss) a.loss[row] = 0.f;
-      a.stats[row] = make_float2(0.f, 0.f);
-    }
-    return;
-  }
-  float m = -__builtin_inff();
-  for (int j = threadIdx.x; j < a.vocab; j += NT) m = max_nan(m, to_f(z[j]));
-  m = block_max<NT>(m, T.red);
-  float s = 0.f;
-  for (int j = threadIdx.x; j < a.vocab; j += NT) s += expf((to_f(z[j]) - m) / a.temp);
-  const float ls = logf(block_sum<NT>(s, T.red));
-  float l = 0.f;
-  for (int k = threadIdx.x; k < a.k; k += NT) {
-    const float lp = T.logp[k];
-    if (lp != -__builtin_inff()) l += expf(lp) * (lp - ((to_f(z[T.idx[k]]) - m) / a.temp - ls));
-  }
-  l = block_sum<NT>(l, T.red);
-  if (threadIdx.x == 0) {
-    if (a.loss) a.loss[row] = a.temp * a.temp * l;
-    a.stats[row] = make_float2(m, ls);
-  }
-}
-
-template <typename Z> __global__ __launch_bounds__(NT) void k_distill_backward(DistillArgs a) {
-  __shared__ Teacher T;
-  const int64_t row = blockIdx.x;
-  const Z* z = (const Z*)a.z + row * a.ldz;
-  Z* dz = (Z*)a.dz + row * a.ldd;
-  const float g = a.gl ? a.gl[row] : 1.f;
-  const bool live = teacher_row(a, row, T);
-  if (!live || g == 0.f) {
-    for (int j = threadIdx.x; j < a.vocab; j += NT) dz[j] = from_f<Z>(0.f);
-    return;
-  }
-  const float2 st = a.stats[row];
-  const float gt = g * a.temp;
-  // the teacher's entries first: dz may be z itself
-  float own[kDistillMaxK / NT];
+// sum of exponentials s relative to the reference m, joined over a wave
+__device__ __forceinline__ float safe_ref(float m) { return m == NEG ? 0.f : m; }
+__device__ __forceinline__ void wave_join(float& m, float& s, float c) {
 #pragma unroll
-  for (int i = 0; i < kDistillMaxK / NT; ++i) {
-    const int k = threadIdx.x + i * NT;
-    if (k < a.k && T.idx[k] >= 0) {
-      float p = 0.f;
+  for (int o = 32; o > 0; o >>= 1) {
+    const float m2 = __shfl_xor(m, o, 64), s2 = __shfl_xor(s, o, 64);
+    const float mm = fmaxf(m, m2), r = safe_ref(mm);
+    s = s * exp2_fast((m - r) * c) + s2 * exp2_fast((m2 - r) * c);
+    m = mm;
+  }
+}
+
+// What the block knows of one row's teacher, in LDS.
+template <int NT> struct Teacher {
+  static constexpr int W = NT / 64, KPT = kDistillMaxK / NT;   // entries a thread holds
+  int idx[kDistillMaxK];     // -1 where absent
+  float e[kDistillMaxK];     // exp((t - top) / T), 0 where absent
+  float fix[kDistillMaxK];   // the gradient at the entry
+  float wm[W], ws[W], wt[W], wl[W], we[W];
+  int live[W];
+};
+
+template <int NT> struct Entries {   // a thread's entries k = tid + i NT of a row
+  static constexpr int KPT = kDistillMaxK / NT;
+  float t[KPT];
+  int idx[KPT];
+  __device__ __forceinline__ void load(const DistillArgs& a, int64_t row) {
+#pragma unroll
+    for (int i = 0; i < KPT; ++i) {
+      const int k = threadIdx.x + i * NT;
+      t[i] = NEG;
+      idx[i] = -1;
+      if (i * NT < a.k && k < a.k) {
+        const int64_t at = row * a.k + k;
+        const int64_t j = a.idx64 ? ((const int64_t*)a.idx)[at] : (int64_t)((const int32_t*)a.idx)[at];
+        const float v = load_fmt(a.t, at, a.t_fmt);
+        if (j >= 0 && j < a.vocab && v != NEG) {
+          t[i] = v;
+          idx[i] = (int)j;
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ bool any() const {
+    bool r = false;
+#pragma unroll
+    for (int i = 0; i < KPT; ++i) r |= idx[i] >= 0;
+    return r;
+  }
+};
+
+template <typename Z, int NT> struct Row {
+  static constexpr int W = NT / 64, KPT = kDistillMaxK / NT;
+  float m, s;        // the row's statistics
+  float lp[KPT];     // log p of the thread's entries (NEG where p is 0)
+  float zi[KPT];     // the student's logit there
+
+  // Joins the threads' (m, s) (when FWD) and forms the teacher's distribution:
+  // E.idx and .e of T are filled.  Two LDS barriers.
+  template <bool FWD>
+  __device__ __forceinline__ void join(const DistillArgs& a, const Entries<NT>& E, Teacher<NT>& T, float c) {
+    const int tid = threadIdx.x, wave = tid >> 6;
+    float top = NEG;
+#pragma unroll
+    for (int i = 0; i < KPT; ++i) {
+      if (i * NT < a.k && E.idx[i] >= 0) top = max_nan(top, E.t[i]);
+    }
+    top = wave_max(top);
+    if (FWD) wave_join(m, s, c);
+    if ((tid & 63) == 0) {
+      T.wt[wave] = top;
+      T.wm[wave] = m;
+      T.ws[wave] = s;
+    }
+    lds_barrier();
+    top = T.wt[0];
+#pragma unroll
+    for (int w = 1; w < W; ++w) top = max_nan(top, T.wt[w]);
+    if (FWD) {
+      m = T.wm[0];
+#pragma unroll
+      for (int w = 1; w < W; ++w) m = fmaxf(m, T.wm[w]);
+      const float r = safe_ref(m);
+      s = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) s += T.ws[w] * exp2_fast((T.wm[w] - r) * c);
+    }
+    float es = 0.f;
+    const float it = 1.f / a.temp;
+#pragma unroll
+    for (int i = 0; i < KPT; ++i) {
+      if (i * NT < a.k) {
+        lp[i] = E.idx[i] >= 0 ? (E.t[i] - top) * it : NEG;
+        const float e = expf(lp[i]);
+        es += e;
+        const int k = tid + i * NT;
+        T.idx[k] = E.idx[i];
+        T.e[k] = e;
+      }
+    }
+    es = wave_sum(es);
+    if ((tid & 63) == 0) T.we[wave] = es;
+    lds_barrier();
+    es = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) es += T.we[w];
+    const float ls = logf(es);
+#pragma unroll
+    for (int i = 0; i < KPT; ++i)
+      if (i * NT < a.k) lp[i] = expf(lp[i] - ls) == 0.f ? NEG : lp[i] - ls;
+    inv_es = 1.f / es;
+  }
+  float inv_es;
+
+  // this thread's share of the loss
+  __device__ __forceinline__ float loss(const DistillArgs& a, float c) const {
+    const float ls = logf(s);
+    float l = 0.f;
+#pragma unroll
+    for (int i = 0; i < KPT; ++i)
+      if (i * NT < a.k && lp[i] != NEG) l += expf(lp[i]) * (lp[i] - ((zi[i] - m) * c * LN2 - ls));
+    return l;
+  }
+
+  // the gradient at the thread's entries, into T.fix (entries in [lo, hi))
+  __device__ __forceinline__ void fix(const DistillArgs& a, const Entries<NT>& E, Teacher<NT>& T, float c, float gt) const {
+#pragma unroll
+    for (int i = 0; i < KPT; ++i) {
+      if (i * NT >= a.k || E.idx[i] < 0) continue;
+      float p = 0.f;   // every entry with this index
       for (int o = 0; o < a.k; ++o)
-        if (T.idx[o] == T.idx[k]) p += expf(T.logp[o]);
-      own[i] = gt * (expf((to_f(z[T.idx[k]]) - st.x) / a.temp - st.y) - p);
+        if (T.idx[o] == E.idx[i]) p += T.e[o];
+      T.fix[threadIdx.x + i * NT] = gt * (exp2_fast((zi[i] - m) * c) / s - p * inv_es);
     }
   }
-  __syncthreads();
-  for (int j = threadIdx.x; j < a.vocab; j += NT)
-    dz[j] = from_f<Z>(gt * expf((to_f(z[j]) - st.x) / a.temp - st.y));
-  __syncthreads();
+
+  __device__ __forceinline__ void gather(const DistillArgs& a, const Entries<NT>& E, const Z* z) {
 #pragma unroll
-  for (int i = 0; i < kDistillMaxK / NT; ++i) {
-    const int k = threadIdx.x + i * NT;
-    if (k < a.k && T.idx[k] >= 0) dz[T.idx[k]] = from_f<Z>(own[i]);
+    for (int i = 0; i < KPT; ++i) zi[i] = i * NT < a.k && E.idx[i] >= 0 ? to_f(z[E.idx[i]]) : 0.f;
+  }
+};
+
+// The entries whose element this wave wrote in its pass over the row: a wave's
+// stores to one address keep their order, so no wait is needed between.
+// Element j belongs to the wave of thread (j / N) % NT.
+template <typename Z, int NT>
+__device__ __forceinline__ void write_fixes(const DistillArgs& a, const Teacher<NT>& T, Z* dz, int lo, int hi) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int k = lane; k < a.k; k += 64) {
+    const int j = T.idx[k];
+    if (j >= lo && j < hi && (((j - lo) / Chunk<Z>::N) % NT) >> 6 == wave) dz[j] = from_f<Z>(T.fix[k]);
+  }
+}
+
+// Loss and statistics (FWD), gradient (BWD), or both with the row read a
+// second time while it is still in the caches.  One block a row; backward
+// alone may share a row between gridDim.y blocks.
+template <typename Z, int NT, bool FWD, bool BWD>
+__global__ __launch_bounds__(NT) void k_distill_rows(DistillArgs a) {
+  typedef Chunk<Z> C;
+  __shared__ Teacher<NT> T;
+  const float c = LOG2E / a.temp;
+  const int tid = threadIdx.x, wave = tid >> 6;
+  // this block's columns: whole chunks of all threads
+  const int per = (int)(((int64_t)a.vocab + gridDim.y - 1) / gridDim.y + NT * C::N - 1) / (NT * C::N) * (NT * C::N);
+  const int lo = min(a.vocab, (int)blockIdx.y * per), hi = min(a.vocab, lo + per);
+  if (lo >= hi) return;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const Z* z = (const Z*)a.z + row * a.ldz;
+    Z* dz = BWD ? (Z*)a.dz + row * a.ldd : nullptr;
+    Entries<NT> E;
+    E.load(a, row);
+    if (row != blockIdx.x) lds_barrier();   // T is free
+    const bool mine = __any(E.any());
+    if ((tid & 63) == 0) T.live[wave] = mine;
+    lds_barrier();
+    bool live = false;
+#pragma unroll
+    for (int w = 0; w < NT / 64; ++w) live |= T.live[w] != 0;
+    const float g = BWD && a.gl ? a.gl[row] : 1.f;
+    if (FWD && !live && tid == 0) {
+      if (a.loss) a.loss[row] = 0.f;
+      if (a.stats) a.stats[row] = make_float2(0.f, 1.f);
+    }
+    if (!live || (!FWD && g == 0.f)) {
+      if (BWD) {
+        const float zero[C::N] = {};
+        for (int j = lo + tid * C::N; j < hi; j += NT * C::N) C::store(dz, j, hi, zero);
+      }
+      continue;
+    }
+    Row<Z, NT> R;
+    R.gather(a, E, z);
+    if (FWD) {
+      // running largest value and sum, one rescaling for each 16 bytes
+      float m = NEG, s = 0.f;
+#pragma unroll 4
+      for (int j = tid * C::N; j < a.vocab; j += NT * C::N) {
+        float f[C::N];
+        C::unpack(C::load(z, j, a.vocab), f);
+        float cm = f[0];
+#pragma unroll
+        for (int i = 1; i < C::N; ++i) cm = fmaxf(cm, f[i]);
+        if (cm > m) {
+          s *= exp2_fast((m - cm) * c);
+          m = cm;
+        }
+        const float r = safe_ref(m);
+#pragma unroll
+        for (int i = 0; i < C::N; ++i) s += exp2_fast((f[i] - r) * c);
+      }
+      R.m = m;
+      R.s = s;
+    } else {
+      const float2 st = a.stats[row];
+      R.m = st.x;
+      R.s = st.y;
+    }
+    R.template join<FWD>(a, E, T, c);
+    const float gt = g * a.temp;
+    if (BWD) R.fix(a, E, T, c, gt);
+    if (FWD) {
+      const float l = wave_sum(R.loss(a, c));
+      if ((tid & 63) == 0) T.wl[wave] = l;
+    }
+    lds_barrier();
+    if (FWD && tid == 0) {
+      float l = 0.f;
+#pragma unroll
+      for (int w = 0; w < NT / 64; ++w) l += T.wl[w];
+      if (a.loss) a.loss[row] = a.temp * a.temp * l;
+      if (a.stats) a.stats[row] = make_float2(R.m, R.s);
+    }
+    if (BWD) {
+      const float k = g == 0.f ? 0.f : gt / R.s;
+      const bool zero = g == 0.f;
+#pragma unroll 4
+      for (int j = lo + tid * C::N; j < hi; j += NT * C::N) {
+        float f[C::N];
+        C::unpack(C::load(z, j, hi), f);
+#pragma unroll
+        for (int i = 0; i < C::N; ++i) f[i] = zero ? 0.f : exp2_fast((f[i] - R.m) * c) * k;
+        C::store(dz, j, hi, f);
+      }
+      if (!zero) write_fixes<Z, NT>(a, T, dz, lo, hi);
+    }
   }
 }
 
 }  // namespace
 
-void launch_distill_forward(int fmt, const DistillArgs& a, hipStream_t s) {
-  const dim3 g((unsigned)a.rows), b(NT);
-  if (fmt == 1) hipLaunchKernelGGL((k_distill_forward<float>), g, b, 0, s, a);
-  else if (fmt == 0) hipLaunchKernelGGL((k_distill_forward<bf16_t>), g, b, 0, s, a);
-  else hipLaunchKernelGGL((k_distill_forward<fp16_t>), g, b, 0, s, a);
+template <typename Z, bool FWD, bool BWD>
+static void launch_rows(const DistillArgs& a, hipStream_t s) {
+  constexpr int NT = 1024;
+  const unsigned rows = (unsigned)(a.rows < (1 << 20) ? a.rows : (1 << 20));
+  hipLaunchKernelGGL((k_distill_rows<Z, NT, FWD, BWD>), dim3(rows), dim3(NT), 0, s, a);
 }
 
-void launch_distill_backward(int fmt, const DistillArgs& a, hipStream_t s) {
-  const dim3 g((unsigned)a.rows), b(NT);
-  if (fmt == 1) hipLaunchKernelGGL((k_distill_backward<float>), g, b, 0, s, a);
-  else if (fmt == 0) hipLaunchKernelGGL((k_distill_backward<bf16_t>), g, b, 0, s, a);
-  else hipLaunchKernelGGL((k_distill_backward<fp16_t>), g, b, 0, s, a);
+template <bool FWD, bool BWD>
+static void launch_fmt(int fmt, const DistillArgs& a, hipStream_t s) {
+  if (fmt == 1) launch_rows<float, FWD, BWD>(a, s);
+  else if (fmt == 0) launch_rows<bf16_t, FWD, BWD>(a, s);
+  else launch_rows<fp16_t, FWD, BWD>(a, s);
 }
+
+void launch_distill_forward(int fmt, const DistillArgs& a, hipStream_t s) { launch_fmt<true, false>(fmt, a, s); }
+void launch_distill_backward(int fmt, const DistillArgs& a, hipStream_t s) { launch_fmt<false, true>(fmt, a, s); }
+void launch_distill_step(int fmt, const DistillArgs& a, hipStream_t s) { launch_fmt<true, true>(fmt, a, s); }
 
 }  // namespace dion

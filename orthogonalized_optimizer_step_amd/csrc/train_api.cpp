@@ -373,10 +373,8 @@ int dion_distill_topk_step(const void* logits, int64_t ldz, const void* teacher,
     if (c.code != DION_OK || rows == 0) return c.done();
     const hipStream_t st = (hipStream_t)stream;
     return run_phase("distill_topk_step", "dion::k_distill_step", 8.0 * rows * vocab,
-                     distill_bytes(a, c.es, idx_bytes, true), st, [&]() {
-                       launch_distill_forward(dtype, a, st);
-                       launch_distill_backward(dtype, a, st);
-                     });
+                     distill_bytes(a, c.es, idx_bytes, true), st,
+                     [&]() { launch_distill_step(dtype, a, st); });
   });
 }
 

@@ -67,7 +67,7 @@ struct DistillArgs {
   const void* idx;        // rows x k their indices (32 or 64 bits)
   const float* gl;        // rows: gradient of each row's loss (NULL: 1)
   float* loss;            // rows
-  float2* stats;          // rows: (largest logit, log of the sum of exponentials)
+  float2* stats;          // rows: (largest logit m, sum of exp((z - m) / T)); NULL: not kept
   void* dz;               // rows x vocab
   int64_t ldz, ldd;
   int64_t rows;
@@ -91,5 +91,6 @@ size_t int8_linear_scratch(int64_t m, int64_t n, int k);
 void launch_int8_linear(const Int8Args& a, hipStream_t s);
 void launch_distill_forward(int fmt, const DistillArgs& a, hipStream_t s);
 void launch_distill_backward(int fmt, const DistillArgs& a, hipStream_t s);
+void launch_distill_step(int fmt, const DistillArgs& a, hipStream_t s);
 
 }  // namespace dion
