@@ -314,6 +314,121 @@ __global__ __launch_bounds__(NT) void k_distill_rows(DistillArgs a) {
   }
 }
 
+// Loss and gradient with the row held in registers: up to NC whole 16-byte
+// chunks a thread (chunk i of thread t at element (i NT + t) N) and one more
+// for the rest of the row, -inf past its end.  A block walks rows
+// gridDim.x apart.  As it writes a chunk of one row's gradient it asks for the
+// same chunk of its next row, so that memory is busy through the arithmetic
+// and each logit is read once; the teacher's entries of the next row are
+// fetched a row ahead too, and a row without any is not read at all.
+template <typename Z, int NT, int NC, int BLOCKS>
+__global__ __launch_bounds__(NT, NT * BLOCKS / 256) void k_distill_step(DistillArgs a) {
+  typedef Chunk<Z> C;
+  constexpr int W = NT / 64, STEP = NT * C::N;
+  __shared__ Teacher<NT> T;
+  const float c = LOG2E / a.temp;
+  const int tid = threadIdx.x, wave = tid >> 6, j0 = tid * C::N;
+  const int whole = a.vocab / STEP, jt = whole * STEP + j0;   // chunks that every thread has; its place in the rest
+  uintx4 data[NC], tail;
+  auto each = [&](auto&& f) {   // f on the N values of every whole chunk and of the rest
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+      if (i < whole) {
+        asm volatile("" : "+v"(data[i]));   // unpacked anew in each pass: held in 32 bits they would not fit
+        float v[C::N];
+        C::unpack(data[i], v);
+        f(v, i);
+      }
+    if (jt < a.vocab) {
+      float v[C::N];
+      C::unpack(tail, v);
+      f(v, NC);
+    }
+  };
+  auto fetch = [&](const Z* z, int i) {
+    if (i < NC) data[i] = *(const uintx4u*)(z + i * STEP + j0);
+    else tail = C::load(z, jt, a.vocab);
+  };
+  auto vote = [&](bool mine) {   // whether any thread says so, after the next barrier
+    const bool r = __any(mine);
+    if ((tid & 63) == 0) T.live[wave] = r;
+  };
+  auto any = [&]() {
+    bool r = false;
+#pragma unroll
+    for (int w = 0; w < W; ++w) r |= T.live[w] != 0;
+    return r;
+  };
+  Entries<NT> E, En;
+  int64_t row = blockIdx.x;
+  E.load(a, row);
+  vote(E.any());
+  lds_barrier();
+  bool live = any();
+  if (live) {
+    const Z* z = (const Z*)a.z + row * a.ldz;
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+      if (i < whole) fetch(z, i);
+    if (jt < a.vocab) fetch(z, NC);
+  }
+  for (; row < a.rows; row += gridDim.x) {
+    const Z* z = (const Z*)a.z + row * a.ldz;
+    Z* dz = (Z*)a.dz + row * a.ldd;
+    const int64_t next = row + gridDim.x;
+    const bool more = next < a.rows;
+    if (more) En.load(a, next);
+    const float g = a.gl ? a.gl[row] : 1.f;
+    Row<Z, NT> R;
+    float k = 0.f;
+    bool zero = true;
+    lds_barrier();   // T is free
+    if (live) {
+      R.gather(a, E, z);
+      float m = NEG, s = 0.f;
+      each([&](const float* v, int) {
+#pragma unroll
+        for (int e = 0; e < C::N; ++e) m = fmaxf(m, v[e]);
+      });
+      const float r = safe_ref(m);
+      each([&](const float* v, int) {
+#pragma unroll
+        for (int e = 0; e < C::N; ++e) s += exp2_fast((v[e] - r) * c);
+      });
+      R.m = m;
+      R.s = s;
+      R.template join<true>(a, E, T, c);
+      R.fix(a, E, T, c, g * a.temp);
+      const float l = wave_sum(R.loss(a, c));
+      if ((tid & 63) == 0) T.wl[wave] = l;
+      k = g * a.temp / R.s;
+      zero = g == 0.f;
+    }
+    vote(more && En.any());
+    lds_barrier();
+    const bool live_next = more && any();
+    if (tid == 0) {
+      float l = 0.f;
+      if (live) {
+#pragma unroll
+        for (int w = 0; w < W; ++w) l += T.wl[w];
+      }
+      a.loss[row] = a.temp * a.temp * l;
+    }
+    const Z* zn = (const Z*)a.z + next * a.ldz;
+    each([&](float* v, int i) {
+#pragma unroll
+      for (int e = 0; e < C::N; ++e) v[e] = zero ? 0.f : exp2_fast((v[e] - R.m) * c) * k;
+      if (i < NC) *(uintx4u*)(dz + i * STEP + j0) = C::pack(v);
+      else C::store(dz, jt, a.vocab, v);
+      if (live_next) fetch(zn, i);
+    });
+    if (!zero) write_fixes<Z, NT>(a, T, dz, 0, a.vocab);
+    E = En;
+    live = live_next;
+  }
+}
+
 }  // namespace
 
 template <typename Z, bool FWD, bool BWD>
@@ -332,6 +447,27 @@ static void launch_fmt(int fmt, const DistillArgs& a, hipStream_t s) {
 
 void launch_distill_forward(int fmt, const DistillArgs& a, hipStream_t s) { launch_fmt<true, false>(fmt, a, s); }
 void launch_distill_backward(int fmt, const DistillArgs& a, hipStream_t s) { launch_fmt<false, true>(fmt, a, s); }
-void launch_distill_step(int fmt, const DistillArgs& a, hipStream_t s) { launch_fmt<true, true>(fmt, a, s); }
+
+template <typename Z, int NT, int NC, int BLOCKS>
+static void launch_held(const DistillArgs& a, hipStream_t s) {
+  const int64_t most = 256 * BLOCKS;   // as many blocks as the CUs hold at once
+  hipLaunchKernelGGL((k_distill_step<Z, NT, NC, BLOCKS>), dim3((unsigned)(a.rows < most ? a.rows : most)), dim3(NT), 0, s, a);
+}
+
+template <typename Z>
+static void launch_step(const DistillArgs& a, hipStream_t s) {
+  constexpr int N = Chunk<Z>::N;
+  if (a.vocab < 256 * 9 * N) launch_held<Z, 256, 8, 4>(a, s);
+  else if (a.vocab < 512 * 9 * N) launch_held<Z, 512, 8, 2>(a, s);
+  else if (a.vocab < 512 * 17 * N) launch_held<Z, 512, 16, 2>(a, s);
+  else if (a.vocab < 1024 * 17 * N) launch_held<Z, 1024, 16, 1>(a, s);
+  else launch_rows<Z, true, true>(a, s);
+}
+
+void launch_distill_step(int fmt, const DistillArgs& a, hipStream_t s) {
+  if (fmt == 1) launch_step<float>(a, s);
+  else if (fmt == 0) launch_step<bf16_t>(a, s);
+  else launch_step<fp16_t>(a, s);
+}
 
 }  // namespace dion
