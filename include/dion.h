@@ -455,7 +455,7 @@ int dion_int8_linear(const int8_t* a, int64_t lda, const float* a_scale, const i
  * the gradient of a row whose grad_loss is 0.  k = 0 .. 1024.
  *   loss       rows floats
  *   stats      rows x 2 floats (8-byte aligned) that the backward call reads:
- *              the largest z and sum exp((z - largest) / T)
+ *              a reference m near the largest z, and sum exp((z - m) / T)
  *   grad_loss  rows floats: the gradient that reaches each row's loss; NULL = 1
  *   dlogits    rows x vocab of `dtype`; may be the logits in place
  * dion_distill_topk_step computes the loss and the gradient in one call, for

@@ -10,9 +10,11 @@
 // A row with no present entry has loss 0 and gradient 0, whatever z holds; a
 // row whose loss has gradient gl = 0 has gradient 0.
 //
-// Exponents are formed as (z - m) (log2(e) / T), subtraction first: exact
-// enough for the whole range of the types (z - m is 0 for the largest however
-// low the mask value that it may be), and one v_exp_f32 each.
+// With c = log2(e) / T an exponential is 2^(z c - R), R = fl(m c), one fma and
+// one v_exp_f32: m need only be near the largest logit, and the rounding of R
+// is the same in every term and cancels in q and in the loss.  Where |m c|
+// reaches 2^20 (a row whose largest is a mask's value) that rounding would
+// not stay small, and 2^((z - m) c) is formed instead.
 #include "train_device.h"
 #include "train_internal.h"
 
@@ -41,6 +43,8 @@ template <typename Z> struct Chunk {
     for (int i = 0; i < N; ++i) c.z[i] = from_f<Z>(f[i]);
     return c.u;
   }
+  // m, or the largest of the values where that is more
+  static __device__ __forceinline__ float largest(float m, const uintx4& v);
   // elements [j, j + N) of a row of n, -inf past its end
   static __device__ __forceinline__ uintx4 load(const Z* row, int j, int n) {
     if (j + N <= n) return *(const uintx4u*)(row + j);
@@ -65,16 +69,58 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 // A barrier for LDS alone: loads and stores of global memory stay in flight.
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory"); }
 
-// sum of exponentials s relative to the reference m, joined over a wave
-__device__ __forceinline__ float safe_ref(float m) { return m == NEG ? 0.f : m; }
-__device__ __forceinline__ void wave_join(float& m, float& s, float c) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    const float m2 = __shfl_xor(m, o, 64), s2 = __shfl_xor(s, o, 64);
-    const float mm = fmaxf(m, m2), r = safe_ref(mm);
-    s = s * exp2_fast((m - r) * c) + s2 * exp2_fast((m2 - r) * c);
-    m = mm;
+__device__ __forceinline__ float max3(float a, float b, float c) {   // drops NaN, which the sums keep
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+
+// Exponentials relative to the reference m.
+struct Ref {
+  float m, c, R;
+  bool wide, none;   // none: of nothing but -inf (a sum of 0)
+  __device__ __forceinline__ Ref(float m_, float c_) : m(m_ == NEG ? 0.f : m_), c(c_), none(m_ == NEG) {
+    R = m * c;
+    wide = !(fabsf(R) < 0x1p20f);
   }
+  __device__ __forceinline__ float far(float z) const { return exp2_fast((z - m) * c); }   // any m
+  __device__ __forceinline__ float near(float z) const { return exp2_fast(fmaf(z, c, -R)); }   // !wide
+  __device__ __forceinline__ float operator()(float z) const { return wide ? far(z) : near(z); }
+  // log of the same
+  __device__ __forceinline__ float log(float z) const { return (wide ? (z - m) * c : fmaf(z, c, -R)) * LN2; }
+  // what a sum relative to `o` is worth here
+  __device__ __forceinline__ float of(const Ref& o) const {
+    return o.none ? 0.f : exp2_fast(wide ? (o.m - m) * c : o.R - R);
+  }
+};
+
+template <typename Z> __device__ __forceinline__ float Chunk<Z>::largest(float m, const uintx4& v) {
+  float f[N];
+  unpack(v, f);
+#pragma unroll
+  for (int i = 0; i < N; i += 2) m = max3(m, f[i], f[i + 1]);
+  return m;
+}
+
+// Joins sums s relative to references m over a wave.
+__device__ __forceinline__ void wave_join(float& m, float& s, float c) {
+  float mm = m;
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor(mm, o, 64));
+  s = wave_sum(s * Ref(mm, c).of(Ref(m, c)));
+  m = mm;
+}
+
+// Joins the W values that the waves of a block left in LDS, the same in every lane.
+template <int W> __device__ __forceinline__ float join_sum(float v) {
+#pragma unroll
+  for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+template <int W> __device__ __forceinline__ float join_max(float v) {
+#pragma unroll
+  for (int o = W / 2; o > 0; o >>= 1) v = max_nan(v, __shfl_xor(v, o, 64));
+  return v;
 }
 
 // What the block knows of one row's teacher, in LDS.
@@ -140,17 +186,11 @@ template <typename Z, int NT> struct Row {
       T.ws[wave] = s;
     }
     lds_barrier();
-    top = T.wt[0];
-#pragma unroll
-    for (int w = 1; w < W; ++w) top = max_nan(top, T.wt[w]);
+    top = join_max<W>(T.wt[tid % W]);
     if (FWD) {
-      m = T.wm[0];
-#pragma unroll
-      for (int w = 1; w < W; ++w) m = fmaxf(m, T.wm[w]);
-      const float r = safe_ref(m);
-      s = 0.f;
-#pragma unroll
-      for (int w = 0; w < W; ++w) s += T.ws[w] * exp2_fast((T.wm[w] - r) * c);
+      const float wm = T.wm[tid % W];
+      m = join_max<W>(wm);
+      s = join_sum<W>(T.ws[tid % W] * Ref(m, c).of(Ref(wm, c)));
     }
     float es = 0.f;
     const float it = 1.f / a.temp;
@@ -168,9 +208,7 @@ template <typename Z, int NT> struct Row {
     es = wave_sum(es);
     if ((tid & 63) == 0) T.we[wave] = es;
     lds_barrier();
-    es = 0.f;
-#pragma unroll
-    for (int w = 0; w < W; ++w) es += T.we[w];
+    es = join_sum<W>(T.we[tid % W]);
     const float ls = logf(es);
 #pragma unroll
     for (int i = 0; i < KPT; ++i)
@@ -181,23 +219,25 @@ template <typename Z, int NT> struct Row {
 
   // this thread's share of the loss
   __device__ __forceinline__ float loss(const DistillArgs& a, float c) const {
+    const Ref r(m, c);
     const float ls = logf(s);
     float l = 0.f;
 #pragma unroll
     for (int i = 0; i < KPT; ++i)
-      if (i * NT < a.k && lp[i] != NEG) l += expf(lp[i]) * (lp[i] - ((zi[i] - m) * c * LN2 - ls));
+      if (i * NT < a.k && lp[i] != NEG) l += expf(lp[i]) * (lp[i] - (r.log(zi[i]) - ls));
     return l;
   }
 
   // the gradient at the thread's entries, into T.fix (entries in [lo, hi))
   __device__ __forceinline__ void fix(const DistillArgs& a, const Entries<NT>& E, Teacher<NT>& T, float c, float gt) const {
+    const Ref r(m, c);
 #pragma unroll
     for (int i = 0; i < KPT; ++i) {
       if (i * NT >= a.k || E.idx[i] < 0) continue;
       float p = 0.f;   // every entry with this index
       for (int o = 0; o < a.k; ++o)
         if (T.idx[o] == E.idx[i]) p += T.e[o];
-      T.fix[threadIdx.x + i * NT] = gt * (exp2_fast((zi[i] - m) * c) / s - p * inv_es);
+      T.fix[threadIdx.x + i * NT] = gt * (r(zi[i]) / s - p * inv_es);
     }
   }
 
@@ -241,9 +281,7 @@ __global__ __launch_bounds__(NT) void k_distill_rows(DistillArgs a) {
     const bool mine = __any(E.any());
     if ((tid & 63) == 0) T.live[wave] = mine;
     lds_barrier();
-    bool live = false;
-#pragma unroll
-    for (int w = 0; w < NT / 64; ++w) live |= T.live[w] != 0;
+    const bool live = __any(T.live[tid % (NT / 64)]);
     const float g = BWD && a.gl ? a.gl[row] : 1.f;
     if (FWD && !live && tid == 0) {
       if (a.loss) a.loss[row] = 0.f;
@@ -263,18 +301,17 @@ __global__ __launch_bounds__(NT) void k_distill_rows(DistillArgs a) {
       float m = NEG, s = 0.f;
 #pragma unroll 4
       for (int j = tid * C::N; j < a.vocab; j += NT * C::N) {
+        const uintx4 v = C::load(z, j, a.vocab);
         float f[C::N];
-        C::unpack(C::load(z, j, a.vocab), f);
-        float cm = f[0];
-#pragma unroll
-        for (int i = 1; i < C::N; ++i) cm = fmaxf(cm, f[i]);
+        C::unpack(v, f);
+        const float cm = C::largest(m, v);
         if (cm > m) {
-          s *= exp2_fast((m - cm) * c);
+          s *= Ref(cm, c).of(Ref(m, c));
           m = cm;
         }
-        const float r = safe_ref(m);
+        const Ref r(m, c);
 #pragma unroll
-        for (int i = 0; i < C::N; ++i) s += exp2_fast((f[i] - r) * c);
+        for (int i = 0; i < C::N; ++i) s += r(f[i]);
       }
       R.m = m;
       R.s = s;
@@ -287,26 +324,25 @@ __global__ __launch_bounds__(NT) void k_distill_rows(DistillArgs a) {
     const float gt = g * a.temp;
     if (BWD) R.fix(a, E, T, c, gt);
     if (FWD) {
-      const float l = wave_sum(R.loss(a, c));
-      if ((tid & 63) == 0) T.wl[wave] = l;
+      const float part = wave_sum(R.loss(a, c));
+      if ((tid & 63) == 0) T.wl[wave] = part;
     }
     lds_barrier();
+    const float l = FWD ? join_sum<NT / 64>(T.wl[tid % (NT / 64)]) : 0.f;
     if (FWD && tid == 0) {
-      float l = 0.f;
-#pragma unroll
-      for (int w = 0; w < NT / 64; ++w) l += T.wl[w];
       if (a.loss) a.loss[row] = a.temp * a.temp * l;
       if (a.stats) a.stats[row] = make_float2(R.m, R.s);
     }
     if (BWD) {
-      const float k = g == 0.f ? 0.f : gt / R.s;
+      const float k = gt / R.s;
       const bool zero = g == 0.f;
+      const Ref r(R.m, c);
 #pragma unroll 4
       for (int j = lo + tid * C::N; j < hi; j += NT * C::N) {
         float f[C::N];
         C::unpack(C::load(z, j, hi), f);
 #pragma unroll
-        for (int i = 0; i < C::N; ++i) f[i] = zero ? 0.f : exp2_fast((f[i] - R.m) * c) * k;
+        for (int i = 0; i < C::N; ++i) f[i] = zero ? 0.f : r(f[i]) * k;
         C::store(dz, j, hi, f);
       }
       if (!zero) write_fixes<Z, NT>(a, T, dz, lo, hi);
@@ -349,29 +385,24 @@ __global__ __launch_bounds__(NT, NT * BLOCKS / 256) void k_distill_step(DistillA
     if (i < NC) data[i] = *(const uintx4u*)(z + i * STEP + j0);
     else tail = C::load(z, jt, a.vocab);
   };
+  auto read = [&](const Z* z) {
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+      if (i < whole) fetch(z, i);
+    if (jt < a.vocab) fetch(z, NC);
+  };
   auto vote = [&](bool mine) {   // whether any thread says so, after the next barrier
     const bool r = __any(mine);
     if ((tid & 63) == 0) T.live[wave] = r;
   };
-  auto any = [&]() {
-    bool r = false;
-#pragma unroll
-    for (int w = 0; w < W; ++w) r |= T.live[w] != 0;
-    return r;
-  };
+  auto any = [&]() { return __any(T.live[tid % W]) != 0; };
   Entries<NT> E, En;
   int64_t row = blockIdx.x;
   E.load(a, row);
   vote(E.any());
   lds_barrier();
   bool live = any();
-  if (live) {
-    const Z* z = (const Z*)a.z + row * a.ldz;
-#pragma unroll
-    for (int i = 0; i < NC; ++i)
-      if (i < whole) fetch(z, i);
-    if (jt < a.vocab) fetch(z, NC);
-  }
+  read((const Z*)a.z + row * a.ldz);
   for (; row < a.rows; row += gridDim.x) {
     const Z* z = (const Z*)a.z + row * a.ldz;
     Z* dz = (Z*)a.dz + row * a.ldd;
@@ -380,6 +411,7 @@ __global__ __launch_bounds__(NT, NT * BLOCKS / 256) void k_distill_step(DistillA
     if (more) En.load(a, next);
     const float g = a.gl ? a.gl[row] : 1.f;
     Row<Z, NT> R;
+    R.m = R.s = 0.f;
     float k = 0.f;
     bool zero = true;
     lds_barrier();   // T is free
@@ -388,40 +420,56 @@ __global__ __launch_bounds__(NT, NT * BLOCKS / 256) void k_distill_step(DistillA
       float m = NEG, s = 0.f;
       each([&](const float* v, int) {
 #pragma unroll
-        for (int e = 0; e < C::N; ++e) m = fmaxf(m, v[e]);
+        for (int e = 0; e < C::N; e += 2) m = max3(m, v[e], v[e + 1]);
       });
-      const float r = safe_ref(m);
+      const Ref r(m, c);
       each([&](const float* v, int) {
 #pragma unroll
-        for (int e = 0; e < C::N; ++e) s += exp2_fast((v[e] - r) * c);
+        for (int e = 0; e < C::N; ++e) s += r.near(v[e]);
       });
+      if (__any(r.wide)) {   // a largest of a mask's value: rare, so from memory again
+        s = 0.f;
+        for (int j = j0; j < a.vocab; j += STEP) {
+          float v[C::N];
+          C::unpack(C::load(z, j, a.vocab), v);
+#pragma unroll
+          for (int e = 0; e < C::N; ++e) s += r(v[e]);
+        }
+      }
       R.m = m;
       R.s = s;
       R.template join<true>(a, E, T, c);
       R.fix(a, E, T, c, g * a.temp);
-      const float l = wave_sum(R.loss(a, c));
-      if ((tid & 63) == 0) T.wl[wave] = l;
+      const float part = wave_sum(R.loss(a, c));
+      if ((tid & 63) == 0) T.wl[wave] = part;
       k = g * a.temp / R.s;
       zero = g == 0.f;
     }
     vote(more && En.any());
     lds_barrier();
     const bool live_next = more && any();
-    if (tid == 0) {
-      float l = 0.f;
-      if (live) {
+    const float l = live ? join_sum<W>(T.wl[tid % W]) : 0.f;
+    if (tid == 0) a.loss[row] = a.temp * a.temp * l;
+    const Z* zn = live_next ? (const Z*)a.z + next * a.ldz : z;   // without a next row the loads are for nothing
+    const Ref r(R.m, c);
+    const bool apart = zero || r.wide;
+    if (apart) {   // rare: from memory
+      for (int j = j0; j < a.vocab; j += STEP) {
+        float v[C::N] = {};
+        if (!zero) C::unpack(C::load(z, j, a.vocab), v);
 #pragma unroll
-        for (int w = 0; w < W; ++w) l += T.wl[w];
+        for (int e = 0; e < C::N; ++e) v[e] = zero ? 0.f : r.far(v[e]) * k;
+        C::store(dz, j, a.vocab, v);
       }
-      a.loss[row] = a.temp * a.temp * l;
     }
-    const Z* zn = (const Z*)a.z + next * a.ldz;
     each([&](float* v, int i) {
 #pragma unroll
-      for (int e = 0; e < C::N; ++e) v[e] = zero ? 0.f : exp2_fast((v[e] - R.m) * c) * k;
-      if (i < NC) *(uintx4u*)(dz + i * STEP + j0) = C::pack(v);
-      else C::store(dz, jt, a.vocab, v);
-      if (live_next) fetch(zn, i);
+      for (int e = 0; e < C::N; ++e) v[e] = r.near(v[e]) * k;
+      if (!apart) {
+        if (i < NC) *(uintx4u*)(dz + i * STEP + j0) = C::pack(v);
+        else C::store(dz, jt, a.vocab, v);
+      }
+      fetch(zn, i);
     });
     if (!zero) write_fixes<Z, NT>(a, T, dz, 0, a.vocab);
     E = En;

@@ -67,7 +67,7 @@ struct DistillArgs {
   const void* idx;        // rows x k their indices (32 or 64 bits)
   const float* gl;        // rows: gradient of each row's loss (NULL: 1)
   float* loss;            // rows
-  float2* stats;          // rows: (largest logit m, sum of exp((z - m) / T)); NULL: not kept
+  float2* stats;          // rows: (a reference m near the largest logit, sum of exp((z - m) / T)); NULL: not kept
   void* dz;               // rows x vocab
   int64_t ldz, ldd;
   int64_t rows;
