@@ -15,6 +15,8 @@
 // is the same in every term and cancels in q and in the loss.  Where |m c|
 // reaches 2^20 (a row whose largest is a mask's value) that rounding would
 // not stay small, and 2^((z - m) c) is formed instead.
+#include <algorithm>
+
 #include "train_device.h"
 #include "train_internal.h"
 
@@ -25,6 +27,8 @@ namespace {
 constexpr float NEG = -__builtin_inff();
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
+typedef int intx4 __attribute__((ext_vector_type(4)));
+typedef float floatx4 __attribute__((ext_vector_type(4)));
 // 16 bytes of logits at element alignment
 typedef uint32_t uintx4 __attribute__((ext_vector_type(4)));
 typedef uintx4 uintx4u __attribute__((aligned(2)));
@@ -55,7 +59,7 @@ template <typename Z> struct Chunk {
   }
   static __device__ __forceinline__ void store(Z* row, int j, int n, const float* f) {
     if (j + N <= n) {
-      *(uintx4u*)(row + j) = pack(f);
+      __builtin_nontemporal_store(pack(f), (uintx4u*)(row + j));
     } else {
 #pragma unroll
       for (int i = 0; i < N; ++i)
@@ -126,8 +130,8 @@ template <int W> __device__ __forceinline__ float join_max(float v) {
 // What the block knows of one row's teacher, in LDS.
 template <int NT> struct Teacher {
   static constexpr int W = NT / 64, KPT = kDistillMaxK / NT;   // entries a thread holds
-  int idx[kDistillMaxK];     // -1 where absent
-  float e[kDistillMaxK];     // exp((t - top) / T), 0 where absent
+  __attribute__((aligned(16))) int idx[kDistillMaxK];   // -1 where absent; up to k rounded up to the wave
+  __attribute__((aligned(16))) float e[kDistillMaxK];   // exp((t - top) / T), 0 where absent
   float fix[kDistillMaxK];   // the gradient at the entry
   float wm[W], ws[W], wt[W], wl[W], we[W];
   int live[W];
@@ -165,6 +169,10 @@ template <int NT> struct Entries {   // a thread's entries k = tid + i NT of a r
 template <typename Z, int NT> struct Row {
   static constexpr int W = NT / 64, KPT = kDistillMaxK / NT;
   float m, s;        // the row's statistics
+  // whether this wave holds any of the entries that its threads number i
+  static __device__ __forceinline__ bool has(const DistillArgs& a, int i) {
+    return i * NT + (int)(threadIdx.x & ~63u) < a.k;
+  }
   float lp[KPT];     // log p of the thread's entries (NEG where p is 0)
   float zi[KPT];     // the student's logit there
 
@@ -176,7 +184,7 @@ template <typename Z, int NT> struct Row {
     float top = NEG;
 #pragma unroll
     for (int i = 0; i < KPT; ++i) {
-      if (i * NT < a.k && E.idx[i] >= 0) top = max_nan(top, E.t[i]);
+      if (has(a, i) && E.idx[i] >= 0) top = max_nan(top, E.t[i]);
     }
     top = wave_max(top);
     if (FWD) wave_join(m, s, c);
@@ -196,7 +204,7 @@ template <typename Z, int NT> struct Row {
     const float it = 1.f / a.temp;
 #pragma unroll
     for (int i = 0; i < KPT; ++i) {
-      if (i * NT < a.k) {
+      if (has(a, i)) {
         lp[i] = E.idx[i] >= 0 ? (E.t[i] - top) * it : NEG;
         const float e = expf(lp[i]);
         es += e;
@@ -212,7 +220,7 @@ template <typename Z, int NT> struct Row {
     const float ls = logf(es);
 #pragma unroll
     for (int i = 0; i < KPT; ++i)
-      if (i * NT < a.k) lp[i] = expf(lp[i] - ls) == 0.f ? NEG : lp[i] - ls;
+      if (has(a, i)) lp[i] = expf(lp[i] - ls) == 0.f ? NEG : lp[i] - ls;
     inv_es = 1.f / es;
   }
   float inv_es;
@@ -224,7 +232,7 @@ template <typename Z, int NT> struct Row {
     float l = 0.f;
 #pragma unroll
     for (int i = 0; i < KPT; ++i)
-      if (i * NT < a.k && lp[i] != NEG) l += expf(lp[i]) * (lp[i] - (r.log(zi[i]) - ls));
+      if (has(a, i) && lp[i] != NEG) l += expf(lp[i]) * (lp[i] - (r.log(zi[i]) - ls));
     return l;
   }
 
@@ -233,17 +241,24 @@ template <typename Z, int NT> struct Row {
     const Ref r(m, c);
 #pragma unroll
     for (int i = 0; i < KPT; ++i) {
-      if (i * NT >= a.k || E.idx[i] < 0) continue;
+      if (!has(a, i)) continue;
       float p = 0.f;   // every entry with this index
-      for (int o = 0; o < a.k; ++o)
-        if (T.idx[o] == E.idx[i]) p += T.e[o];
+#pragma unroll 4
+      for (int o = 0; o < a.k; o += 4) {
+        const intx4 j = *(const intx4*)(T.idx + o);
+        const floatx4 e = *(const floatx4*)(T.e + o);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) p += j[q] == E.idx[i] ? e[q] : 0.f;
+      }
+      if (E.idx[i] < 0) continue;
       T.fix[threadIdx.x + i * NT] = gt * (r(zi[i]) / s - p * inv_es);
     }
   }
 
-  __device__ __forceinline__ void gather(const DistillArgs& a, const Entries<NT>& E, const Z* z) {
+  // the student's logits at the entries in [lo, hi)
+  __device__ __forceinline__ void gather(const DistillArgs& a, const Entries<NT>& E, const Z* z, int lo, int hi) {
 #pragma unroll
-    for (int i = 0; i < KPT; ++i) zi[i] = i * NT < a.k && E.idx[i] >= 0 ? to_f(z[E.idx[i]]) : 0.f;
+    for (int i = 0; i < KPT; ++i) zi[i] = has(a, i) && E.idx[i] >= lo && E.idx[i] < hi ? to_f(z[E.idx[i]]) : 0.f;
   }
 };
 
@@ -295,7 +310,7 @@ __global__ __launch_bounds__(NT) void k_distill_rows(DistillArgs a) {
       continue;
     }
     Row<Z, NT> R;
-    R.gather(a, E, z);
+    R.gather(a, E, z, FWD ? 0 : lo, FWD ? a.vocab : hi);
     if (FWD) {
       // running largest value and sum, one rescaling for each 16 bytes
       float m = NEG, s = 0.f;
@@ -352,57 +367,70 @@ __global__ __launch_bounds__(NT) void k_distill_rows(DistillArgs a) {
 
 // Loss and gradient with the row held in registers: up to NC whole 16-byte
 // chunks a thread (chunk i of thread t at element (i NT + t) N) and one more
-// for the rest of the row, -inf past its end.  A block walks rows
-// gridDim.x apart.  As it writes a chunk of one row's gradient it asks for the
-// same chunk of its next row, so that memory is busy through the arithmetic
-// and each logit is read once; the teacher's entries of the next row are
-// fetched a row ahead too, and a row without any is not read at all.
+// for the rest of the row, -inf past its end.  A block walks rows gridDim.x
+// apart.  As it writes chunk i of one row's gradient it asks for chunk i of
+// its next row, and takes the chunk that it asked for LAG steps before into
+// that row's largest value and sum: each logit is read once, and the
+// arithmetic of both passes runs while memory is busy.  The teacher's entries
+// and the logits at them are fetched a row ahead too, for between two rows
+// nothing else is under way.  8192 x 128256 bf16 takes 925 us (4.4 TB/s over
+// the logits read and the gradients written); a plain pass that reads and
+// writes rows in the same order takes 810, one in the order of addresses 670.
+// Reading the row twice (k_distill_rows) takes 1218.
 template <typename Z, int NT, int NC, int BLOCKS>
 __global__ __launch_bounds__(NT, NT * BLOCKS / 256) void k_distill_step(DistillArgs a) {
   typedef Chunk<Z> C;
-  constexpr int W = NT / 64, STEP = NT * C::N;
-  __shared__ Teacher<NT> T;
+  constexpr int W = NT / 64, STEP = NT * C::N, LAG = 4;
+  __shared__ Teacher<NT> both[2];   // rows in turn, so that one may be written while the last is still read
+  int turn = 0;
   const float c = LOG2E / a.temp;
   const int tid = threadIdx.x, wave = tid >> 6, j0 = tid * C::N;
   const int whole = a.vocab / STEP, jt = whole * STEP + j0;   // chunks that every thread has; its place in the rest
   uintx4 data[NC], tail;
-  auto each = [&](auto&& f) {   // f on the N values of every whole chunk and of the rest
-#pragma unroll
-    for (int i = 0; i < NC; ++i)
-      if (i < whole) {
-        asm volatile("" : "+v"(data[i]));   // unpacked anew in each pass: held in 32 bits they would not fit
-        float v[C::N];
-        C::unpack(data[i], v);
-        f(v, i);
-      }
-    if (jt < a.vocab) {
-      float v[C::N];
-      C::unpack(tail, v);
-      f(v, NC);
-    }
+  auto values = [&](uintx4& d, float* v) {   // unpacked anew in each pass: held in 32 bits they would not fit
+    asm volatile("" : "+v"(d));
+    C::unpack(d, v);
   };
   auto fetch = [&](const Z* z, int i) {
     if (i < NC) data[i] = *(const uintx4u*)(z + i * STEP + j0);
     else tail = C::load(z, jt, a.vocab);
   };
-  auto read = [&](const Z* z) {
+  // the running largest value and the sum relative to it
+  float m = NEG, s = 0.f;
+  auto absorb = [&](uintx4& d) {
+    float v[C::N];
+    values(d, v);
+    float cm = m;
+#pragma unroll
+    for (int e = 0; e < C::N; e += 2) cm = max3(cm, v[e], v[e + 1]);
+    if (cm > m) {
+      s *= Ref(cm, c).of(Ref(m, c));
+      m = cm;
+    }
+    const Ref r(m, c);
+#pragma unroll
+    for (int e = 0; e < C::N; ++e) s += r.near(v[e]);
+  };
+  Entries<NT> E, En;
+  int64_t row = blockIdx.x;
+  E.load(a, row);
+  if (__any(E.any()) && (tid & 63) == 0) both[1].live[wave] = 1;
+  else if ((tid & 63) == 0) both[1].live[wave] = 0;
+  lds_barrier();
+  bool live = __any(both[1].live[tid % W]);
+  Row<Z, NT> R, Rn;
+  {
+    const Z* z = (const Z*)a.z + row * a.ldz;
+    R.gather(a, E, z, 0, a.vocab);
 #pragma unroll
     for (int i = 0; i < NC; ++i)
       if (i < whole) fetch(z, i);
     if (jt < a.vocab) fetch(z, NC);
-  };
-  auto vote = [&](bool mine) {   // whether any thread says so, after the next barrier
-    const bool r = __any(mine);
-    if ((tid & 63) == 0) T.live[wave] = r;
-  };
-  auto any = [&]() { return __any(T.live[tid % W]) != 0; };
-  Entries<NT> E, En;
-  int64_t row = blockIdx.x;
-  E.load(a, row);
-  vote(E.any());
-  lds_barrier();
-  bool live = any();
-  read((const Z*)a.z + row * a.ldz);
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+      if (i < whole) absorb(data[i]);
+    if (jt < a.vocab) absorb(tail);
+  }
   for (; row < a.rows; row += gridDim.x) {
     const Z* z = (const Z*)a.z + row * a.ldz;
     Z* dz = (Z*)a.dz + row * a.ldd;
@@ -410,34 +438,23 @@ __global__ __launch_bounds__(NT, NT * BLOCKS / 256) void k_distill_step(DistillA
     const bool more = next < a.rows;
     if (more) En.load(a, next);
     const float g = a.gl ? a.gl[row] : 1.f;
-    Row<Z, NT> R;
-    R.m = R.s = 0.f;
+    Teacher<NT>& T = both[turn];
+    turn ^= 1;
+    R.m = m;
+    R.s = s;
     float k = 0.f;
     bool zero = true;
-    lds_barrier();   // T is free
     if (live) {
-      R.gather(a, E, z);
-      float m = NEG, s = 0.f;
-      each([&](const float* v, int) {
-#pragma unroll
-        for (int e = 0; e < C::N; e += 2) m = max3(m, v[e], v[e + 1]);
-      });
       const Ref r(m, c);
-      each([&](const float* v, int) {
-#pragma unroll
-        for (int e = 0; e < C::N; ++e) s += r.near(v[e]);
-      });
       if (__any(r.wide)) {   // a largest of a mask's value: rare, so from memory again
-        s = 0.f;
+        R.s = 0.f;
         for (int j = j0; j < a.vocab; j += STEP) {
           float v[C::N];
           C::unpack(C::load(z, j, a.vocab), v);
 #pragma unroll
-          for (int e = 0; e < C::N; ++e) s += r(v[e]);
+          for (int e = 0; e < C::N; ++e) R.s += r(v[e]);
         }
       }
-      R.m = m;
-      R.s = s;
       R.template join<true>(a, E, T, c);
       R.fix(a, E, T, c, g * a.temp);
       const float part = wave_sum(R.loss(a, c));
@@ -445,9 +462,10 @@ __global__ __launch_bounds__(NT, NT * BLOCKS / 256) void k_distill_step(DistillA
       k = g * a.temp / R.s;
       zero = g == 0.f;
     }
-    vote(more && En.any());
+    const bool some = __any(more && En.any());
+    if ((tid & 63) == 0) T.live[wave] = some;
     lds_barrier();
-    const bool live_next = more && any();
+    const bool live_next = __any(T.live[tid % W]);
     const float l = live ? join_sum<W>(T.wl[tid % W]) : 0.f;
     if (tid == 0) a.loss[row] = a.temp * a.temp * l;
     const Z* zn = live_next ? (const Z*)a.z + next * a.ldz : z;   // without a next row the loads are for nothing
@@ -462,17 +480,35 @@ __global__ __launch_bounds__(NT, NT * BLOCKS / 256) void k_distill_step(DistillA
         C::store(dz, j, a.vocab, v);
       }
     }
-    each([&](float* v, int i) {
+    if (live_next) Rn.gather(a, En, zn, 0, a.vocab);
+    m = NEG;
+    s = 0.f;
+    auto write = [&](uintx4& d, int i) {
+      float v[C::N];
+      values(d, v);
 #pragma unroll
       for (int e = 0; e < C::N; ++e) v[e] = r.near(v[e]) * k;
       if (!apart) {
-        if (i < NC) *(uintx4u*)(dz + i * STEP + j0) = C::pack(v);
+        if (i < NC) __builtin_nontemporal_store(C::pack(v), (uintx4u*)(dz + i * STEP + j0));
         else C::store(dz, jt, a.vocab, v);
       }
       fetch(zn, i);
-    });
+    };
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+      if (i < whole) {
+        write(data[i], i);
+        if (i >= LAG) absorb(data[i - LAG]);
+      }
+    if (jt < a.vocab) write(tail, NC);
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+      if (i < whole && i >= whole - LAG) absorb(data[i]);
+    if (jt < a.vocab) absorb(tail);
     if (!zero) write_fixes<Z, NT>(a, T, dz, 0, a.vocab);
     E = En;
+#pragma unroll
+    for (int i = 0; i < Row<Z, NT>::KPT; ++i) R.zi[i] = Rn.zi[i];
     live = live_next;
   }
 }
@@ -481,9 +517,14 @@ __global__ __launch_bounds__(NT, NT * BLOCKS / 256) void k_distill_step(DistillA
 
 template <typename Z, bool FWD, bool BWD>
 static void launch_rows(const DistillArgs& a, hipStream_t s) {
-  constexpr int NT = 1024;
-  const unsigned rows = (unsigned)(a.rows < (1 << 20) ? a.rows : (1 << 20));
-  hipLaunchKernelGGL((k_distill_rows<Z, NT, FWD, BWD>), dim3(rows), dim3(NT), 0, s, a);
+  // A block of 512 threads a row keeps three rows to a CU; where there are not
+  // that many rows, one of 1024, and the gradient's rows are shared out to
+  // fill the CUs.
+  const bool few = a.rows <= 256;
+  const int64_t share = !FWD && few ? std::min<int64_t>(256 / a.rows, (a.vocab + 16383) / 16384) : 1;
+  const dim3 grid((unsigned)std::min<int64_t>(a.rows, 1 << 20), (unsigned)share);
+  if (few) hipLaunchKernelGGL((k_distill_rows<Z, 1024, FWD, BWD>), grid, dim3(1024), 0, s, a);
+  else hipLaunchKernelGGL((k_distill_rows<Z, 512, FWD, BWD>), grid, dim3(512), 0, s, a);
 }
 
 template <bool FWD, bool BWD>
