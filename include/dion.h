@@ -404,7 +404,7 @@ int dion_apply_batched(const float* const* Q, const void* const* X, void* const*
  *   rstd                rows floats (dion_rmsnorm_backward reads them)
  *   cols                1 .. 65536 (DION_E_UNSUPPORTED above)
  * dion_rmsnorm_int8 writes y as 8-bit codes q with a scale for each row,
- * for dion_int8_linear: scale = max|y| / 127, q = rint(y * (127 / max|y|)).
+ * for dion_int8_linear: scale = max|y| / 127, q = rint(y * (127 * (1 / max|y|))).
  * A row with max|y| below 2^-119 has scale 0 and codes 0; a row in which an
  * infinity or a NaN is left has scale NaN (and codes 0).  dion_int8_quantize
  * does the same to rows of x as they are; dion_int8_dequantize reads codes
@@ -426,7 +426,7 @@ int dion_int8_dequantize(const int8_t* q, int64_t ldq, const float* scale, void*
  * that reaches h itself along the residual stream, may be NULL.  dx is the
  * gradient of x and of the residual alike; it may be dy or dh in place.
  * dweight (cols values of weight_dtype) is summed in a fixed order. */
-size_t dion_rmsnorm_backward_workspace_size(int64_t rows, int32_t cols);
+size_t dion_rmsnorm_backward_workspace_size(int64_t rows, int32_t cols, int32_t dtype);
 int dion_rmsnorm_backward(const void* dy, int64_t lddy, const void* h, int64_t ldh, const void* weight,
                           const float* rstd, const void* dh, int64_t lddh, void* dx, int64_t lddx, void* dweight,
                           int64_t rows, int32_t cols, int32_t dtype, int32_t weight_dtype, void* workspace,

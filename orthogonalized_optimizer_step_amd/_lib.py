@@ -136,7 +136,7 @@ def _load():
     lib.dion_int8_quantize.restype = ctypes.c_int
     lib.dion_int8_dequantize.argtypes = mat + [vp] + mat + [i64, i32, i32, vp]
     lib.dion_int8_dequantize.restype = ctypes.c_int
-    lib.dion_rmsnorm_backward_workspace_size.argtypes = [i64, i32]
+    lib.dion_rmsnorm_backward_workspace_size.argtypes = [i64, i32, i32]
     lib.dion_rmsnorm_backward_workspace_size.restype = sz
     lib.dion_rmsnorm_backward.argtypes = mat + mat + [vp, vp] + mat + mat + [vp, i64, i32, i32, i32, vp, sz, vp]
     lib.dion_rmsnorm_backward.restype = ctypes.c_int

@@ -27,57 +27,7 @@ namespace {
 constexpr float NEG = -__builtin_inff();
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
-typedef int intx4 __attribute__((ext_vector_type(4)));
-typedef float floatx4 __attribute__((ext_vector_type(4)));
-// 16 bytes of logits at element alignment
-typedef uint32_t uintx4 __attribute__((ext_vector_type(4)));
-typedef uintx4 uintx4u __attribute__((aligned(2)));
-
-template <typename Z> struct Chunk {
-  static constexpr int N = 16 / (int)sizeof(Z);
-  static __device__ __forceinline__ void unpack(const uintx4& v, float* f) {
-    union { uintx4 u; Z z[N]; } c;
-    c.u = v;
-#pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = to_f(c.z[i]);
-  }
-  static __device__ __forceinline__ uintx4 pack(const float* f) {
-    union { uintx4 u; Z z[N]; } c;
-#pragma unroll
-    for (int i = 0; i < N; ++i) c.z[i] = from_f<Z>(f[i]);
-    return c.u;
-  }
-  // m, or the largest of the values where that is more
-  static __device__ __forceinline__ float largest(float m, const uintx4& v);
-  // elements [j, j + N) of a row of n, -inf past its end
-  static __device__ __forceinline__ uintx4 load(const Z* row, int j, int n) {
-    if (j + N <= n) return *(const uintx4u*)(row + j);
-    float f[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = j + i < n ? to_f(row[j + i]) : NEG;
-    return pack(f);
-  }
-  static __device__ __forceinline__ void store(Z* row, int j, int n, const float* f) {
-    if (j + N <= n) {
-      __builtin_nontemporal_store(pack(f), (uintx4u*)(row + j));
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (j + i < n) row[j + i] = from_f<Z>(f[i]);
-    }
-  }
-};
-
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
-
-// A barrier for LDS alone: loads and stores of global memory stay in flight.
-__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory"); }
-
-__device__ __forceinline__ float max3(float a, float b, float c) {   // drops NaN, which the sums keep
-  float r;
-  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
-  return r;
-}
 
 // Exponentials relative to the reference m.
 struct Ref {
@@ -97,14 +47,6 @@ struct Ref {
     return o.none ? 0.f : exp2_fast(wide ? (o.m - m) * c : o.R - R);
   }
 };
-
-template <typename Z> __device__ __forceinline__ float Chunk<Z>::largest(float m, const uintx4& v) {
-  float f[N];
-  unpack(v, f);
-#pragma unroll
-  for (int i = 0; i < N; i += 2) m = max3(m, f[i], f[i + 1]);
-  return m;
-}
 
 // Joins sums s relative to references m over a wave.
 __device__ __forceinline__ void wave_join(float& m, float& s, float c) {
@@ -316,7 +258,7 @@ __global__ __launch_bounds__(NT) void k_distill_rows(DistillArgs a) {
       float m = NEG, s = 0.f;
 #pragma unroll 4
       for (int j = tid * C::N; j < a.vocab; j += NT * C::N) {
-        const uintx4 v = C::load(z, j, a.vocab);
+        const uintx4 v = C::load(z, j, a.vocab, NEG);
         float f[C::N];
         C::unpack(v, f);
         const float cm = C::largest(m, v);
@@ -355,7 +297,7 @@ __global__ __launch_bounds__(NT) void k_distill_rows(DistillArgs a) {
 #pragma unroll 4
       for (int j = lo + tid * C::N; j < hi; j += NT * C::N) {
         float f[C::N];
-        C::unpack(C::load(z, j, hi), f);
+        C::unpack(C::load(z, j, hi, NEG), f);
 #pragma unroll
         for (int i = 0; i < C::N; ++i) f[i] = zero ? 0.f : r(f[i]) * k;
         C::store(dz, j, hi, f);
@@ -393,7 +335,7 @@ __global__ __launch_bounds__(NT, NT * BLOCKS / 256) void k_distill_step(DistillA
   };
   auto fetch = [&](const Z* z, int i) {
     if (i < NC) data[i] = *(const uintx4u*)(z + i * STEP + j0);
-    else tail = C::load(z, jt, a.vocab);
+    else tail = C::load(z, jt, a.vocab, NEG);
   };
   // the running largest value and the sum relative to it
   float m = NEG, s = 0.f;
@@ -450,7 +392,7 @@ __global__ __launch_bounds__(NT, NT * BLOCKS / 256) void k_distill_step(DistillA
         R.s = 0.f;
         for (int j = j0; j < a.vocab; j += STEP) {
           float v[C::N];
-          C::unpack(C::load(z, j, a.vocab), v);
+          C::unpack(C::load(z, j, a.vocab, NEG), v);
 #pragma unroll
           for (int e = 0; e < C::N; ++e) R.s += r(v[e]);
         }
@@ -474,7 +416,7 @@ __global__ __launch_bounds__(NT, NT * BLOCKS / 256) void k_distill_step(DistillA
     if (apart) {   // rare: from memory
       for (int j = j0; j < a.vocab; j += STEP) {
         float v[C::N] = {};
-        if (!zero) C::unpack(C::load(z, j, a.vocab), v);
+        if (!zero) C::unpack(C::load(z, j, a.vocab, NEG), v);
 #pragma unroll
         for (int e = 0; e < C::N; ++e) v[e] = zero ? 0.f : r.far(v[e]) * k;
         C::store(dz, j, a.vocab, v);

@@ -18,7 +18,6 @@ namespace dion {
 
 namespace {
 
-typedef int intx4 __attribute__((ext_vector_type(4)));
 typedef int intx16 __attribute__((ext_vector_type(16)));
 // sixteen bytes at any alignment
 typedef intx4 intx4u __attribute__((aligned(1)));
@@ -40,9 +39,6 @@ __device__ __forceinline__ void dma16(uint32_t voff, intx4 rsrc, uint32_t soff, 
                : "memory", "m0");
 }
 template <int N> __device__ __forceinline__ void wait_vmcnt() { asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory"); }
-// a barrier that waits for the wave's LDS accesses but not for copies in flight
-__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory"); }
-
 constexpr uint32_t OUT_OF_RANGE = 0x80000000u;
 
 // Descriptor of `bytes` bytes from p (raw: offsets in bytes, past the end reads zero).

@@ -4,9 +4,16 @@
 //
 //   s = x + residual (fp32)      h = s rounded to the input's type
 //   rstd = 1 / sqrt(mean(s^2) + eps)      y = s rstd w, rounded once
-//   8 bits: a = max |y|, scale = a / 127, q = rint(y (127 / a)) (ties to even)
+//   8 bits: a = max |y|, scale = a / 127, q = rint(y (127 (1 / a))) (ties to even)
 //   backward, with g = dy w and c = rstd^2 mean(g h):
 //     dx = rstd (g - h c) + dh        dw_j = sum over rows of dy_j h_j rstd
+//
+// A row is read once into registers, CH 16-byte chunks by each of its NT
+// threads (chunk i of thread t at element (i NT + t) N), and everything is
+// formed from there.  All of it is bound by memory; what it takes at 8192 x
+// 4096 and the like stands at the launch rules below.
+#include <algorithm>
+
 #include "train_device.h"
 #include "train_internal.h"
 
@@ -14,150 +21,419 @@ namespace dion {
 
 namespace {
 
-constexpr int NT = 256;
-
 // A row whose largest |y| is below 2^-119 has scale 0 and codes 0 (127 / a
 // would come near overflow); a row with an infinity or a NaN has scale NaN, so
 // that what is computed from its codes shows it.
 __device__ __forceinline__ void row_scale(float a, float& scale, float& inv) {
   const bool bad = !(a <= 3.402823466e+38f), tiny = a < 0x1p-119f;
   scale = bad ? __builtin_nanf("") : (tiny ? 0.f : a / 127.f);
-  inv = bad || tiny ? 0.f : 127.f / a;
+  inv = bad || tiny ? 0.f : 127.f * (1.f / a);
 }
 
-template <typename T, typename W, bool INT8>
-__global__ __launch_bounds__(NT) void k_rmsnorm(NormArgs a) {
+// Threads of a block: rows of one wave go four to a block.
+constexpr int block_of(int nt) { return nt == 64 ? 256 : nt; }
+
+// Sum or largest over the NT threads of a row.
+template <int NT> __device__ __forceinline__ float row_sum(float v, float* red) {
+  if constexpr (NT == 64) return wave_sum(v);
+  else return block_sum<NT>(v, red);
+}
+template <int NT> __device__ __forceinline__ float row_max(float v, float* red) {
+  if constexpr (NT == 64) return wave_max(v);
+  else return block_max<NT>(v, red);
+}
+
+// N weights from element j on, 0 past the row's end
+template <typename T>
+__device__ __forceinline__ void load_weight(const void* w, bool w32, int j, int n, float* f) {
+  constexpr int N = Chunk<T>::N;
+  if (sizeof(T) == 4 || !w32) {
+    Chunk<T>::unpack(Chunk<T>::load((const T*)w, j, n, 0.f), f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) Chunk<float>::unpack(Chunk<float>::load((const float*)w, j + i, n, 0.f), f + i);
+  }
+}
+
+// Forward.  Without a weight (codes of plain rows) y = s.
+template <typename T, bool INT8, int NT, int CH>
+__global__ __launch_bounds__(block_of(NT)) void k_rmsnorm(NormArgs a, bool w32) {
+  typedef Chunk<T> C;
+  constexpr int N = C::N, RPB = block_of(NT) / NT;
   __shared__ float red[NT / 64];
-  const int64_t row = blockIdx.x;
-  const T* x = (const T*)a.x + row * a.ldx;
-  const T* r = a.residual ? (const T*)a.residual + row * a.ldr : nullptr;
-  const W* w = (const W*)a.weight;
-  T* h = a.h ? (T*)a.h + row * a.ldh : nullptr;
-  auto value = [&](int j) {
-    float s = to_f(x[j]);
-    if (r) s += to_f(r[j]);
-    return s;
-  };
-  float rstd = 1.f;
-  if (w) {
-    float ss = 0.f;
-    for (int j = threadIdx.x; j < a.cols; j += NT) {
-      const float s = value(j);
-      ss += s * s;
+  const int t = threadIdx.x % NT;
+  for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / NT; row < a.rows; row += (int64_t)gridDim.x * RPB) {
+    const T* x = (const T*)a.x + row * a.ldx;
+    const T* r = a.residual ? (const T*)a.residual + row * a.ldr : nullptr;
+    T* h = a.h ? (T*)a.h + row * a.ldh : nullptr;
+    float s[CH][N];
+    {
+      uintx4 vx[CH], vr[CH];
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const int j = (i * NT + t) * N;
+        if (j < a.cols) {
+          vx[i] = C::load(x, j, a.cols, 0.f);
+          if (r) vr[i] = C::load(r, j, a.cols, 0.f);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const int j = (i * NT + t) * N;
+        if (j < a.cols) {
+          C::unpack(vx[i], s[i]);
+          if (r) {
+            float f[N];
+            C::unpack(vr[i], f);
+#pragma unroll
+            for (int e = 0; e < N; ++e) s[i][e] += f[e];
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < N; ++e) s[i][e] = 0.f;
+        }
+      }
     }
-    rstd = 1.f / sqrtf(block_sum<NT>(ss, red) / (float)a.cols + a.eps);
-  }
-  auto out = [&](int j, float s) { return w ? s * rstd * to_f(w[j]) : s; };
-  float scale = 0.f, inv = 0.f;
-  if (INT8) {
+    float rstd = 1.f;
+    if (a.weight) {
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < CH; ++i)
+#pragma unroll
+        for (int e = 0; e < N; ++e) ss += s[i][e] * s[i][e];
+      ss = row_sum<NT>(ss, red);
+      rstd = 1.f / sqrtf(ss / (float)a.cols + a.eps);
+    }
     float m = 0.f;
-    for (int j = threadIdx.x; j < a.cols; j += NT) m = max_nan(m, fabsf(out(j, value(j))));
-    row_scale(block_max<NT>(m, red), scale, inv);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int j = (i * NT + t) * N;
+      if (j >= a.cols) continue;
+      if (h) C::store_near(h, j, a.cols, s[i]);
+      if (a.weight) {
+        float w[N];
+        load_weight<T>(a.weight, w32, j, a.cols, w);
+#pragma unroll
+        for (int e = 0; e < N; ++e) s[i][e] = s[i][e] * rstd * w[e];
+      }
+      if (!INT8) C::store_near((T*)a.y + row * a.ldy, j, a.cols, s[i]);
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (INT8) m = max_nan(m, fabsf(s[i][e]));
+    }
+    float scale = 0.f, inv = 0.f;
+    if (INT8) {
+      row_scale(row_max<NT>(m, red), scale, inv);
+      int8_t* q = (int8_t*)a.y + row * a.ldy;
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const int j = (i * NT + t) * N;
+        if (j >= a.cols) continue;
+        uint32_t p[N / 4];
+#pragma unroll
+        for (int e = 0; e < N; e += 4) {
+          p[e / 4] = 0;
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            p[e / 4] |= (uint32_t)(uint8_t)(int8_t)(int)rintf(inv == 0.f ? 0.f : s[i][e + b] * inv) << (8 * b);
+        }
+        if (j + N <= a.cols) {
+          __builtin_memcpy(q + j, p, N);
+        } else {
+#pragma unroll
+          for (int e = 0; e < N; ++e)
+            if (j + e < a.cols) q[j + e] = (int8_t)(p[e / 4] >> (8 * (e % 4)));
+        }
+      }
+    }
+    if (t == 0) a.stat[row] = INT8 ? scale : rstd;
   }
-  for (int j = threadIdx.x; j < a.cols; j += NT) {
-    const float s = value(j), y = out(j, s);
-    if (h) h[j] = from_f<T>(s);
-    if (INT8) ((int8_t*)a.y)[row * a.ldy + j] = (int8_t)(int)rintf(inv == 0.f ? 0.f : y * inv);
-    else ((T*)a.y)[row * a.ldy + j] = from_f<T>(y);
+}
+
+// y = q scale, 16 codes a thread
+template <typename T>
+__global__ __launch_bounds__(256) void k_int8_dequantize(const int8_t* q, int64_t ldq, const float* scale, T* y,
+                                                         int64_t ldy, int64_t rows, int cols) {
+  typedef Chunk<T> C;
+  const int j = ((int)blockIdx.y * 256 + (int)threadIdx.x) * 16;
+  if (j >= cols) return;
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    const int8_t* src = q + row * ldq;
+    const float s = scale[row];
+    int8_t c[16];
+    if (j + 16 <= cols) {
+      __builtin_memcpy(c, src + j, 16);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) c[e] = j + e < cols ? src[j + e] : 0;
+    }
+    float f[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) f[e] = (float)c[e] * s;
+#pragma unroll
+    for (int e = 0; e < 16; e += C::N)
+      if (j + e < cols) C::store_near(y + row * ldy, j + e, cols, f + e);
   }
-  if (threadIdx.x == 0) a.stat[row] = INT8 ? scale : rstd;
+}
+
+// Backward.  A row's threads take rows gridDim.x RPB apart; the next row's
+// chunks are asked for before this row's dx is written, and dweight's terms
+// stay in registers until the end: one partial sum for each block, in the
+// order of its rows, joined over blocks by k_rmsnorm_dw.
+template <typename T, int NT, int CH>
+__global__ __launch_bounds__(block_of(NT)) void k_rmsnorm_backward(NormBackArgs a, bool w32) {
+  typedef Chunk<T> C;
+  constexpr int N = C::N, RPB = block_of(NT) / NT;
+  __shared__ float red[NT / 64 > 1 ? NT / 64 : 1];
+  __shared__ float joined[RPB > 1 ? RPB * NT * CH * N : 1];
+  const int t = threadIdx.x % NT, slot = threadIdx.x / NT;
+  float w[CH][N], dw[CH][N];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int j = (i * NT + t) * N;
+#pragma unroll
+    for (int e = 0; e < N; ++e) w[i][e] = dw[i][e] = 0.f;
+    if (j < a.cols) load_weight<T>(a.weight, w32, j, a.cols, w[i]);
+  }
+  uintx4 vy[CH], vh[CH], vd[CH];
+  float rs = 0.f;
+  auto fetch = [&](int64_t row, uintx4* y, uintx4* h, uintx4* d, float& r) {
+    if (row >= a.rows) return;
+    r = a.rstd[row];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int j = (i * NT + t) * N;
+      if (j >= a.cols) continue;
+      y[i] = C::load((const T*)a.dy + row * a.lddy, j, a.cols, 0.f);
+      h[i] = C::load((const T*)a.h + row * a.ldh, j, a.cols, 0.f);
+      if (a.dh) d[i] = C::load((const T*)a.dh + row * a.lddh, j, a.cols, 0.f);
+    }
+  };
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  int64_t row = (int64_t)blockIdx.x * RPB + slot;
+  fetch(row, vy, vh, vd, rs);
+  for (; row < a.rows; row += step) {
+    float dy[CH][N], h[CH][N], dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      if ((i * NT + t) * N < a.cols) {
+        C::unpack(vy[i], dy[i]);
+        C::unpack(vh[i], h[i]);
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          dw[i][e] += dy[i][e] * h[i][e] * rs;
+          dy[i][e] *= w[i][e];
+          dot += dy[i][e] * h[i][e];
+        }
+      }
+    }
+    uintx4 ny[CH], nh[CH], nd[CH];
+    float nr = 0.f;
+    fetch(row + step, ny, nh, nd, nr);
+    const float c = row_sum<NT>(dot, red) / (float)a.cols * rs * rs;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int j = (i * NT + t) * N;
+      if (j >= a.cols) continue;
+#pragma unroll
+      for (int e = 0; e < N; ++e) dy[i][e] = rs * (dy[i][e] - h[i][e] * c);
+      if (a.dh) {
+        float d[N];
+        C::unpack(vd[i], d);
+#pragma unroll
+        for (int e = 0; e < N; ++e) dy[i][e] += d[e];
+      }
+      C::store_near((T*)a.dx + row * a.lddx, j, a.cols, dy[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      vy[i] = ny[i];
+      vh[i] = nh[i];
+      vd[i] = nd[i];
+    }
+    rs = nr;
+  }
+  float* out = a.partial + (int64_t)blockIdx.x * a.cols;
+  if (RPB > 1) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+#pragma unroll
+      for (int e = 0; e < N; ++e) joined[slot * NT * CH * N + (i * NT + t) * N + e] = dw[i][e];
+    __syncthreads();
+    for (int j = threadIdx.x; j < a.cols; j += block_of(NT)) {
+      float v = 0.f;
+#pragma unroll
+      for (int r = 0; r < RPB; ++r) v += joined[r * NT * CH * N + j];
+      out[j] = v;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const int j = (i * NT + t) * N + e;
+        if (j < a.cols) out[j] = dw[i][e];
+      }
+  }
+}
+
+// Rows too long to be held with their weights and sums: dx with a second read
+// of the row, dweight's partial sums by columns.
+template <typename T>
+__global__ __launch_bounds__(1024) void k_rmsnorm_dx_long(NormBackArgs a, bool w32) {
+  typedef Chunk<T> C;
+  constexpr int N = C::N;
+  __shared__ float red[16];
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const T* dy = (const T*)a.dy + row * a.lddy;
+    const T* h = (const T*)a.h + row * a.ldh;
+    const T* dh = a.dh ? (const T*)a.dh + row * a.lddh : nullptr;
+    const float rstd = a.rstd[row];
+    float dot = 0.f;
+    for (int j = threadIdx.x * N; j < a.cols; j += 1024 * N) {
+      float y[N], v[N], w[N];
+      C::unpack(C::load(dy, j, a.cols, 0.f), y);
+      C::unpack(C::load(h, j, a.cols, 0.f), v);
+      load_weight<T>(a.weight, w32, j, a.cols, w);
+#pragma unroll
+      for (int e = 0; e < N; ++e) dot += y[e] * w[e] * v[e];
+    }
+    const float c = block_sum<1024>(dot, red) / (float)a.cols * rstd * rstd;
+    for (int j = threadIdx.x * N; j < a.cols; j += 1024 * N) {
+      float y[N], v[N], w[N];
+      C::unpack(C::load(dy, j, a.cols, 0.f), y);
+      C::unpack(C::load(h, j, a.cols, 0.f), v);
+      load_weight<T>(a.weight, w32, j, a.cols, w);
+#pragma unroll
+      for (int e = 0; e < N; ++e) y[e] = rstd * (y[e] * w[e] - v[e] * c);
+      if (dh) {
+        float d[N];
+        C::unpack(C::load(dh, j, a.cols, 0.f), d);
+#pragma unroll
+        for (int e = 0; e < N; ++e) y[e] += d[e];
+      }
+      C::store_near((T*)a.dx + row * a.lddx, j, a.cols, y);
+    }
+  }
 }
 
 template <typename T>
-__global__ __launch_bounds__(NT) void k_int8_dequantize(const int8_t* q, int64_t ldq, const float* scale, T* y,
-                                                        int64_t ldy, int cols) {
-  const int64_t row = blockIdx.x;
-  const float s = scale[row];
-  for (int j = threadIdx.x; j < cols; j += NT) y[row * ldy + j] = from_f<T>((float)q[row * ldq + j] * s);
-}
-
-template <typename T, typename W>
-__global__ __launch_bounds__(NT) void k_rmsnorm_dx(NormBackArgs a) {
-  __shared__ float red[NT / 64];
-  const int64_t row = blockIdx.x;
-  const T* dy = (const T*)a.dy + row * a.lddy;
-  const T* h = (const T*)a.h + row * a.ldh;
-  const T* dh = a.dh ? (const T*)a.dh + row * a.lddh : nullptr;
-  const W* w = (const W*)a.weight;
-  const float rstd = a.rstd[row];
-  float d = 0.f;
-  for (int j = threadIdx.x; j < a.cols; j += NT) d += to_f(dy[j]) * to_f(w[j]) * to_f(h[j]);
-  const float c = block_sum<NT>(d, red) / (float)a.cols * rstd * rstd;
-  for (int j = threadIdx.x; j < a.cols; j += NT) {
-    float v = rstd * (to_f(dy[j]) * to_f(w[j]) - to_f(h[j]) * c);
-    if (dh) v += to_f(dh[j]);
-    ((T*)a.dx)[row * a.lddx + j] = from_f<T>(v);
-  }
-}
-
-// partial[p][j]: the rows of part p in order
-template <typename T>
-__global__ __launch_bounds__(NT) void k_rmsnorm_dw_part(NormBackArgs a) {
-  const int j = blockIdx.x * NT + threadIdx.x;
+__global__ __launch_bounds__(256) void k_rmsnorm_dw_long(NormBackArgs a) {
+  const int j = blockIdx.x * 256 + threadIdx.x;
   if (j >= a.cols) return;
-  const int64_t chunk = (a.rows + a.parts - 1) / a.parts, r0 = blockIdx.y * chunk;
-  const int64_t r1 = r0 + chunk < a.rows ? r0 + chunk : a.rows;
+  const int64_t r0 = a.rows * blockIdx.y / a.parts, r1 = a.rows * (blockIdx.y + 1) / a.parts;
   float d = 0.f;
   for (int64_t r = r0; r < r1; ++r)
     d += to_f(((const T*)a.dy)[r * a.lddy + j]) * to_f(((const T*)a.h)[r * a.ldh + j]) * a.rstd[r];
   a.partial[(int64_t)blockIdx.y * a.cols + j] = d;
 }
 
-template <typename W>
-__global__ __launch_bounds__(NT) void k_rmsnorm_dw(NormBackArgs a) {
-  const int j = blockIdx.x * NT + threadIdx.x;
-  if (j >= a.cols) return;
+// dweight from the parts' sums: 32 columns a block, the parts shared by 16
+// groups of threads, whose sums meet in LDS.
+template <typename W> __global__ __launch_bounds__(512) void k_rmsnorm_dw(NormBackArgs a) {
+  __shared__ float sum[16][33];
+  const int x = threadIdx.x & 31, g = threadIdx.x >> 5, j = blockIdx.x * 32 + x;
   float d = 0.f;
-  for (int p = 0; p < a.parts; ++p) d += a.partial[(int64_t)p * a.cols + j];
-  ((W*)a.dweight)[j] = from_f<W>(d);
+  if (j < a.cols) {
+#pragma unroll 8
+    for (int p = g; p < a.parts; p += 16) d += a.partial[(int64_t)p * a.cols + j];
+  }
+  sum[g][x] = d;
+  __syncthreads();
+  if (g == 0 && j < a.cols) {
+    d = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) d += sum[i][x];
+    ((W*)a.dweight)[j] = from_f<W>(d);
+  }
 }
 
-template <typename T, typename W>
-void launch_norm(bool int8_out, const NormArgs& a, hipStream_t s) {
-  const dim3 g((unsigned)a.rows);
-  if (int8_out) hipLaunchKernelGGL((k_rmsnorm<T, W, true>), g, dim3(NT), 0, s, a);
-  else hipLaunchKernelGGL((k_rmsnorm<T, W, false>), g, dim3(NT), 0, s, a);
+template <typename T, bool INT8, int NT, int CH>
+void launch_forward(const NormArgs& a, bool w32, hipStream_t s) {
+  constexpr int RPB = block_of(NT) / NT;
+  const unsigned grid = (unsigned)std::min<int64_t>((a.rows + RPB - 1) / RPB, 1 << 20);
+  hipLaunchKernelGGL((k_rmsnorm<T, INT8, NT, CH>), dim3(grid), dim3(block_of(NT)), 0, s, a, w32);
 }
 
-template <typename T, typename W>
-void launch_back(const NormBackArgs& a, hipStream_t s) {
-  const unsigned gx = (unsigned)((a.cols + NT - 1) / NT);
-  // dweight first: dx may overwrite dy or dh
-  if (a.parts) hipLaunchKernelGGL((k_rmsnorm_dw_part<T>), dim3(gx, (unsigned)a.parts), dim3(NT), 0, s, a);
-  hipLaunchKernelGGL((k_rmsnorm_dw<W>), dim3(gx), dim3(NT), 0, s, a);
-  if (a.rows) hipLaunchKernelGGL((k_rmsnorm_dx<T, W>), dim3((unsigned)a.rows), dim3(NT), 0, s, a);
+// Threads and chunks of a row: the fewest that hold it.
+template <typename T, bool INT8>
+void launch_norm(const NormArgs& a, bool w32, hipStream_t s) {
+  const int chunks = (a.cols + Chunk<T>::N - 1) / Chunk<T>::N;
+  if (chunks <= 64) launch_forward<T, INT8, 64, 1>(a, w32, s);
+  else if (chunks <= 128) launch_forward<T, INT8, 64, 2>(a, w32, s);
+  else if (chunks <= 256) launch_forward<T, INT8, 64, 4>(a, w32, s);
+  else if (chunks <= 512) launch_forward<T, INT8, 256, 2>(a, w32, s);
+  else if (chunks <= 1024) launch_forward<T, INT8, 256, 4>(a, w32, s);
+  else if (chunks <= 2048) launch_forward<T, INT8, 512, 4>(a, w32, s);
+  else launch_forward<T, INT8, 1024, sizeof(T) == 4 ? 16 : 8>(a, w32, s);
+}
+
+constexpr int kHeldChunks = 2048;   // longest row that the backward pass holds, in 16-byte chunks
+
+template <typename T, int NT, int CH>
+void launch_backward(const NormBackArgs& a, bool w32, hipStream_t s) {
+  hipLaunchKernelGGL((k_rmsnorm_backward<T, NT, CH>), dim3((unsigned)a.parts), dim3(block_of(NT)), 0, s, a, w32);
+}
+
+template <typename T>
+void launch_back(const NormBackArgs& a, bool w32, hipStream_t s) {
+  const int chunks = (a.cols + Chunk<T>::N - 1) / Chunk<T>::N;
+  if (a.rows > 0) {
+    if (chunks <= 64) launch_backward<T, 64, 1>(a, w32, s);
+    else if (chunks <= 128) launch_backward<T, 64, 2>(a, w32, s);
+    else if (chunks <= 256) launch_backward<T, 64, 4>(a, w32, s);
+    else if (chunks <= 512) launch_backward<T, 256, 2>(a, w32, s);
+    else if (chunks <= 1024) launch_backward<T, 256, 4>(a, w32, s);
+    else if (chunks <= kHeldChunks) launch_backward<T, 512, 4>(a, w32, s);
+    else {
+      const unsigned gx = (unsigned)((a.cols + 255) / 256);
+      // dweight first: dx may be written over dy or dh
+      hipLaunchKernelGGL((k_rmsnorm_dw_long<T>), dim3(gx, (unsigned)a.parts), dim3(256), 0, s, a);
+      hipLaunchKernelGGL((k_rmsnorm_dx_long<T>), dim3((unsigned)std::min<int64_t>(a.rows, 1 << 20)), dim3(1024), 0, s, a,
+                         w32);
+    }
+  }
+  const dim3 gw((unsigned)((a.cols + 31) / 32));
+  if (w32) hipLaunchKernelGGL((k_rmsnorm_dw<float>), gw, dim3(512), 0, s, a);
+  else hipLaunchKernelGGL((k_rmsnorm_dw<T>), gw, dim3(512), 0, s, a);
 }
 
 }  // namespace
 
-int norm_back_parts(int64_t rows, int cols) {
-  (void)cols;
-  return (int)(rows < 64 ? (rows > 0 ? 1 : 0) : rows / 64 < 256 ? rows / 64 : 256);
+// Blocks of the backward pass, each with a partial sum of dweight.
+int norm_back_parts(int64_t rows, int cols, int fmt) {
+  const int chunks = (cols + (fmt == 1 ? 3 : 7)) / (fmt == 1 ? 4 : 8);
+  if (chunks > kHeldChunks) return (int)std::min<int64_t>(256, (rows + 31) / 32);
+  if (chunks <= 256) return (int)std::min<int64_t>(1024, (rows + 3) / 4);
+  return (int)std::min<int64_t>(chunks <= 1024 ? 1024 : 512, rows);
 }
 
-#define DION_FMT2(F, fmt, wfmt, ...)                                         \
-  do {                                                                       \
-    if (fmt == 1) F<float, float>(__VA_ARGS__);                              \
-    else if (fmt == 0 && wfmt == 1) F<bf16_t, float>(__VA_ARGS__);           \
-    else if (fmt == 0) F<bf16_t, bf16_t>(__VA_ARGS__);                       \
-    else if (wfmt == 1) F<fp16_t, float>(__VA_ARGS__);                       \
-    else F<fp16_t, fp16_t>(__VA_ARGS__);                                     \
-  } while (0)
-
 void launch_rmsnorm(int fmt, int wfmt, bool int8_out, const NormArgs& a, hipStream_t s) {
-  DION_FMT2(launch_norm, fmt, wfmt, int8_out, a, s);
+  const bool w32 = wfmt == 1;
+  if (int8_out) {
+    if (fmt == 1) launch_norm<float, true>(a, w32, s);
+    else if (fmt == 0) launch_norm<bf16_t, true>(a, w32, s);
+    else launch_norm<fp16_t, true>(a, w32, s);
+  } else {
+    if (fmt == 1) launch_norm<float, false>(a, w32, s);
+    else if (fmt == 0) launch_norm<bf16_t, false>(a, w32, s);
+    else launch_norm<fp16_t, false>(a, w32, s);
+  }
 }
 
 void launch_rmsnorm_backward(int fmt, int wfmt, const NormBackArgs& a, hipStream_t s) {
-  DION_FMT2(launch_back, fmt, wfmt, a, s);
+  const bool w32 = wfmt == 1;
+  if (fmt == 1) launch_back<float>(a, w32, s);
+  else if (fmt == 0) launch_back<bf16_t>(a, w32, s);
+  else launch_back<fp16_t>(a, w32, s);
 }
 
 void launch_int8_dequantize(int fmt, const int8_t* q, int64_t ldq, const float* scale, void* y, int64_t ldy,
                             int64_t rows, int cols, hipStream_t s) {
-  const dim3 g((unsigned)rows), b(NT);
-  if (fmt == 1) hipLaunchKernelGGL((k_int8_dequantize<float>), g, b, 0, s, q, ldq, scale, (float*)y, ldy, cols);
-  else if (fmt == 0) hipLaunchKernelGGL((k_int8_dequantize<bf16_t>), g, b, 0, s, q, ldq, scale, (bf16_t*)y, ldy, cols);
-  else hipLaunchKernelGGL((k_int8_dequantize<fp16_t>), g, b, 0, s, q, ldq, scale, (fp16_t*)y, ldy, cols);
+  const dim3 g((unsigned)std::min<int64_t>(rows, 1 << 20), (unsigned)((cols + 4095) / 4096)), b(256);
+  if (fmt == 1) hipLaunchKernelGGL((k_int8_dequantize<float>), g, b, 0, s, q, ldq, scale, (float*)y, ldy, rows, cols);
+  else if (fmt == 0) hipLaunchKernelGGL((k_int8_dequantize<bf16_t>), g, b, 0, s, q, ldq, scale, (bf16_t*)y, ldy, rows, cols);
+  else hipLaunchKernelGGL((k_int8_dequantize<fp16_t>), g, b, 0, s, q, ldq, scale, (fp16_t*)y, ldy, rows, cols);
 }
 
 }  // namespace dion

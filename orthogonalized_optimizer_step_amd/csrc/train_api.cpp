@@ -80,12 +80,9 @@ void check_workspace(Check& c, const void* ws, size_t have, size_t need) {
                                  std::to_string(have) + " given");
 }
 
-constexpr int64_t kMaxRows = 1 << 23;   // one block of 256 threads a row
-
 void check_rows(Check& c, int64_t rows, int32_t cols, const char* what) {
   c.need(rows >= 0, "rows must not be negative");
   c.need(cols > 0, what);
-  if (rows > kMaxRows) c.fail(DION_E_UNSUPPORTED, "more than 2^23 rows");
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
@@ -178,12 +175,12 @@ int dion_int8_dequantize(const int8_t* q, int64_t ldq, const float* scale, void*
   });
 }
 
-size_t dion_rmsnorm_backward_workspace_size(int64_t rows, int32_t cols) {
-  if (rows < 0 || cols <= 0 || cols > kNormMaxCols || rows > kMaxRows) {
-    (void)guarded([&]() { return set_error(DION_E_INVAL, "invalid rows or cols"); });
+size_t dion_rmsnorm_backward_workspace_size(int64_t rows, int32_t cols, int32_t dtype) {
+  if (rows < 0 || cols <= 0 || cols > kNormMaxCols || !valid_dtype(dtype)) {
+    (void)guarded([&]() { return set_error(DION_E_INVAL, "invalid rows, cols or dtype"); });
     return 0;
   }
-  return align256((size_t)norm_back_parts(rows, cols) * cols * 4 + 1);
+  return align256((size_t)norm_back_parts(rows, cols, dtype) * cols * 4 + 1);
 }
 
 int dion_rmsnorm_backward(const void* dy, int64_t lddy, const void* h, int64_t ldh, const void* weight,
@@ -207,7 +204,7 @@ int dion_rmsnorm_backward(const void* dy, int64_t lddy, const void* h, int64_t l
     for (const View& in : {vdy, vdh}) check_apart(c, vdx, in, true);
     for (const View& in : {vh, vw, vr, vdw}) check_apart(c, vdx, in);
     for (const View& in : {vdy, vdh, vh, vw, vr}) check_apart(c, vdw, in);
-    check_workspace(c, workspace, workspace_bytes, dion_rmsnorm_backward_workspace_size(rows, cols));
+    check_workspace(c, workspace, workspace_bytes, dion_rmsnorm_backward_workspace_size(rows, cols, dtype));
     if (c.code == DION_OK) {
       const View vws{workspace, (int64_t)workspace_bytes, 1, (int64_t)workspace_bytes, 1, "workspace"};
       for (const View& in : {vdy, vdh, vh, vw, vr, vdx, vdw}) check_apart(c, vws, in);
@@ -215,7 +212,7 @@ int dion_rmsnorm_backward(const void* dy, int64_t lddy, const void* h, int64_t l
     if (c.code != DION_OK) return c.done();
     const hipStream_t st = (hipStream_t)stream;
     const NormBackArgs a{dy,  h,    weight, rstd, dh,   dx,   dweight, (float*)workspace, lddy, ldh,
-                         lddh, lddx, rows,   cols, norm_back_parts(rows, cols)};
+                         lddh, lddx, rows,   cols, norm_back_parts(rows, cols, dtype)};
     const double n = (double)rows * cols;
     return run_phase("rmsnorm_backward", "dion::k_rmsnorm_backward", 10.0 * n, n * es * (3 + (dh ? 1 : 0)), st,
                      [&]() { launch_rmsnorm_backward(dtype, weight_dtype, a, st); });

@@ -78,7 +78,7 @@ struct DistillArgs {
 
 // rows of one dweight partial sum (fixed by the sizes alone, so that the
 // order of the sum is too)
-int norm_back_parts(int64_t rows, int cols);
+int norm_back_parts(int64_t rows, int cols, int fmt);
 constexpr int kNormMaxCols = 65536;
 constexpr int kDistillMaxK = 1024;
 

@@ -166,7 +166,7 @@ def rmsnorm_backward(dy, h, weight, rstd, dh=None, workspace=None, stream=None):
     _vector(weight, "weight", cols, (h.dtype, torch.float32))
     _vector(rstd, "rstd", rows, (torch.float32,))
     s = _Stream(stream)
-    keep, ws, have = s.workspace(lib.dion_rmsnorm_backward_workspace_size(rows, cols), h, workspace)
+    keep, ws, have = s.workspace(lib.dion_rmsnorm_backward_workspace_size(rows, cols, code), h, workspace)
     dx = s.empty(h.shape, h.dtype, h)
     dw = s.empty(weight.shape, weight.dtype, h)
     check(lib.dion_rmsnorm_backward(dy.data_ptr(), lddy, h.data_ptr(), ldh, weight.data_ptr(), rstd.data_ptr(),

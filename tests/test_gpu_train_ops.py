@@ -183,7 +183,7 @@ def test_quantize_codes_are_the_definition(dion, rows, cols, dtype, pad):
     q, scale = dion.int8_quantize(x)
     a = x.float().abs().amax(1)
     assert torch.equal(scale, (a.double() / 127).float())
-    assert torch.equal(q.float(), torch.round(x.float() * (127 / a.double()).float()[:, None]))
+    assert torch.equal(q.float(), torch.round(x.float() * (127 * (1 / a.double()).float())[:, None]))
     for out in (torch.bfloat16, torch.float16, torch.float32):
         assert torch.equal(dion.int8_dequantize(q, scale, out), (q.float() * scale[:, None]).to(out))
 
