@@ -436,7 +436,8 @@ int dion_rmsnorm_backward(const void* dy, int64_t lddy, const void* h, int64_t l
  *   out[i][j] = (sum_l a[i][l] b[j][l]) * a_scale[i] * b_scale[j] + bias[j]
  * a: m x k activations, b: n x k weights (output channels as rows), both any
  * int8 values; the sum is exact in 32 bits, k < 2^17 (DION_E_UNSUPPORTED
- * above).  bias: n values of bias_dtype, or NULL.  out: m x n of out_dtype. */
+ * above).  bias: n values of bias_dtype, or NULL.  out: m x n of out_dtype.
+ * Sizes whose workspace size is 256 use none: it may be NULL. */
 size_t dion_int8_linear_workspace_size(int64_t m, int64_t n, int32_t k);
 int dion_int8_linear(const int8_t* a, int64_t lda, const float* a_scale, const int8_t* b, int64_t ldb,
                      const float* b_scale, const void* bias, int32_t bias_dtype, void* out, int64_t ldo, int64_t m,
@@ -460,10 +461,9 @@ int dion_int8_linear(const int8_t* a, int64_t lda, const float* a_scale, const i
  *   dlogits    rows x vocab of `dtype`; may be the logits in place
  * dion_distill_topk_step computes the loss and the gradient in one call, for
  * a grad_loss known ahead of it. */
-size_t dion_distill_topk_workspace_size(int64_t rows, int32_t vocab);
 int dion_distill_topk(const void* logits, int64_t ldz, const void* teacher, const void* teacher_idx, float* loss,
                       float* stats, int64_t rows, int32_t vocab, int32_t k, int32_t dtype, int32_t teacher_dtype,
-                      int32_t idx_bytes, float temperature, void* workspace, size_t workspace_bytes, void* stream);
+                      int32_t idx_bytes, float temperature, void* stream);
 int dion_distill_topk_backward(const float* grad_loss, const void* logits, int64_t ldz, const float* stats,
                                const void* teacher, const void* teacher_idx, void* dlogits, int64_t ldd, int64_t rows,
                                int32_t vocab, int32_t k, int32_t dtype, int32_t teacher_dtype, int32_t idx_bytes,
@@ -471,7 +471,7 @@ int dion_distill_topk_backward(const float* grad_loss, const void* logits, int64
 int dion_distill_topk_step(const void* logits, int64_t ldz, const void* teacher, const void* teacher_idx,
                            const float* grad_loss, float* loss, void* dlogits, int64_t ldd, int64_t rows,
                            int32_t vocab, int32_t k, int32_t dtype, int32_t teacher_dtype, int32_t idx_bytes,
-                           float temperature, void* workspace, size_t workspace_bytes, void* stream);
+                           float temperature, void* stream);
 
 /* Useful floating-point operations of one dion_orth_batched call on this
  * batch, in the executed formulation, symmetric products counted once:

@@ -244,8 +244,9 @@ int dion_int8_linear(const int8_t* a, int64_t lda, const float* a_scale, const i
     for (const View& v : {va, vb, vsa, vsb, vo}) check_view(c, v);
     if (bias) check_view(c, vbias);
     for (const View& in : {va, vb, vsa, vsb, vbias}) check_apart(c, vo, in);
-    check_workspace(c, workspace, workspace_bytes, dion_int8_linear_workspace_size(m, n, k));
-    if (c.code == DION_OK) {
+    const size_t need = dion_int8_linear_workspace_size(m, n, k);
+    if (need > 256) {   // 256: none is used
+      check_workspace(c, workspace, workspace_bytes, need);
       const View vws{workspace, (int64_t)workspace_bytes, 1, (int64_t)workspace_bytes, 1, "workspace"};
       for (const View& in : {va, vb, vsa, vsb, vbias, vo}) check_apart(c, vws, in);
     }
@@ -302,17 +303,9 @@ double distill_bytes(const DistillArgs& a, int64_t es, int idx_bytes, bool grad)
 
 extern "C" {
 
-size_t dion_distill_topk_workspace_size(int64_t rows, int32_t vocab) {
-  if (rows < 0 || vocab <= 0) {
-    (void)guarded([&]() { return set_error(DION_E_INVAL, "invalid rows or vocab"); });
-    return 0;
-  }
-  return align256((size_t)rows * 8 + 1);
-}
-
 int dion_distill_topk(const void* logits, int64_t ldz, const void* teacher, const void* teacher_idx, float* loss,
                       float* stats, int64_t rows, int32_t vocab, int32_t k, int32_t dtype, int32_t teacher_dtype,
-                      int32_t idx_bytes, float temperature, void* workspace, size_t workspace_bytes, void* stream) {
+                      int32_t idx_bytes, float temperature, void* stream) {
   return guarded([&]() {
     const DistillArgs a{logits, teacher, teacher_idx, nullptr, loss, (float2*)stats, nullptr, ldz, 0, rows, vocab, k,
                         teacher_dtype, idx_bytes == 8, temperature};
@@ -322,7 +315,6 @@ int dion_distill_topk(const void* logits, int64_t ldz, const void* teacher, cons
     c.output(c.stats);
     c.need((uintptr_t)stats % 8 == 0, "stats must be 8-byte aligned");
     check_apart(c, c.loss, c.stats);
-    check_workspace(c, workspace, workspace_bytes, dion_distill_topk_workspace_size(rows, vocab));
     if (c.code != DION_OK || rows == 0) return c.done();
     const hipStream_t st = (hipStream_t)stream;
     return run_phase("distill_topk", "dion::k_distill_forward", 4.0 * rows * vocab,
@@ -353,20 +345,15 @@ int dion_distill_topk_backward(const float* grad_loss, const void* logits, int64
 int dion_distill_topk_step(const void* logits, int64_t ldz, const void* teacher, const void* teacher_idx,
                            const float* grad_loss, float* loss, void* dlogits, int64_t ldd, int64_t rows,
                            int32_t vocab, int32_t k, int32_t dtype, int32_t teacher_dtype, int32_t idx_bytes,
-                           float temperature, void* workspace, size_t workspace_bytes, void* stream) {
+                           float temperature, void* stream) {
   return guarded([&]() {
-    const DistillArgs a{logits, teacher, teacher_idx, grad_loss, loss, (float2*)workspace, dlogits, ldz, ldd, rows,
+    const DistillArgs a{logits, teacher, teacher_idx, grad_loss, loss, nullptr, dlogits, ldz, ldd, rows,
                         vocab, k, teacher_dtype, idx_bytes == 8, temperature};
     DistillCheck c(a, dtype, idx_bytes);
     if (c.code != DION_OK) return c.done();
     c.output(c.loss);
     c.output(c.dz, true);
     check_apart(c, c.dz, c.loss);
-    check_workspace(c, workspace, workspace_bytes, dion_distill_topk_workspace_size(rows, vocab));
-    if (c.code == DION_OK) {
-      const View vws{workspace, (int64_t)workspace_bytes, 1, (int64_t)workspace_bytes, 1, "workspace"};
-      for (const View& in : {c.z, c.t, c.ix, c.gl, c.loss, c.dz}) check_apart(c, vws, in);
-    }
     if (c.code != DION_OK || rows == 0) return c.done();
     const hipStream_t st = (hipStream_t)stream;
     return run_phase("distill_topk_step", "dion::k_distill_step", 8.0 * rows * vocab,

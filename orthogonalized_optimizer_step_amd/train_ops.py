@@ -33,21 +33,38 @@ def _code(dtype, what):
     return code
 
 
-def _gpu(t, what):
+# the handle of a device's current stream, without a Stream object around it
+# (0.1 against 2.7 us, of a call that takes about 10 on the host)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _device(t, what):
+    """the tensor's device, which has to be the current one"""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         _fail(f"{what} must be a tensor on the GPU")
-    if t.get_device() != torch.cuda.current_device():
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
         _fail(f"{what} is on another device than the current one")
+    return dev
+
+
+def _beside(t, what, dev):
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        _fail(f"{what} must be a tensor on the same GPU as the others")
 
 
 def _matrix(t, what):
     """rows, cols and row stride of a tensor whose leading dimensions flatten into rows"""
-    _gpu(t, what)
-    if t.dim() != 2:
-        if t.dim() == 0:
+    shape = t.shape
+    if len(shape) == 2 and t.is_contiguous():
+        rows, cols = shape
+        return rows, cols, cols
+    if len(shape) != 2:
+        if len(shape) == 0:
             _fail(f"{what} must have at least one dimension")
         try:
-            t = t.view(-1, t.shape[-1]) if t.numel() else t.reshape(t.numel() // max(1, t.shape[-1]), t.shape[-1])
+            t = t.view(-1, shape[-1]) if t.numel() else t.reshape(t.numel() // max(1, shape[-1]), shape[-1])
         except RuntimeError:
             _fail(f"{what}: the leading dimensions do not flatten into equally spaced rows")
     rows, cols = t.shape
@@ -56,69 +73,84 @@ def _matrix(t, what):
     return rows, cols, (t.stride(0) if rows > 1 else cols)
 
 
-def _same(t, what, shape, dtype):
-    if t.shape != shape:
-        _fail(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != dtype:
-        _fail(f"{what}: expected {dtype}, got {t.dtype}")
+def _same(t, what, like, dev):
+    """row stride of a tensor that has to match another's shape and dtype"""
+    _beside(t, what, dev)
+    if t.shape != like.shape:
+        _fail(f"{what}: shape {tuple(t.shape)}, expected {tuple(like.shape)}")
+    if t.dtype != like.dtype:
+        _fail(f"{what}: expected {like.dtype}, got {t.dtype}")
     return _matrix(t, what)[2]
 
 
-def _vector(t, what, n, dtypes):
-    _gpu(t, what)
+def _vector(t, what, n, dtypes, dev):
+    _beside(t, what, dev)
     if t.numel() != n or (n > 1 and not t.is_contiguous()):
         _fail(f"{what} must be contiguous with {n} entries")
     if t.dtype not in dtypes:
         _fail(f"{what}: unsupported dtype {t.dtype}")
-    return t
 
 
-class _Stream:
-    """The stream of a call: its handle, allocations that belong to it, and the tensors it uses."""
+def _handle(stream, dev):
+    return _raw_stream(dev) if stream is None else stream.cuda_stream
 
-    def __init__(self, stream):
-        self.stream = stream
-        self.handle = (torch.cuda.current_stream() if stream is None else stream).cuda_stream
 
-    def empty(self, shape, dtype, like):
-        if self.stream is None:
-            return torch.empty(shape, dtype=dtype, device=like.device)
-        with torch.cuda.stream(self.stream):
-            out = torch.empty(shape, dtype=dtype, device=like.device)
-        out.record_stream(torch.cuda.current_stream())
-        return out
+def _new(shape, dtype, like, stream):
+    """A tensor for a call on `stream`: allocated in that stream's memory, and
+    known to be used by the current one, which reads the results."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        out = torch.empty(shape, dtype=dtype, device=like.device)
+    out.record_stream(torch.cuda.current_stream())
+    return out
 
-    def workspace(self, nbytes, like, given):
-        """address and length of the caller's workspace, or of a new one (kept alive by the returned tensor)"""
-        if nbytes == 0:
-            raise DionError(-1, lib.dion_last_error().decode())
-        if given is None:
-            given = self.empty(nbytes + 256, torch.uint8, like)
-        at = given.data_ptr()
-        off = -at % 256
-        have = given.numel() * given.element_size() - off
-        if have < nbytes:
-            raise DionError(-3, f"workspace too small: need {nbytes} bytes")
-        return given, at + off, have
 
-    def used(self, *tensors):
-        if self.stream is not None:
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(self.stream)
+def _new_like(like, dtype, stream):
+    """the same with another tensor's shape, contiguous"""
+    if stream is None and like.is_contiguous():
+        return torch.empty_like(like, dtype=dtype)
+    return _new(like.shape, dtype, like, stream)
+
+
+def _workspace(nbytes, like, given, stream):
+    """the caller's workspace, or a new one, with its aligned address and length"""
+    if nbytes == 0:
+        raise DionError(-1, lib.dion_last_error().decode())
+    if given is None:
+        given = _new(nbytes + 256, torch.uint8, like, stream)
+    elif not given.is_cuda or not given.is_contiguous():
+        _fail("the workspace must be a contiguous tensor on the GPU")
+    at = given.data_ptr()
+    off = -at % 256
+    have = given.numel() * given.element_size() - off
+    if have < nbytes:
+        raise DionError(-3, f"workspace too small: need {nbytes} bytes")
+    return given, at + off, have
+
+
+def _used(stream, *tensors):
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+_F32 = (torch.float32,)
+
+
 # ------------------------------------------------------------------ RMS norm
 def _norm_inputs(x, weight, residual):
+    dev = _device(x, "x")
     rows, cols, ldx = _matrix(x, "x")
     code = _code(x.dtype, "x")
-    ldr = 0 if residual is None else _same(residual, "residual", x.shape, x.dtype)
-    _vector(weight, "weight", cols, (x.dtype, torch.float32))
-    return rows, cols, ldx, ldr, code, _CODE[weight.dtype]
+    ldr = 0 if residual is None else _same(residual, "residual", x, dev)
+    _vector(weight, "weight", cols, (x.dtype, torch.float32), dev)
+    return dev, rows, cols, ldx, ldr, code, _CODE[weight.dtype]
 
 
 def rmsnorm(x, weight, residual=None, eps=1e-6, stream=None):
@@ -127,14 +159,15 @@ def rmsnorm(x, weight, residual=None, eps=1e-6, stream=None):
     ``h`` is the sum in x's type, the residual stream carried on (x itself
     without a residual); ``rstd`` (fp32, one for each row) and ``h`` are what
     ``rmsnorm_backward`` needs.  ``weight``: x's type or fp32."""
-    rows, cols, ldx, ldr, code, wcode = _norm_inputs(x, weight, residual)
-    s = _Stream(stream)
-    y = s.empty(x.shape, x.dtype, x)
-    h = None if residual is None else s.empty(x.shape, x.dtype, x)
-    rstd = s.empty(x.shape[:-1], torch.float32, x)
-    check(lib.dion_rmsnorm(x.data_ptr(), ldx, _ptr(residual), ldr, weight.data_ptr(), _ptr(h), cols, y.data_ptr(),
-                           cols, rstd.data_ptr(), rows, cols, code, wcode, eps, s.handle))
-    s.used(x, weight, residual)
+    dev, rows, cols, ldx, ldr, code, wcode = _norm_inputs(x, weight, residual)
+    y = _new_like(x, x.dtype, stream)
+    h = None if residual is None else _new_like(x, x.dtype, stream)
+    rstd = _new(x.shape[:-1], torch.float32, x, stream)
+    rc = lib.dion_rmsnorm(x.data_ptr(), ldx, _ptr(residual), ldr, weight.data_ptr(), _ptr(h), cols, y.data_ptr(), cols,
+                          rstd.data_ptr(), rows, cols, code, wcode, eps, _handle(stream, dev))
+    if rc:
+        check(rc)
+    _used(stream, x, weight, residual)
     return y, (x if h is None else h), rstd
 
 
@@ -143,14 +176,15 @@ def rmsnorm_int8(x, weight, residual=None, eps=1e-6, stream=None):
 
     ``scale`` (fp32, one for each row) is the row's largest |y| over 127; a row
     that holds an infinity or a NaN has scale NaN."""
-    rows, cols, ldx, ldr, code, wcode = _norm_inputs(x, weight, residual)
-    s = _Stream(stream)
-    q = s.empty(x.shape, torch.int8, x)
-    h = None if residual is None else s.empty(x.shape, x.dtype, x)
-    scale = s.empty(x.shape[:-1], torch.float32, x)
-    check(lib.dion_rmsnorm_int8(x.data_ptr(), ldx, _ptr(residual), ldr, weight.data_ptr(), _ptr(h), cols,
-                                q.data_ptr(), cols, scale.data_ptr(), rows, cols, code, wcode, eps, s.handle))
-    s.used(x, weight, residual)
+    dev, rows, cols, ldx, ldr, code, wcode = _norm_inputs(x, weight, residual)
+    q = _new_like(x, torch.int8, stream)
+    h = None if residual is None else _new_like(x, x.dtype, stream)
+    scale = _new(x.shape[:-1], torch.float32, x, stream)
+    rc = lib.dion_rmsnorm_int8(x.data_ptr(), ldx, _ptr(residual), ldr, weight.data_ptr(), _ptr(h), cols, q.data_ptr(),
+                               cols, scale.data_ptr(), rows, cols, code, wcode, eps, _handle(stream, dev))
+    if rc:
+        check(rc)
+    _used(stream, x, weight, residual)
     return q, scale, (x if h is None else h)
 
 
@@ -159,20 +193,22 @@ def rmsnorm_backward(dy, h, weight, rstd, dh=None, workspace=None, stream=None):
 
     ``dh`` is the gradient that reaches h itself along the residual stream; dx
     is the gradient of x and of the residual alike."""
+    dev = _device(h, "h")
     rows, cols, ldh = _matrix(h, "h")
     code = _code(h.dtype, "h")
-    lddy = _same(dy, "dy", h.shape, h.dtype)
-    lddh = 0 if dh is None else _same(dh, "dh", h.shape, h.dtype)
-    _vector(weight, "weight", cols, (h.dtype, torch.float32))
-    _vector(rstd, "rstd", rows, (torch.float32,))
-    s = _Stream(stream)
-    keep, ws, have = s.workspace(lib.dion_rmsnorm_backward_workspace_size(rows, cols, code), h, workspace)
-    dx = s.empty(h.shape, h.dtype, h)
-    dw = s.empty(weight.shape, weight.dtype, h)
-    check(lib.dion_rmsnorm_backward(dy.data_ptr(), lddy, h.data_ptr(), ldh, weight.data_ptr(), rstd.data_ptr(),
-                                    _ptr(dh), lddh, dx.data_ptr(), cols, dw.data_ptr(), rows, cols, code,
-                                    _CODE[weight.dtype], ws, have, s.handle))
-    s.used(dy, h, weight, rstd, dh, keep)
+    lddy = _same(dy, "dy", h, dev)
+    lddh = 0 if dh is None else _same(dh, "dh", h, dev)
+    _vector(weight, "weight", cols, (h.dtype, torch.float32), dev)
+    _vector(rstd, "rstd", rows, _F32, dev)
+    keep, ws, have = _workspace(lib.dion_rmsnorm_backward_workspace_size(rows, cols, code), h, workspace, stream)
+    dx = _new_like(h, h.dtype, stream)
+    dw = _new_like(weight, weight.dtype, stream)
+    rc = lib.dion_rmsnorm_backward(dy.data_ptr(), lddy, h.data_ptr(), ldh, weight.data_ptr(), rstd.data_ptr(),
+                                   _ptr(dh), lddh, dx.data_ptr(), cols, dw.data_ptr(), rows, cols, code,
+                                   _CODE[weight.dtype], ws, have, _handle(stream, dev))
+    if rc:
+        check(rc)
+    _used(stream, dy, h, weight, rstd, dh, keep)
     return dx, dw
 
 
@@ -180,83 +216,97 @@ def rmsnorm_backward(dy, h, weight, rstd, dh=None, workspace=None, stream=None):
 def int8_quantize(x, stream=None):
     """8-bit codes of the rows of x: returns (q, scale), x = q * scale up to rounding.
     (The weights of a product, once; activations that no norm wrote.)"""
+    dev = _device(x, "x")
     rows, cols, ldx = _matrix(x, "x")
     code = _code(x.dtype, "x")
-    s = _Stream(stream)
-    q = s.empty(x.shape, torch.int8, x)
-    scale = s.empty(x.shape[:-1], torch.float32, x)
-    check(lib.dion_int8_quantize(x.data_ptr(), ldx, q.data_ptr(), cols, scale.data_ptr(), rows, cols, code, s.handle))
-    s.used(x)
+    q = _new_like(x, torch.int8, stream)
+    scale = _new(x.shape[:-1], torch.float32, x, stream)
+    rc = lib.dion_int8_quantize(x.data_ptr(), ldx, q.data_ptr(), cols, scale.data_ptr(), rows, cols, code,
+                                _handle(stream, dev))
+    if rc:
+        check(rc)
+    _used(stream, x)
     return q, scale
 
 
 def int8_dequantize(q, scale, dtype=torch.bfloat16, stream=None):
     """The values that 8-bit codes with a scale for each row stand for."""
+    dev = _device(q, "q")
     rows, cols, ldq = _matrix(q, "q")
     if q.dtype != torch.int8:
         _fail(f"q: expected torch.int8, got {q.dtype}")
-    _vector(scale, "scale", rows, (torch.float32,))
+    _vector(scale, "scale", rows, _F32, dev)
     code = _code(dtype, "dtype")
-    s = _Stream(stream)
-    y = s.empty(q.shape, dtype, q)
-    check(lib.dion_int8_dequantize(q.data_ptr(), ldq, scale.data_ptr(), y.data_ptr(), cols, rows, cols, code,
-                                   s.handle))
-    s.used(q, scale)
+    y = _new_like(q, dtype, stream)
+    rc = lib.dion_int8_dequantize(q.data_ptr(), ldq, scale.data_ptr(), y.data_ptr(), cols, rows, cols, code,
+                                  _handle(stream, dev))
+    if rc:
+        check(rc)
+    _used(stream, q, scale)
     return y
 
 
 def int8_linear(a, a_scale, b, b_scale, bias=None, out_dtype=torch.bfloat16, workspace=None, stream=None):
     """a (tokens x k) times b (channels x k) transposed, both int8, with a scale
     for each token and channel and an optional bias; the sum is exact."""
+    dev = _device(a, "a")
+    _beside(b, "b", dev)
     m, k, lda = _matrix(a, "a")
     n, kb, ldb = _matrix(b, "b")
     if a.dtype != torch.int8 or b.dtype != torch.int8:
         _fail(f"a and b must be int8, got {a.dtype} and {b.dtype}")
     if b.dim() != 2 or kb != k:
         _fail(f"b: shape {tuple(b.shape)}, expected (channels, {k})")
-    _vector(a_scale, "a_scale", m, (torch.float32,))
-    _vector(b_scale, "b_scale", n, (torch.float32,))
+    _vector(a_scale, "a_scale", m, _F32, dev)
+    _vector(b_scale, "b_scale", n, _F32, dev)
     code = _code(out_dtype, "out_dtype")
     if bias is not None:
-        _vector(bias, "bias", n, _CODE)
-    s = _Stream(stream)
-    keep, ws, have = s.workspace(lib.dion_int8_linear_workspace_size(m, n, k), a, workspace)
-    out = s.empty((*a.shape[:-1], n), out_dtype, a)
-    check(lib.dion_int8_linear(a.data_ptr(), lda, a_scale.data_ptr(), b.data_ptr(), ldb, b_scale.data_ptr(),
-                               _ptr(bias), 0 if bias is None else _CODE[bias.dtype], out.data_ptr(), n, m, n, k, code,
-                               ws, have, s.handle))
-    s.used(a, a_scale, b, b_scale, bias, keep)
+        _vector(bias, "bias", n, _CODE, dev)
+    need = lib.dion_int8_linear_workspace_size(m, n, k)
+    if need <= 256 and workspace is None:   # these sizes use none
+        keep, ws, have = None, None, 0
+    else:
+        keep, ws, have = _workspace(need, a, workspace, stream)
+    out = _new((*a.shape[:-1], n), out_dtype, a, stream)
+    rc = lib.dion_int8_linear(a.data_ptr(), lda, a_scale.data_ptr(), b.data_ptr(), ldb, b_scale.data_ptr(),
+                              _ptr(bias), 0 if bias is None else _CODE[bias.dtype], out.data_ptr(), n, m, n, k, code,
+                              ws, have, _handle(stream, dev))
+    if rc:
+        check(rc)
+    _used(stream, a, a_scale, b, b_scale, bias, keep)
     return out
 
 
 # ---------------------------------------------------------------- distillation
 def _distill_inputs(logits, teacher, teacher_idx):
+    dev = _device(logits, "logits")
     rows, vocab, ldz = _matrix(logits, "logits")
     code = _code(logits.dtype, "logits")
-    if teacher.dim() == 0 or teacher.shape != teacher_idx.shape or teacher.shape[:-1] != logits.shape[:-1]:
-        _fail(f"teacher logits {tuple(teacher.shape)} and indices {tuple(teacher_idx.shape)} must be one row of "
+    _beside(teacher, "teacher logits", dev)
+    _beside(teacher_idx, "teacher indices", dev)
+    shape = teacher.shape
+    if len(shape) == 0 or shape != teacher_idx.shape or shape[:-1] != logits.shape[:-1]:
+        _fail(f"teacher logits {tuple(shape)} and indices {tuple(teacher_idx.shape)} must be one row of "
               f"entries for each row of logits {tuple(logits.shape)}")
-    _gpu(teacher, "teacher logits")
-    _gpu(teacher_idx, "teacher indices")
     tcode = _code(teacher.dtype, "teacher logits")
     if teacher_idx.dtype not in (torch.int64, torch.int32):
         _fail(f"teacher indices: unsupported dtype {teacher_idx.dtype}")
-    return (rows, vocab, ldz, code, teacher.contiguous(), tcode, teacher_idx.contiguous(),
-            teacher_idx.element_size(), teacher.shape[-1])
+    return (dev, rows, vocab, ldz, code, teacher.contiguous(), tcode, teacher_idx.contiguous(),
+            teacher_idx.element_size(), shape[-1])
 
 
-def _gradient(s, logits, rows, vocab, out):
+def _gradient(logits, rows, vocab, out, stream, dev):
     """The gradient's tensor and row stride: new rows start at multiples of 16
     bytes, so that they are written in whole 16-byte pieces whatever the vocabulary."""
     if out is None:
         per = 16 // logits.element_size()
         wide = (vocab + per - 1) // per * per
-        out = s.empty((*logits.shape[:-1], wide), logits.dtype, logits)[..., :vocab]
-        return out, (wide if rows > 1 else vocab)
-    return out, _same(out, "out", logits.shape, logits.dtype)
+        out = _new((*logits.shape[:-1], wide), logits.dtype, logits, stream)
+        return (out if wide == vocab else out[..., :vocab]), (wide if rows > 1 else vocab)
+    return out, _same(out, "out", logits, dev)
 
 
-def distill_topk(logits, teacher, teacher_idx, temperature=1.0, workspace=None, stream=None):
+def distill_topk(logits, teacher, teacher_idx, temperature=1.0, stream=None):
     """Loss of each row against a teacher's top logits: returns (loss, stats).
 
     ``logits``: rows x vocab; ``teacher`` and ``teacher_idx`` (int64 or int32):
@@ -264,49 +314,49 @@ def distill_topk(logits, teacher, teacher_idx, temperature=1.0, workspace=None, 
     entries and q that of logits / T over the vocabulary; entries with an index
     outside the vocabulary or a logit of -inf are absent, and a row without any
     has loss and gradient 0.  ``stats`` is for ``distill_topk_backward``."""
-    rows, vocab, ldz, code, t, tcode, idx, ib, k = _distill_inputs(logits, teacher, teacher_idx)
-    s = _Stream(stream)
-    keep, ws, have = s.workspace(lib.dion_distill_topk_workspace_size(rows, vocab), logits, workspace)
-    loss = s.empty(logits.shape[:-1], torch.float32, logits)
-    stats = s.empty((*logits.shape[:-1], 2), torch.float32, logits)
-    check(lib.dion_distill_topk(logits.data_ptr(), ldz, t.data_ptr(), idx.data_ptr(), loss.data_ptr(),
-                                stats.data_ptr(), rows, vocab, k, code, tcode, ib, temperature, ws, have, s.handle))
-    s.used(logits, t, idx, keep)
+    dev, rows, vocab, ldz, code, t, tcode, idx, ib, k = _distill_inputs(logits, teacher, teacher_idx)
+    loss = _new(logits.shape[:-1], torch.float32, logits, stream)
+    stats = _new((*logits.shape[:-1], 2), torch.float32, logits, stream)
+    rc = lib.dion_distill_topk(logits.data_ptr(), ldz, t.data_ptr(), idx.data_ptr(), loss.data_ptr(), stats.data_ptr(),
+                               rows, vocab, k, code, tcode, ib, temperature, _handle(stream, dev))
+    if rc:
+        check(rc)
+    _used(stream, logits, t, idx)
     return loss, stats
 
 
 def distill_topk_backward(grad_loss, logits, stats, teacher, teacher_idx, temperature=1.0, out=None, stream=None):
     """Gradient of the logits from ``distill_topk``'s stats and the gradient of
     each row's loss (None: 1).  ``out`` may be the logits themselves."""
-    rows, vocab, ldz, code, t, tcode, idx, ib, k = _distill_inputs(logits, teacher, teacher_idx)
+    dev, rows, vocab, ldz, code, t, tcode, idx, ib, k = _distill_inputs(logits, teacher, teacher_idx)
     if grad_loss is not None:
-        _vector(grad_loss, "grad_loss", rows, (torch.float32,))
-    _vector(stats, "stats", 2 * rows, (torch.float32,))
-    s = _Stream(stream)
-    out, ldd = _gradient(s, logits, rows, vocab, out)
-    check(lib.dion_distill_topk_backward(_ptr(grad_loss), logits.data_ptr(), ldz, stats.data_ptr(), t.data_ptr(),
-                                         idx.data_ptr(), out.data_ptr(), ldd, rows, vocab, k, code, tcode, ib,
-                                         temperature, s.handle))
-    s.used(grad_loss, logits, stats, t, idx, out)
+        _vector(grad_loss, "grad_loss", rows, _F32, dev)
+    _vector(stats, "stats", 2 * rows, _F32, dev)
+    out, ldd = _gradient(logits, rows, vocab, out, stream, dev)
+    rc = lib.dion_distill_topk_backward(_ptr(grad_loss), logits.data_ptr(), ldz, stats.data_ptr(), t.data_ptr(),
+                                        idx.data_ptr(), out.data_ptr(), ldd, rows, vocab, k, code, tcode, ib,
+                                        temperature, _handle(stream, dev))
+    if rc:
+        check(rc)
+    _used(stream, grad_loss, logits, stats, t, idx, out)
     return out
 
 
-def distill_topk_step(logits, teacher, teacher_idx, grad_loss=None, temperature=1.0, out=None, workspace=None,
-                      stream=None):
+def distill_topk_step(logits, teacher, teacher_idx, grad_loss=None, temperature=1.0, out=None, stream=None):
     """Loss and gradient in one call, for a ``grad_loss`` known ahead (such as
     one over the number of tokens; None: 1): returns (loss, dlogits).
     ``out`` may be the logits themselves."""
-    rows, vocab, ldz, code, t, tcode, idx, ib, k = _distill_inputs(logits, teacher, teacher_idx)
+    dev, rows, vocab, ldz, code, t, tcode, idx, ib, k = _distill_inputs(logits, teacher, teacher_idx)
     if grad_loss is not None:
-        _vector(grad_loss, "grad_loss", rows, (torch.float32,))
-    s = _Stream(stream)
-    keep, ws, have = s.workspace(lib.dion_distill_topk_workspace_size(rows, vocab), logits, workspace)
-    loss = s.empty(logits.shape[:-1], torch.float32, logits)
-    out, ldd = _gradient(s, logits, rows, vocab, out)
-    check(lib.dion_distill_topk_step(logits.data_ptr(), ldz, t.data_ptr(), idx.data_ptr(), _ptr(grad_loss),
-                                     loss.data_ptr(), out.data_ptr(), ldd, rows, vocab, k, code, tcode, ib,
-                                     temperature, ws, have, s.handle))
-    s.used(logits, t, idx, grad_loss, out, keep)
+        _vector(grad_loss, "grad_loss", rows, _F32, dev)
+    loss = _new(logits.shape[:-1], torch.float32, logits, stream)
+    out, ldd = _gradient(logits, rows, vocab, out, stream, dev)
+    rc = lib.dion_distill_topk_step(logits.data_ptr(), ldz, t.data_ptr(), idx.data_ptr(), _ptr(grad_loss),
+                                    loss.data_ptr(), out.data_ptr(), ldd, rows, vocab, k, code, tcode, ib, temperature,
+                                    _handle(stream, dev))
+    if rc:
+        check(rc)
+    _used(stream, logits, t, idx, grad_loss, out)
     return loss, out
 
 
