@@ -437,8 +437,12 @@ int dion_rmsnorm_backward(const void* dy, int64_t lddy, const void* h, int64_t l
  * a: m x k activations, b: n x k weights (output channels as rows), both any
  * int8 values; the sum is exact in 32 bits, k < 2^17 (DION_E_UNSUPPORTED
  * above).  bias: n values of bias_dtype, or NULL.  out: m x n of out_dtype.
- * Sizes whose workspace size is 256 use none: it may be NULL. */
-size_t dion_int8_linear_workspace_size(int64_t m, int64_t n, int32_t k);
+ * The workspace holds the sums of splits of k, and copies of a or b where
+ * their rows do not start at multiples of 16 bytes (a k that is not a multiple
+ * of 16, an unaligned pointer or stride) and m > 16; its size depends on the
+ * pointers' alignment.  Products whose size is 256 use none: it may be NULL. */
+size_t dion_int8_linear_workspace_size(const int8_t* a, int64_t lda, const int8_t* b, int64_t ldb, int64_t m,
+                                       int64_t n, int32_t k);
 int dion_int8_linear(const int8_t* a, int64_t lda, const float* a_scale, const int8_t* b, int64_t ldb,
                      const float* b_scale, const void* bias, int32_t bias_dtype, void* out, int64_t ldo, int64_t m,
                      int64_t n, int32_t k, int32_t out_dtype, void* workspace, size_t workspace_bytes, void* stream);

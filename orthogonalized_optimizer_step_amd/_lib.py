@@ -140,7 +140,7 @@ def _load():
     lib.dion_rmsnorm_backward_workspace_size.restype = sz
     lib.dion_rmsnorm_backward.argtypes = mat + mat + [vp, vp] + mat + mat + [vp, i64, i32, i32, i32, vp, sz, vp]
     lib.dion_rmsnorm_backward.restype = ctypes.c_int
-    lib.dion_int8_linear_workspace_size.argtypes = [i64, i64, i32]
+    lib.dion_int8_linear_workspace_size.argtypes = mat + mat + [i64, i64, i32]
     lib.dion_int8_linear_workspace_size.restype = sz
     lib.dion_int8_linear.argtypes = mat + [vp] + mat + [vp, vp, i32] + mat + [i64, i64, i32, i32, vp, sz, vp]
     lib.dion_int8_linear.restype = ctypes.c_int

@@ -88,12 +88,11 @@ __device__ __forceinline__ void tile_of_block(int TM, int TN, int& ti, int& tj) 
 }
 
 // One BM x BN tile of the output by WM x WN waves, S stages of BK bytes in
-// LDS.  DMA: the stages are copied straight into LDS S - 1 stages ahead (rows
-// at multiples of 16 bytes); otherwise they pass through registers (any
-// alignment).  Each wave holds two sets of fragments: those of the next 32
+// LDS, copied straight there S - 1 stages ahead (a and b in rows at multiples
+// of 16 bytes).  Each wave holds two sets of fragments: those of the next 32
 // bytes are read from LDS while the present ones are multiplied, across the
 // stage's end too.
-template <int BM, int BN, int WM, int WN, int S, bool DMA, typename O>
+template <int BM, int BN, int WM, int WN, int S, typename O>
 __global__ __launch_bounds__(64 * WM * WN) void k_int8_mma(Int8Args g, int* partial) {
   constexpr int W = WM * WN, NT = 64 * W;
   constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32;   // wave tile, its fragments
@@ -105,8 +104,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_int8_mma(Int8Args g, int* part
   constexpr int LDS = S * STAGE > STAGED ? S * STAGE : STAGED;
   // Copies of the stage S - 1 ahead: all at once after the turn, or (the
   // largest tile, with one block per CU) spread over the products of two steps.
-  constexpr int KS = BK / 32, AHEAD = DMA ? S - 1 : 1;
-  constexpr bool SPREAD = DMA && BM * BN >= 256 * 256;
+  constexpr int KS = BK / 32;
+  constexpr bool SPREAD = BM * BN >= 256 * 256;
   constexpr int PW = NP / 2, EVERY = SPREAD ? FM * FN / PW : 1;
   static_assert(!SPREAD || (PW * 2 == NP && EVERY * PW == FM * FN), "the copies divide the products");
   static_assert(S <= 4 && NP * W * 1024 == STAGE && BM % PR == 0, "whole pieces");
@@ -130,7 +129,6 @@ __global__ __launch_bounds__(64 * WM * WN) void k_int8_mma(Int8Args g, int* part
   uint32_t voff[NP];
   int vk[NP];
   const intx4 ra = raw_buffer(A, (uint32_t)((rm - 1) * g.lda + g.k)), rb = raw_buffer(B, (uint32_t)((rn - 1) * g.ldb + g.k));
-  intx4 reg[NP];
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
     const int q = wave + i * W;
@@ -139,22 +137,11 @@ __global__ __launch_bounds__(64 * WM * WN) void k_int8_mma(Int8Args g, int* part
     vk[i] = swz(r, lane % CR) * 16;
     voff[i] = r < (isa ? rm : rn) ? (uint32_t)(r * (isa ? g.lda : g.ldb)) + vk[i] : OUT_OF_RANGE;
   }
-  // piece i of stage kt: into LDS, or into registers
-  auto issue = [&](int kt, int i) {
+  auto issue = [&](int kt, int i) {   // piece i of stage kt
     const int k0 = (kt0 + kt) * BK, q = wave + i * W;
-    const bool isa = q < BM / PR;
-    if (DMA) {
-      const uint32_t v = k0 + vk[i] < g.k ? voff[i] : OUT_OF_RANGE;
-      dma16(v, isa ? ra : rb, (uint32_t)k0,
-            (uint32_t)__builtin_amdgcn_readfirstlane(lds0 + (kt % S) * STAGE + q * 1024));
-    } else {
-      const int8_t* p = (isa ? A : B) + (int64_t)((isa ? q : q - BM / PR) * PR + lane / CR) * (isa ? g.lda : g.ldb);
-      reg[i] = voff[i] != OUT_OF_RANGE ? load_chunk(p, k0 + vk[i], g.k) : intx4{0, 0, 0, 0};
-    }
-  };
-  auto store = [&](int kt) {   // registers to LDS
-#pragma unroll
-    for (int i = 0; i < NP; ++i) *(intx4*)(smem + (kt % S) * STAGE + (wave + i * W) * 1024 + lane * 16) = reg[i];
+    const uint32_t v = k0 + vk[i] < g.k ? voff[i] : OUT_OF_RANGE;
+    dma16(v, q < BM / PR ? ra : rb, (uint32_t)k0,
+          (uint32_t)__builtin_amdgcn_readfirstlane(lds0 + (kt % S) * STAGE + q * 1024));
   };
 
   intx16 acc[FM][FN] = {};
@@ -169,32 +156,23 @@ __global__ __launch_bounds__(64 * WM * WN) void k_int8_mma(Int8Args g, int* part
   };
   // the stage that is needed next has landed, and every wave is done with the one before it
   auto turn = [&](int kt) {
-    if (DMA) {
-      const int later = min(nk - 1, kt + S - 2) - kt;   // stages issued after kt
-      if (S >= 4 && later >= 2) wait_vmcnt<2 * NP>();
-      else if (S >= 3 && later >= 1) wait_vmcnt<NP>();
-      else wait_vmcnt<0>();
-    } else {
-      store(kt);
-    }
+    const int later = min(nk - 1, kt + S - 2) - kt;   // stages issued after kt
+    if (S >= 4 && later >= 2) wait_vmcnt<2 * NP>();
+    else if (S >= 3 && later >= 1) wait_vmcnt<NP>();
+    else wait_vmcnt<0>();
     lds_barrier();
-    if (!SPREAD && kt + AHEAD < nk) {
+    if (!SPREAD && kt + S - 1 < nk) {
 #pragma unroll
-      for (int i = 0; i < NP; ++i) issue(kt + AHEAD, i);
+      for (int i = 0; i < NP; ++i) issue(kt + S - 1, i);
     }
   };
   if (nk > 0) {
-    if (DMA) {
 #pragma unroll
-      for (int t = 0; t < S - 1; ++t)
-        if (t < nk) {
+    for (int t = 0; t < S - 1; ++t)
+      if (t < nk) {
 #pragma unroll
-          for (int i = 0; i < NP; ++i) issue(t, i);
-        }
-    } else {
-#pragma unroll
-      for (int i = 0; i < NP; ++i) issue(0, i);
-    }
+        for (int i = 0; i < NP; ++i) issue(t, i);
+      }
     turn(0);
     if (SPREAD && S - 1 < nk) {
 #pragma unroll
@@ -211,8 +189,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_int8_mma(Int8Args g, int* part
           fetch(kt + 1, 0, 0);
         }
         __builtin_amdgcn_sched_barrier(0);   // the reads above go out before the products, not beside their use
-        // the copies of step ks, one after every EVERY products: half of a
-        // stage's right after its turn, half beside the next step's products
+        // spread copies, one after every EVERY products: half of a stage's
+        // right after its turn, half beside the next step's products
         const int w = (ks + 1) % KS, st = ks + 1 < KS ? kt + S - 1 : kt + S;
 #pragma unroll
         for (int i = 0; i < FM; ++i)
@@ -310,14 +288,14 @@ void launch_join(const Int8Args& a, int splits, hipStream_t s) {
   else hipLaunchKernelGGL((k_int8_join<fp16_t>), grid, dim3(256), 0, s, a, a.partial, splits);
 }
 
-template <int BM, int BN, int WM, int WN, int S, bool DMA>
+template <int BM, int BN, int WM, int WN, int S>
 void launch_mma(const Int8Args& a, int splits, hipStream_t s) {
   const int64_t tiles = (a.m + BM - 1) / BM * ((a.n + BN - 1) / BN);
   const dim3 grid((unsigned)tiles, splits), block(64 * WM * WN);
   int* part = splits > 1 ? a.partial : nullptr;
-  if (a.out_fmt == 1) hipLaunchKernelGGL((k_int8_mma<BM, BN, WM, WN, S, DMA, float>), grid, block, 0, s, a, part);
-  else if (a.out_fmt == 0) hipLaunchKernelGGL((k_int8_mma<BM, BN, WM, WN, S, DMA, bf16_t>), grid, block, 0, s, a, part);
-  else hipLaunchKernelGGL((k_int8_mma<BM, BN, WM, WN, S, DMA, fp16_t>), grid, block, 0, s, a, part);
+  if (a.out_fmt == 1) hipLaunchKernelGGL((k_int8_mma<BM, BN, WM, WN, S, float>), grid, block, 0, s, a, part);
+  else if (a.out_fmt == 0) hipLaunchKernelGGL((k_int8_mma<BM, BN, WM, WN, S, bf16_t>), grid, block, 0, s, a, part);
+  else hipLaunchKernelGGL((k_int8_mma<BM, BN, WM, WN, S, fp16_t>), grid, block, 0, s, a, part);
   if (part) launch_join(a, splits, s);
 }
 
@@ -379,71 +357,120 @@ void launch_rows(const Int8Args& a, int splits, hipStream_t s) {
   if (part) launch_join(a, splits, s);
 }
 
-}  // namespace
+// Rows of a and b at multiples of 16 bytes, zeros past k: 16 bytes a thread.
+__global__ __launch_bounds__(256) void k_int8_align(Int8Args g, int8_t* a, int8_t* b, int pitch) {
+  const int per = pitch / 16;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, na = a ? g.m * per : 0, nb = b ? g.n * per : 0;
+  if (i < na) {
+    const int64_t r = i / per;
+    const int c = (int)(i % per) * 16;
+    *(intx4*)(a + r * pitch + c) = load_chunk(g.a + r * g.lda, c, g.k);
+  } else if (i < na + nb) {
+    const int64_t r = (i - na) / per;
+    const int c = (int)((i - na) % per) * 16;
+    *(intx4*)(b + r * pitch + c) = load_chunk(g.b + r * g.ldb, c, g.k);
+  }
+}
 
-// Which kernel takes a product, by its sizes alone (us on an MI355X, one
-// bf16 output).
-//  - Up to 16 tokens the rows kernel: its traffic is the weights', read once.
-//    Four channel groups to a block where that leaves most CUs a block (1 x
-//    14336 x 4096: 11.4 against 13.0 with one, and 5.0 TB/s); one where it
-//    would not (1 x 4096 x 4096: 6.2 against 11.2), and k split over blocks
-//    when there are few channels and each wave would have more than seven
-//    pieces of k (8 x 512 x 14336: 7.5 against 12.0).  Beyond 16 tokens its
-//    fragments of a cost more than they save (20 x 14336 x 4096: 20.7 against
-//    the 64 x 64 tile's 13.8).
-//  - Otherwise the tile whose rounds over the 256 CUs are shortest, from the
-//    time of one stage (128 bytes of k) and a tile's fixed cost: 256 x 256 one
-//    block per CU (8192 x 14336 x 4096: 490, 128 x 128: 590), 128 x 128
-//    (2048 x 4096 x 4096: 43, 256 x 256: 54) and 64 x 64 (512 x 4096 x 4096:
-//    18, 128 x 128: 28) two, at about half the time for a block alone.  Fewer
-//    than 128 tiles of 64 split k so that up to 256 blocks run, of eight
-//    stages at least (24 x 4096 x 14336: 14.3 against 35.3).
+// Which kernel takes a product, by its sizes alone (us on an MI355X, bf16
+// output).
+//  - Up to 16 tokens the rows kernel: its traffic is the weights', read once,
+//    at any alignment.  Four channel groups to a block where that leaves most
+//    CUs a block (1 x 14336 x 4096: 11.4 against 13.0 with one, and 5.0 TB/s);
+//    one where it would not (1 x 4096 x 4096: 5.2 against 11.1), and k split
+//    over blocks when there are few channels and each wave would still have
+//    some pieces of k (8 x 512 x 14336: 7.5 against 12.0).  Beyond 16 tokens
+//    its fragments of a cost more than they save (20 x 14336 x 4096: 20.7
+//    against the 64 x 64 tile's 13.8).
+//  - Otherwise the tile and the split of k with the least of the sum of the
+//    rounds over the 256 CUs at a stage's time (128 bytes of k), a tile's
+//    fixed time, and the time of writing and joining the splits' sums.  A
+//    stage takes 1.31 for 256 x 256, one block per CU (8192 x 14336 x 4096:
+//    490, 128 x 128: 590); 1.28 for 128 x 128 two to a CU, 0.70 alone (2048 x
+//    4096 x 4096: 43, 256 x 256: 54); 0.55 and 0.30 for 64 x 64 (512 x 4096 x
+//    4096: 18, 128 x 128: 28).  24 x 4096 x 14336 on 64 x 64: 14.3 in four
+//    splits, 35.3 in one.
 struct Int8Plan {
   enum { ROWS1, ROWS4, TILE64, TILE128, TILE256 } kind;
   int splits;
 };
 
-static Int8Plan int8_plan(int64_t m, int64_t n, int k) {
-  const auto tiles = [&](int64_t t) { return (m + t - 1) / t * ((n + t - 1) / t); };
+Int8Plan int8_plan(int64_t m, int64_t n, int k) {
   const int stages = (k + 127) / 128;
-  const auto split = [&](int64_t blocks, int least) {
-    return (int)std::max<int64_t>(1, std::min<int64_t>(256 / std::max<int64_t>(1, blocks), stages / least));
-  };
   if (m <= 16) {
     if (n >= 64 * 208) return {Int8Plan::ROWS4, 1};
-    return {Int8Plan::ROWS1, split((n + 15) / 16, 28)};
+    const int64_t blocks = (n + 15) / 16;
+    return {Int8Plan::ROWS1, (int)std::max<int64_t>(1, std::min<int64_t>(256 / blocks, stages / 28))};
   }
-  const int64_t t64 = tiles(64), t128 = tiles(128), t256 = tiles(256);
-  const int s64 = split(t64, 8);
-  const double c64 = (t64 * s64 <= 256 ? 0.30 : 0.55 * (double)((t64 * s64 + 511) / 512)) * stages / s64 +
-                     (s64 > 1 ? 5.0 : 3.0);
-  const double c128 = (t128 <= 256 ? 0.70 : 1.28 * (double)((t128 + 511) / 512)) * stages + 5.0;
-  const double c256 = 1.31 * (double)((t256 + 255) / 256) * stages + 9.0;
-  if (c256 <= c128 && c256 <= c64) return {Int8Plan::TILE256, 1};
-  if (c128 <= c64) return {Int8Plan::TILE128, 1};
-  return {Int8Plan::TILE64, s64};
+  const auto tiles = [&](int64_t t) { return (m + t - 1) / t * ((n + t - 1) / t); };
+  Int8Plan best{Int8Plan::TILE64, 1};
+  double least = 1e30;
+  const auto consider = [&](decltype(Int8Plan::TILE64) kind, int64_t t, double alone, double two, double fixed) {
+    for (int s = 1; s <= 16; ++s) {
+      if (s > 1 && stages / s < 4) break;
+      const int64_t blocks = tiles(t) * s;
+      const double round = two > 0 ? (blocks <= 256 ? alone : two * (double)((blocks + 511) / 512))
+                                   : alone * (double)((blocks + 255) / 256);
+      const double us = round * ((stages + s - 1) / s) + fixed + (s > 1 ? 3.0 + 8e-6 * s * (double)m * (double)n / 4.0 : 0.0);
+      if (us < least) {
+        least = us;
+        best = {kind, s};
+      }
+    }
+  };
+  consider(Int8Plan::TILE256, 256, 1.31, 0, 9);
+  consider(Int8Plan::TILE128, 128, 0.70, 1.28, 5);
+  consider(Int8Plan::TILE64, 64, 0.30, 0.55, 3);
+  return best;
 }
 
-size_t int8_linear_scratch(int64_t m, int64_t n, int k) {
-  const int splits = int8_plan(m, n, k).splits;
-  return splits > 1 ? (size_t)splits * m * n * 4 : 0;
+// Scratch of a call: the splits' sums, then aligned copies of what is not
+// aligned (copies straight into LDS need rows at multiples of 16 bytes and
+// 31-bit offsets inside a tile; k padded to whole 16 bytes).
+struct Int8Layout {
+  Int8Plan plan;
+  size_t partial, a, b;   // bytes
+  int pitch;
+};
+
+Int8Layout int8_layout(const Int8Args& g) {
+  Int8Layout l{int8_plan(g.m, g.n, g.k), 0, 0, 0, (g.k + 15) / 16 * 16};
+  const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  if (l.plan.splits > 1) l.partial = up((size_t)l.plan.splits * g.m * g.n * 4);
+  if (l.plan.kind == Int8Plan::ROWS1 || l.plan.kind == Int8Plan::ROWS4 || g.k == 0) return l;
+  const auto bad = [&](const int8_t* p, int64_t ld) {
+    return ((uintptr_t)p | (uint64_t)ld | (uint64_t)g.k) % 16 != 0 || ld >= (1 << 22);
+  };
+  if (bad(g.a, g.lda)) l.a = up((size_t)g.m * l.pitch);
+  if (bad(g.b, g.ldb)) l.b = up((size_t)g.n * l.pitch);
+  return l;
 }
 
-void launch_int8_linear(const Int8Args& a, hipStream_t s) {
-  // copies straight into LDS need rows at multiples of 16 bytes, whole 16-byte
-  // chunks and 31-bit offsets inside a tile
-  const bool dma = ((uintptr_t)a.a | (uintptr_t)a.b | (uint64_t)a.lda | (uint64_t)a.ldb | (uint64_t)a.k) % 16 == 0 &&
-                   a.lda < (1 << 22) && a.ldb < (1 << 22);
-  const Int8Plan p = int8_plan(a.m, a.n, a.k);
-  switch (p.kind) {
-    case Int8Plan::ROWS1: return launch_rows<1, 4>(a, p.splits, s);
-    case Int8Plan::ROWS4: return launch_rows<4, 4>(a, p.splits, s);
-    case Int8Plan::TILE64:
-      return dma ? launch_mma<64, 64, 2, 2, 4, true>(a, p.splits, s) : launch_mma<64, 64, 2, 2, 2, false>(a, p.splits, s);
-    case Int8Plan::TILE128:
-      return dma ? launch_mma<128, 128, 2, 2, 2, true>(a, 1, s) : launch_mma<128, 128, 2, 2, 2, false>(a, 1, s);
-    case Int8Plan::TILE256:
-      return dma ? launch_mma<256, 256, 2, 4, 2, true>(a, 1, s) : launch_mma<128, 128, 2, 2, 2, false>(a, 1, s);
+}  // namespace
+
+size_t int8_linear_scratch(const Int8Args& g) {
+  const Int8Layout l = int8_layout(g);
+  return l.partial + l.a + l.b;
+}
+
+void launch_int8_linear(Int8Args g, hipStream_t s) {
+  const Int8Layout l = int8_layout(g);
+  if (l.a || l.b) {
+    int8_t* a = l.a ? (int8_t*)g.partial + l.partial : nullptr;
+    int8_t* b = l.b ? (int8_t*)g.partial + l.partial + l.a : nullptr;
+    const int64_t chunks = ((a ? g.m : 0) + (b ? g.n : 0)) * (l.pitch / 16);
+    hipLaunchKernelGGL(k_int8_align, dim3((unsigned)((chunks + 255) / 256)), dim3(256), 0, s, g, a, b, l.pitch);
+    if (a) g.a = a, g.lda = l.pitch;
+    if (b) g.b = b, g.ldb = l.pitch;
+    g.k = l.pitch;   // the zeros of at least one of the two factors fill the rest
+    // (k is a multiple of 16 already where only one of them was copied)
+  }
+  switch (l.plan.kind) {
+    case Int8Plan::ROWS1: return launch_rows<1, 16>(g, l.plan.splits, s);
+    case Int8Plan::ROWS4: return launch_rows<4, 4>(g, l.plan.splits, s);
+    case Int8Plan::TILE64: return launch_mma<64, 64, 2, 2, 4>(g, l.plan.splits, s);
+    case Int8Plan::TILE128: return launch_mma<128, 128, 2, 2, 2>(g, l.plan.splits, s);
+    case Int8Plan::TILE256: return launch_mma<256, 256, 2, 4, 2>(g, l.plan.splits, s);
   }
 }
 

@@ -55,6 +55,32 @@ __device__ __forceinline__ void load_weight(const void* w, bool w32, int j, int 
   }
 }
 
+template <typename T> __device__ __forceinline__ void add(const uintx4& v, float* f) {
+  float g[Chunk<T>::N];
+  Chunk<T>::unpack(v, g);
+#pragma unroll
+  for (int e = 0; e < Chunk<T>::N; ++e) f[e] += g[e];
+}
+
+// N codes from element j on
+template <int N> __device__ __forceinline__ void store_codes(int8_t* q, int j, int n, const float* y, float inv) {
+  uint32_t p[N / 4];
+#pragma unroll
+  for (int e = 0; e < N; e += 4) {
+    p[e / 4] = 0;
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+      p[e / 4] |= (uint32_t)(uint8_t)(int8_t)(int)rintf(inv == 0.f ? 0.f : y[e + b] * inv) << (8 * b);
+  }
+  if (j + N <= n) {
+    __builtin_memcpy(q + j, p, N);
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (j + e < n) q[j + e] = (int8_t)(p[e / 4] >> (8 * (e % 4)));
+  }
+}
+
 // Forward.  Without a weight (codes of plain rows) y = s.
 template <typename T, bool INT8, int NT, int CH>
 __global__ __launch_bounds__(block_of(NT)) void k_rmsnorm(NormArgs a, bool w32) {
@@ -68,7 +94,7 @@ __global__ __launch_bounds__(block_of(NT)) void k_rmsnorm(NormArgs a, bool w32) 
     T* h = a.h ? (T*)a.h + row * a.ldh : nullptr;
     float s[CH][N];
     {
-      uintx4 vx[CH], vr[CH];
+      uintx4 vx[CH], vr[CH];   // every load of the row ahead of its use
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
         const int j = (i * NT + t) * N;
@@ -79,18 +105,11 @@ __global__ __launch_bounds__(block_of(NT)) void k_rmsnorm(NormArgs a, bool w32) 
       }
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
-        const int j = (i * NT + t) * N;
-        if (j < a.cols) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) s[i][e] = 0.f;
+        if ((i * NT + t) * N < a.cols) {
           C::unpack(vx[i], s[i]);
-          if (r) {
-            float f[N];
-            C::unpack(vr[i], f);
-#pragma unroll
-            for (int e = 0; e < N; ++e) s[i][e] += f[e];
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < N; ++e) s[i][e] = 0.f;
+          if (r) add<T>(vr[i], s[i]);
         }
       }
     }
@@ -129,24 +148,66 @@ __global__ __launch_bounds__(block_of(NT)) void k_rmsnorm(NormArgs a, bool w32) 
       for (int i = 0; i < CH; ++i) {
         const int j = (i * NT + t) * N;
         if (j >= a.cols) continue;
-        uint32_t p[N / 4];
-#pragma unroll
-        for (int e = 0; e < N; e += 4) {
-          p[e / 4] = 0;
-#pragma unroll
-          for (int b = 0; b < 4; ++b)
-            p[e / 4] |= (uint32_t)(uint8_t)(int8_t)(int)rintf(inv == 0.f ? 0.f : s[i][e + b] * inv) << (8 * b);
-        }
-        if (j + N <= a.cols) {
-          __builtin_memcpy(q + j, p, N);
-        } else {
-#pragma unroll
-          for (int e = 0; e < N; ++e)
-            if (j + e < a.cols) q[j + e] = (int8_t)(p[e / 4] >> (8 * (e % 4)));
-        }
+        store_codes<N>(q, j, a.cols, s[i], inv);
       }
     }
     if (t == 0) a.stat[row] = INT8 ? scale : rstd;
+  }
+}
+
+// Rows too long to be held: read again for each step, from the caches.
+template <typename T, bool INT8>
+__global__ __launch_bounds__(1024) void k_rmsnorm_long(NormArgs a, bool w32) {
+  typedef Chunk<T> C;
+  constexpr int N = C::N;
+  __shared__ float red[16];
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const T* x = (const T*)a.x + row * a.ldx;
+    const T* r = a.residual ? (const T*)a.residual + row * a.ldr : nullptr;
+    T* h = a.h ? (T*)a.h + row * a.ldh : nullptr;
+    auto sum = [&](int j, float* s) {
+      C::unpack(C::load(x, j, a.cols, 0.f), s);
+      if (r) add<T>(C::load(r, j, a.cols, 0.f), s);
+    };
+    float rstd = 1.f;
+    if (a.weight) {
+      float ss = 0.f;
+      for (int j = threadIdx.x * N; j < a.cols; j += 1024 * N) {
+        float s[N];
+        sum(j, s);
+#pragma unroll
+        for (int e = 0; e < N; ++e) ss += s[e] * s[e];
+      }
+      rstd = 1.f / sqrtf(block_sum<1024>(ss, red) / (float)a.cols + a.eps);
+    }
+    auto norm = [&](int j, float* s) {
+      if (!a.weight) return;
+      float w[N];
+      load_weight<T>(a.weight, w32, j, a.cols, w);
+#pragma unroll
+      for (int e = 0; e < N; ++e) s[e] = s[e] * rstd * w[e];
+    };
+    float scale = 0.f, inv = 0.f;
+    if (INT8) {
+      float m = 0.f;
+      for (int j = threadIdx.x * N; j < a.cols; j += 1024 * N) {
+        float s[N];
+        sum(j, s);
+        norm(j, s);
+#pragma unroll
+        for (int e = 0; e < N; ++e) m = max_nan(m, fabsf(s[e]));
+      }
+      row_scale(block_max<1024>(m, red), scale, inv);
+    }
+    for (int j = threadIdx.x * N; j < a.cols; j += 1024 * N) {
+      float s[N];
+      sum(j, s);
+      if (h) C::store_near(h, j, a.cols, s);
+      norm(j, s);
+      if (INT8) store_codes<N>((int8_t*)a.y + row * a.ldy, j, a.cols, s, inv);
+      else C::store_near((T*)a.y + row * a.ldy, j, a.cols, s);
+    }
+    if (threadIdx.x == 0) a.stat[row] = INT8 ? scale : rstd;
   }
 }
 
@@ -355,6 +416,8 @@ void launch_forward(const NormArgs& a, bool w32, hipStream_t s) {
   hipLaunchKernelGGL((k_rmsnorm<T, INT8, NT, CH>), dim3(grid), dim3(block_of(NT)), 0, s, a, w32);
 }
 
+constexpr int kHeldChunks = 2048;   // longest row that is held, in 16-byte chunks
+
 // Threads and chunks of a row: the fewest that hold it.
 template <typename T, bool INT8>
 void launch_norm(const NormArgs& a, bool w32, hipStream_t s) {
@@ -364,11 +427,11 @@ void launch_norm(const NormArgs& a, bool w32, hipStream_t s) {
   else if (chunks <= 256) launch_forward<T, INT8, 64, 4>(a, w32, s);
   else if (chunks <= 512) launch_forward<T, INT8, 256, 2>(a, w32, s);
   else if (chunks <= 1024) launch_forward<T, INT8, 256, 4>(a, w32, s);
-  else if (chunks <= 2048) launch_forward<T, INT8, 512, 4>(a, w32, s);
-  else launch_forward<T, INT8, 1024, sizeof(T) == 4 ? 16 : 8>(a, w32, s);
+  else if (chunks <= kHeldChunks) launch_forward<T, INT8, 512, 4>(a, w32, s);
+  else
+    hipLaunchKernelGGL((k_rmsnorm_long<T, INT8>), dim3((unsigned)std::min<int64_t>(a.rows, 1 << 20)), dim3(1024), 0, s, a,
+                       w32);
 }
-
-constexpr int kHeldChunks = 2048;   // longest row that the backward pass holds, in 16-byte chunks
 
 template <typename T, int NT, int CH>
 void launch_backward(const NormBackArgs& a, bool w32, hipStream_t s) {

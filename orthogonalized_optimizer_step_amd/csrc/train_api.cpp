@@ -219,12 +219,22 @@ int dion_rmsnorm_backward(const void* dy, int64_t lddy, const void* h, int64_t l
   });
 }
 
-size_t dion_int8_linear_workspace_size(int64_t m, int64_t n, int32_t k) {
-  if (m < 0 || n < 0 || k < 0) {
-    (void)guarded([&]() { return set_error(DION_E_INVAL, "m, n and k must not be negative"); });
+size_t dion_int8_linear_workspace_size(const int8_t* a, int64_t lda, const int8_t* b, int64_t ldb, int64_t m,
+                                       int64_t n, int32_t k) {
+  if (m < 0 || n < 0 || k < 0 || k >= (1 << 17) || m > (1 << 22) || n > (1 << 22)) {
+    (void)guarded([&]() { return set_error(DION_E_INVAL, "m, n or k out of range"); });
     return 0;
   }
-  return std::max<size_t>(256, align256(int8_linear_scratch(m, n, k)));
+  if (m == 0 || n == 0) return 256;
+  Int8Args g{};
+  g.a = a;
+  g.b = b;
+  g.lda = lda;
+  g.ldb = ldb;
+  g.m = m;
+  g.n = n;
+  g.k = k;
+  return std::max<size_t>(256, int8_linear_scratch(g));
 }
 
 int dion_int8_linear(const int8_t* a, int64_t lda, const float* a_scale, const int8_t* b, int64_t ldb,
@@ -244,7 +254,7 @@ int dion_int8_linear(const int8_t* a, int64_t lda, const float* a_scale, const i
     for (const View& v : {va, vb, vsa, vsb, vo}) check_view(c, v);
     if (bias) check_view(c, vbias);
     for (const View& in : {va, vb, vsa, vsb, vbias}) check_apart(c, vo, in);
-    const size_t need = dion_int8_linear_workspace_size(m, n, k);
+    const size_t need = dion_int8_linear_workspace_size(a, lda, b, ldb, m, n, k);
     if (need > 256) {   // 256: none is used
       check_workspace(c, workspace, workspace_bytes, need);
       const View vws{workspace, (int64_t)workspace_bytes, 1, (int64_t)workspace_bytes, 1, "workspace"};

@@ -58,7 +58,7 @@ struct Int8Args {
   int64_t m, n;
   int k;
   int bias_fmt, out_fmt;
-  int* partial;           // splits x m x n sums, where the plan splits k
+  int* partial;           // scratch: splits x m x n sums, then aligned copies
 };
 
 struct DistillArgs {
@@ -86,9 +86,10 @@ void launch_rmsnorm(int fmt, int wfmt, bool int8_out, const NormArgs& a, hipStre
 void launch_int8_dequantize(int fmt, const int8_t* q, int64_t ldq, const float* scale, void* y, int64_t ldy,
                             int64_t rows, int cols, hipStream_t s);
 void launch_rmsnorm_backward(int fmt, int wfmt, const NormBackArgs& a, hipStream_t s);
-// bytes of Int8Args::partial that the plan for these sizes needs
-size_t int8_linear_scratch(int64_t m, int64_t n, int k);
-void launch_int8_linear(const Int8Args& a, hipStream_t s);
+// bytes of Int8Args::partial that this product needs (its sizes, strides and
+// the alignment of a and b)
+size_t int8_linear_scratch(const Int8Args& a);
+void launch_int8_linear(Int8Args a, hipStream_t s);
 void launch_distill_forward(int fmt, const DistillArgs& a, hipStream_t s);
 void launch_distill_backward(int fmt, const DistillArgs& a, hipStream_t s);
 void launch_distill_step(int fmt, const DistillArgs& a, hipStream_t s);

@@ -262,13 +262,14 @@ def int8_linear(a, a_scale, b, b_scale, bias=None, out_dtype=torch.bfloat16, wor
     code = _code(out_dtype, "out_dtype")
     if bias is not None:
         _vector(bias, "bias", n, _CODE, dev)
-    need = lib.dion_int8_linear_workspace_size(m, n, k)
+    pa, pb = a.data_ptr(), b.data_ptr()
+    need = lib.dion_int8_linear_workspace_size(pa, lda, pb, ldb, m, n, k)
     if need <= 256 and workspace is None:   # these sizes use none
         keep, ws, have = None, None, 0
     else:
         keep, ws, have = _workspace(need, a, workspace, stream)
     out = _new((*a.shape[:-1], n), out_dtype, a, stream)
-    rc = lib.dion_int8_linear(a.data_ptr(), lda, a_scale.data_ptr(), b.data_ptr(), ldb, b_scale.data_ptr(),
+    rc = lib.dion_int8_linear(pa, lda, a_scale.data_ptr(), pb, ldb, b_scale.data_ptr(),
                               _ptr(bias), 0 if bias is None else _CODE[bias.dtype], out.data_ptr(), n, m, n, k, code,
                               ws, have, _handle(stream, dev))
     if rc:
