@@ -234,26 +234,34 @@ __global__ __launch_bounds__(64 * WM * WN) void k_int8_mma(Int8Args g, int* part
   O* st = (O*)smem + wave * 32 * SROW;
   const int64_t cbase = n0 + wn * TN;
   constexpr int CPR = TN / OV;   // 16-byte pieces of a staged row
-  const O* outp = (const O*)g.out;
+  // the lane's channels' scales and biases, once for all its rows (past the
+  // last channel the last one's: not written)
+  float sb[FN][16], bias[FN][16];
+#pragma unroll
+  for (int j = 0; j < FN; ++j)
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      const int64_t col = min(cbase + j * 32 + (q >> 2) * 8 + (lane >> 5) * 4 + (q & 3), g.n - 1);
+      sb[j][q] = g.sb[col];
+      bias[j][q] = g.bias ? load_fmt(g.bias, col, g.bias_fmt) : 0.f;
+    }
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
     const int64_t row = m0 + wm * TM + i * 32 + r;
-    const float sa = row < g.m ? g.sa[row] : 0.f;
+    const float sa = g.sa[min(row, g.m - 1)];
 #pragma unroll
     for (int j = 0; j < FN; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int c = j * 32 + q * 8 + (lane >> 5) * 4;
+        typedef O Ox4 __attribute__((ext_vector_type(4)));
+        Ox4 v;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int64_t col = cbase + c + e;
-          float v = 0.f;
-          if (col < g.n) {
-            v = (float)acc[i][j][q * 4 + e] * sa * g.sb[col];
-            if (g.bias) v += load_fmt(g.bias, col, g.bias_fmt);
-          }
-          st[r * SROW + c + e] = from_f<O>(v);
+          float f = (float)acc[i][j][q * 4 + e] * sa * sb[j][q * 4 + e];
+          if (g.bias) f += bias[j][q * 4 + e];
+          v[e] = from_f<O>(f);
         }
+        *(Ox4*)(st + r * SROW + j * 32 + q * 8 + (lane >> 5) * 4) = v;
       }
     asm volatile("" : : : "memory");   // a wave's LDS accesses execute in order
 #pragma unroll
@@ -262,7 +270,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_int8_mma(Int8Args g, int* part
       const int64_t orow = m0 + wm * TM + i * 32 + rr, col = cbase + c;
       if (orow < g.m && col < g.n) {
         const O* s = st + rr * SROW + c;
-        O* o = (O*)outp + orow * g.ldo + col;
+        O* o = (O*)g.out + orow * g.ldo + col;
         if (col + OV <= g.n) *(intx4u*)o = *(const intx4*)s;
         else
           for (int e = 0; col + e < g.n; ++e) o[e] = s[e];
