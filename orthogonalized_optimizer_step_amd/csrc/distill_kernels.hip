@@ -50,23 +50,19 @@ struct Ref {
 
 // Joins sums s relative to references m over a wave.
 __device__ __forceinline__ void wave_join(float& m, float& s, float c) {
-  float mm = m;
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor(mm, o, 64));
+  const float mm = wave_max(m);
   s = wave_sum(s * Ref(mm, c).of(Ref(m, c)));
   m = mm;
 }
 
 // Joins the W values that the waves of a block left in LDS, the same in every lane.
-template <int W> __device__ __forceinline__ float join_sum(float v) {
-#pragma unroll
-  for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-  return v;
+template <int W> __device__ __forceinline__ float join_sum(const float* v) {
+  const int lane = threadIdx.x & 63;
+  return row_reduce<W>(lane < W ? v[lane] : 0.f, 0.f, Add());
 }
-template <int W> __device__ __forceinline__ float join_max(float v) {
-#pragma unroll
-  for (int o = W / 2; o > 0; o >>= 1) v = max_nan(v, __shfl_xor(v, o, 64));
-  return v;
+template <int W> __device__ __forceinline__ float join_max(const float* v) {
+  const int lane = threadIdx.x & 63;
+  return row_reduce<W>(lane < W ? v[lane] : NEG, NEG, MaxNan());
 }
 
 // What the block knows of one row's teacher, in LDS.
@@ -136,11 +132,11 @@ template <typename Z, int NT> struct Row {
       T.ws[wave] = s;
     }
     lds_barrier();
-    top = join_max<W>(T.wt[tid % W]);
+    top = join_max<W>(T.wt);
     if (FWD) {
-      const float wm = T.wm[tid % W];
-      m = join_max<W>(wm);
-      s = join_sum<W>(T.ws[tid % W] * Ref(m, c).of(Ref(wm, c)));
+      m = join_max<W>(T.wm);
+      const int lane = tid & 63;
+      s = row_reduce<W>(lane < W ? T.ws[lane] * Ref(m, c).of(Ref(T.wm[lane], c)) : 0.f, 0.f, Add());
     }
     float es = 0.f;
     const float it = 1.f / a.temp;
@@ -158,7 +154,7 @@ template <typename Z, int NT> struct Row {
     es = wave_sum(es);
     if ((tid & 63) == 0) T.we[wave] = es;
     lds_barrier();
-    es = join_sum<W>(T.we[tid % W]);
+    es = join_sum<W>(T.we);
     const float ls = logf(es);
 #pragma unroll
     for (int i = 0; i < KPT; ++i)
@@ -285,7 +281,7 @@ __global__ __launch_bounds__(NT) void k_distill_rows(DistillArgs a) {
       if ((tid & 63) == 0) T.wl[wave] = part;
     }
     lds_barrier();
-    const float l = FWD ? join_sum<NT / 64>(T.wl[tid % (NT / 64)]) : 0.f;
+    const float l = FWD ? join_sum<NT / 64>(T.wl) : 0.f;
     if (FWD && tid == 0) {
       if (a.loss) a.loss[row] = a.temp * a.temp * l;
       if (a.stats) a.stats[row] = make_float2(R.m, R.s);
@@ -408,7 +404,7 @@ __global__ __launch_bounds__(NT, NT * BLOCKS / 256) void k_distill_step(DistillA
     if ((tid & 63) == 0) T.live[wave] = some;
     lds_barrier();
     const bool live_next = __any(T.live[tid % W]);
-    const float l = live ? join_sum<W>(T.wl[tid % W]) : 0.f;
+    const float l = live ? join_sum<W>(T.wl) : 0.f;
     if (tid == 0) a.loss[row] = a.temp * a.temp * l;
     const Z* zn = live_next ? (const Z*)a.z + next * a.ldz : z;   // without a next row the loads are for nothing
     const Ref r(R.m, c);

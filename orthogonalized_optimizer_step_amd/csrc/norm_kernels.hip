@@ -33,14 +33,11 @@ __device__ __forceinline__ void row_scale(float a, float& scale, float& inv) {
 // Threads of a block: rows of one wave go four to a block.
 constexpr int block_of(int nt) { return nt == 64 ? 256 : nt; }
 
-// Sum or largest over the NT threads of a row.
-template <int NT> __device__ __forceinline__ float row_sum(float v, float* red) {
-  if constexpr (NT == 64) return wave_sum(v);
-  else return block_sum<NT>(v, red);
-}
-template <int NT> __device__ __forceinline__ float row_max(float v, float* red) {
-  if constexpr (NT == 64) return wave_max(v);
-  else return block_max<NT>(v, red);
+// Over the NT threads of a row; `red`: 16 floats, one array for each of two
+// uses in turn.
+template <int NT, typename Op> __device__ __forceinline__ float row_join(float v, float* red, Op op) {
+  if constexpr (NT == 64) return wave_reduce(v, 0.f, op);
+  else return block_reduce<NT>(v, 0.f, red, op);
 }
 
 // N weights from element j on, 0 past the row's end
@@ -62,15 +59,19 @@ template <typename T> __device__ __forceinline__ void add(const uintx4& v, float
   for (int e = 0; e < Chunk<T>::N; ++e) f[e] += g[e];
 }
 
-// N codes from element j on
+// N codes from element j on: rint(y inv).  |y inv| <= 127.5, so that adding
+// 1.5 2^23 rounds it to the integer in the sum's low bits.
 template <int N> __device__ __forceinline__ void store_codes(int8_t* q, int j, int n, const float* y, float inv) {
+#pragma clang fp contract(off)   // the product is rounded first
   uint32_t p[N / 4];
 #pragma unroll
   for (int e = 0; e < N; e += 4) {
-    p[e / 4] = 0;
+    uint32_t u[4];
 #pragma unroll
-    for (int b = 0; b < 4; ++b)
-      p[e / 4] |= (uint32_t)(uint8_t)(int8_t)(int)rintf(inv == 0.f ? 0.f : y[e + b] * inv) << (8 * b);
+    for (int b = 0; b < 4; ++b) u[b] = __float_as_uint(y[e + b] * inv + 12582912.f);
+    p[e / 4] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(u[3], u[2], 0x0c0c0400u),
+                                     __builtin_amdgcn_perm(u[1], u[0], 0x0c0c0400u), 0x05040100u);
+    if (inv == 0.f) p[e / 4] = 0;   // whatever y holds
   }
   if (j + N <= n) {
     __builtin_memcpy(q + j, p, N);
@@ -86,8 +87,9 @@ template <typename T, bool INT8, int NT, int CH>
 __global__ __launch_bounds__(block_of(NT)) void k_rmsnorm(NormArgs a, bool w32) {
   typedef Chunk<T> C;
   constexpr int N = C::N, RPB = block_of(NT) / NT;
-  __shared__ float red[NT / 64];
+  __shared__ float red[3][16];
   const int t = threadIdx.x % NT;
+  int turn = 0;
   for (int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / NT; row < a.rows; row += (int64_t)gridDim.x * RPB) {
     const T* x = (const T*)a.x + row * a.ldx;
     const T* r = a.residual ? (const T*)a.residual + row * a.ldr : nullptr;
@@ -120,7 +122,7 @@ __global__ __launch_bounds__(block_of(NT)) void k_rmsnorm(NormArgs a, bool w32) 
       for (int i = 0; i < CH; ++i)
 #pragma unroll
         for (int e = 0; e < N; ++e) ss += s[i][e] * s[i][e];
-      ss = row_sum<NT>(ss, red);
+      ss = row_join<NT>(ss, red[turn ^= 1], Add());
       rstd = 1.f / sqrtf(ss / (float)a.cols + a.eps);
     }
     float m = 0.f;
@@ -138,11 +140,12 @@ __global__ __launch_bounds__(block_of(NT)) void k_rmsnorm(NormArgs a, bool w32) 
       if (!INT8) C::store_near((T*)a.y + row * a.ldy, j, a.cols, s[i]);
 #pragma unroll
       for (int e = 0; e < N; ++e)
-        if (INT8) m = max_nan(m, fabsf(s[i][e]));
+        if (INT8) m = MaxAbs()(m, s[i][e]);
     }
     float scale = 0.f, inv = 0.f;
     if (INT8) {
-      row_scale(row_max<NT>(m, red), scale, inv);
+      if (NT > 64 && !a.weight) turn ^= 1;   // the only join of the row
+      row_scale(row_join<NT>(m, a.weight ? red[2] : red[turn], MaxAbs()), scale, inv);
       int8_t* q = (int8_t*)a.y + row * a.ldy;
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
@@ -160,7 +163,8 @@ template <typename T, bool INT8>
 __global__ __launch_bounds__(1024) void k_rmsnorm_long(NormArgs a, bool w32) {
   typedef Chunk<T> C;
   constexpr int N = C::N;
-  __shared__ float red[16];
+  __shared__ float red[3][16];
+  int turn = 0;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const T* x = (const T*)a.x + row * a.ldx;
     const T* r = a.residual ? (const T*)a.residual + row * a.ldr : nullptr;
@@ -178,7 +182,7 @@ __global__ __launch_bounds__(1024) void k_rmsnorm_long(NormArgs a, bool w32) {
 #pragma unroll
         for (int e = 0; e < N; ++e) ss += s[e] * s[e];
       }
-      rstd = 1.f / sqrtf(block_sum<1024>(ss, red) / (float)a.cols + a.eps);
+      rstd = 1.f / sqrtf(block_reduce<1024>(ss, 0.f, red[turn ^= 1], Add()) / (float)a.cols + a.eps);
     }
     auto norm = [&](int j, float* s) {
       if (!a.weight) return;
@@ -195,9 +199,10 @@ __global__ __launch_bounds__(1024) void k_rmsnorm_long(NormArgs a, bool w32) {
         sum(j, s);
         norm(j, s);
 #pragma unroll
-        for (int e = 0; e < N; ++e) m = max_nan(m, fabsf(s[e]));
+        for (int e = 0; e < N; ++e) m = MaxAbs()(m, s[e]);
       }
-      row_scale(block_max<1024>(m, red), scale, inv);
+      if (!a.weight) turn ^= 1;   // the only join of the row
+      row_scale(block_reduce<1024>(m, 0.f, a.weight ? red[2] : red[turn], MaxAbs()), scale, inv);
     }
     for (int j = threadIdx.x * N; j < a.cols; j += 1024 * N) {
       float s[N];
@@ -245,7 +250,8 @@ template <typename T, int NT, int CH>
 __global__ __launch_bounds__(block_of(NT)) void k_rmsnorm_backward(NormBackArgs a, bool w32) {
   typedef Chunk<T> C;
   constexpr int N = C::N, RPB = block_of(NT) / NT;
-  __shared__ float red[NT / 64 > 1 ? NT / 64 : 1];
+  __shared__ float red[2][16];
+  int turn = 0;
   __shared__ float joined[RPB > 1 ? RPB * NT * CH * N : 1];
   const int t = threadIdx.x % NT, slot = threadIdx.x / NT;
   float w[CH][N], dw[CH][N];
@@ -291,7 +297,7 @@ __global__ __launch_bounds__(block_of(NT)) void k_rmsnorm_backward(NormBackArgs 
     uintx4 ny[CH], nh[CH], nd[CH];
     float nr = 0.f;
     fetch(row + step, ny, nh, nd, nr);
-    const float c = row_sum<NT>(dot, red) / (float)a.cols * rs * rs;
+    const float c = row_join<NT>(dot, red[turn ^= 1], Add()) / (float)a.cols * rs * rs;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int j = (i * NT + t) * N;
@@ -344,7 +350,8 @@ template <typename T>
 __global__ __launch_bounds__(1024) void k_rmsnorm_dx_long(NormBackArgs a, bool w32) {
   typedef Chunk<T> C;
   constexpr int N = C::N;
-  __shared__ float red[16];
+  __shared__ float red[2][16];
+  int turn = 0;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const T* dy = (const T*)a.dy + row * a.lddy;
     const T* h = (const T*)a.h + row * a.ldh;
@@ -359,7 +366,7 @@ __global__ __launch_bounds__(1024) void k_rmsnorm_dx_long(NormBackArgs a, bool w
 #pragma unroll
       for (int e = 0; e < N; ++e) dot += y[e] * w[e] * v[e];
     }
-    const float c = block_sum<1024>(dot, red) / (float)a.cols * rstd * rstd;
+    const float c = block_reduce<1024>(dot, 0.f, red[turn ^= 1], Add()) / (float)a.cols * rstd * rstd;
     for (int j = threadIdx.x * N; j < a.cols; j += 1024 * N) {
       float y[N], v[N], w[N];
       C::unpack(C::load(dy, j, a.cols, 0.f), y);
@@ -424,10 +431,10 @@ void launch_norm(const NormArgs& a, bool w32, hipStream_t s) {
   const int chunks = (a.cols + Chunk<T>::N - 1) / Chunk<T>::N;
   if (chunks <= 64) launch_forward<T, INT8, 64, 1>(a, w32, s);
   else if (chunks <= 128) launch_forward<T, INT8, 64, 2>(a, w32, s);
-  else if (chunks <= 256) launch_forward<T, INT8, 64, 4>(a, w32, s);
-  else if (chunks <= 512) launch_forward<T, INT8, 256, 2>(a, w32, s);
-  else if (chunks <= 1024) launch_forward<T, INT8, 256, 4>(a, w32, s);
-  else if (chunks <= kHeldChunks) launch_forward<T, INT8, 512, 4>(a, w32, s);
+  else if (chunks <= 256) launch_forward<T, INT8, 256, 1>(a, w32, s);
+  else if (chunks <= 512) launch_forward<T, INT8, 512, 1>(a, w32, s);
+  else if (chunks <= 1024) launch_forward<T, INT8, 1024, 1>(a, w32, s);
+  else if (chunks <= kHeldChunks) launch_forward<T, INT8, 1024, 2>(a, w32, s);
   else
     hipLaunchKernelGGL((k_rmsnorm_long<T, INT8>), dim3((unsigned)std::min<int64_t>(a.rows, 1 << 20)), dim3(1024), 0, s, a,
                        w32);
@@ -444,10 +451,10 @@ void launch_back(const NormBackArgs& a, bool w32, hipStream_t s) {
   if (a.rows > 0) {
     if (chunks <= 64) launch_backward<T, 64, 1>(a, w32, s);
     else if (chunks <= 128) launch_backward<T, 64, 2>(a, w32, s);
-    else if (chunks <= 256) launch_backward<T, 64, 4>(a, w32, s);
-    else if (chunks <= 512) launch_backward<T, 256, 2>(a, w32, s);
-    else if (chunks <= 1024) launch_backward<T, 256, 4>(a, w32, s);
-    else if (chunks <= kHeldChunks) launch_backward<T, 512, 4>(a, w32, s);
+    else if (chunks <= 256) launch_backward<T, 256, 1>(a, w32, s);
+    else if (chunks <= 512) launch_backward<T, 512, 1>(a, w32, s);
+    else if (chunks <= 1024) launch_backward<T, 1024, 1>(a, w32, s);
+    else if (chunks <= kHeldChunks) launch_backward<T, 1024, 2>(a, w32, s);
     else {
       const unsigned gx = (unsigned)((a.cols + 255) / 256);
       // dweight first: dx may be written over dy or dh
@@ -467,8 +474,8 @@ void launch_back(const NormBackArgs& a, bool w32, hipStream_t s) {
 int norm_back_parts(int64_t rows, int cols, int fmt) {
   const int chunks = (cols + (fmt == 1 ? 3 : 7)) / (fmt == 1 ? 4 : 8);
   if (chunks > kHeldChunks) return (int)std::min<int64_t>(256, (rows + 31) / 32);
-  if (chunks <= 256) return (int)std::min<int64_t>(1024, (rows + 3) / 4);
-  return (int)std::min<int64_t>(chunks <= 1024 ? 1024 : 512, rows);
+  if (chunks <= 128) return (int)std::min<int64_t>(1024, (rows + 3) / 4);
+  return (int)std::min<int64_t>(chunks <= 256 ? 1024 : 512, rows);
 }
 
 void launch_rmsnorm(int fmt, int wfmt, bool int8_out, const NormArgs& a, hipStream_t s) {

@@ -94,38 +94,59 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return a != a ? a : (b != b ? b : fmaxf(a, b));
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-  return v;
-}
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v = max_nan(v, __shfl_xor(v, o, 64));
-  return v;
+// v moved across lanes (a data-parallel primitive of the VALU: no LDS round
+// trip), `none` where nothing comes in
+template <int CTRL, int ROWS> __device__ __forceinline__ float lane_move(float none, float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(none), __float_as_int(v), CTRL, ROWS, 0xf, false));
 }
 
-// Sum or largest value over a block of THREADS threads, the same in every
-// thread; `red` holds THREADS / 64 floats and is free for reuse afterwards.
-template <int THREADS> __device__ __forceinline__ float block_sum(float v, float* red) {
-  v = wave_sum(v);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = 0.f;
-#pragma unroll
-  for (int i = 0; i < THREADS / 64; ++i) v += red[i];
-  __syncthreads();
-  return v;
+// op over the 64 lanes of a wave, the same in every lane: within rows of 16
+// lanes (shifts by 1, 2, 4 and 8), then the rows' last lanes into the next.
+template <typename Op> __device__ __forceinline__ float wave_reduce(float v, float none, Op op) {
+  v = op(v, lane_move<0x111, 0xf>(none, v));
+  v = op(v, lane_move<0x112, 0xf>(none, v));
+  v = op(v, lane_move<0x114, 0xf>(none, v));
+  v = op(v, lane_move<0x118, 0xf>(none, v));
+  v = op(v, lane_move<0x142, 0xa>(none, v));
+  v = op(v, lane_move<0x143, 0xc>(none, v));
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
-template <int THREADS> __device__ __forceinline__ float block_max(float v, float* red) {
-  v = wave_max(v);
+// the same over the W <= 16 values that lane l < W holds
+template <int W, typename Op> __device__ __forceinline__ float row_reduce(float v, float none, Op op) {
+  v = op(v, lane_move<0x111, 0xf>(none, v));
+  if (W > 2) v = op(v, lane_move<0x112, 0xf>(none, v));
+  if (W > 4) v = op(v, lane_move<0x114, 0xf>(none, v));
+  if (W > 8) v = op(v, lane_move<0x118, 0xf>(none, v));
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), W - 1));
+}
+
+struct Add {
+  __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+struct MaxNan {
+  __device__ __forceinline__ float operator()(float a, float b) const { return max_nan(a, b); }
+};
+// Largest of magnitudes: as unsigned integers they are in order, with NaN above all.
+struct MaxAbs {
+  __device__ __forceinline__ float operator()(float a, float b) const {
+    return __uint_as_float(max(__float_as_uint(a) & 0x7fffffffu, __float_as_uint(b) & 0x7fffffffu));
+  }
+};
+
+__device__ __forceinline__ float wave_sum(float v) { return wave_reduce(v, 0.f, Add()); }
+__device__ __forceinline__ float wave_max(float v) { return wave_reduce(v, -__builtin_inff(), MaxNan()); }
+
+// op over a block of THREADS threads, the same in every thread.  `red` holds
+// THREADS / 64 floats; it may be written again once every thread has passed
+// another barrier.
+template <int THREADS, typename Op> __device__ __forceinline__ float block_reduce(float v, float none, float* red, Op op) {
+  constexpr int W = THREADS / 64;
+  static_assert(W >= 2 && W <= 16, "a row of lanes holds the waves' values");
+  v = wave_reduce(v, none, op);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = red[0];
-#pragma unroll
-  for (int i = 1; i < THREADS / 64; ++i) v = max_nan(v, red[i]);
-  __syncthreads();
-  return v;
+  lds_barrier();
+  const int lane = threadIdx.x & 63;
+  return row_reduce<W>(lane < W ? red[lane] : none, none, op);
 }
 
 }  // namespace dion
