@@ -464,10 +464,14 @@ int dion_int8_linear(const int8_t* a, int64_t lda, const float* a_scale, const i
  *   grad_loss  rows floats: the gradient that reaches each row's loss; NULL = 1
  *   dlogits    rows x vocab of `dtype`; may be the logits in place
  * dion_distill_topk_step computes the loss and the gradient in one call, for
- * a grad_loss known ahead of it. */
+ * a grad_loss known ahead of it.  The workspace holds parts of a few rows that
+ * are shared out between blocks (gradient: 1 for dion_distill_topk_step, 0
+ * for dion_distill_topk); sizes whose workspace size is 256 use none, and it
+ * may be NULL. */
+size_t dion_distill_topk_workspace_size(int64_t rows, int32_t vocab, int32_t k, int32_t dtype, int32_t gradient);
 int dion_distill_topk(const void* logits, int64_t ldz, const void* teacher, const void* teacher_idx, float* loss,
                       float* stats, int64_t rows, int32_t vocab, int32_t k, int32_t dtype, int32_t teacher_dtype,
-                      int32_t idx_bytes, float temperature, void* stream);
+                      int32_t idx_bytes, float temperature, void* workspace, size_t workspace_bytes, void* stream);
 int dion_distill_topk_backward(const float* grad_loss, const void* logits, int64_t ldz, const float* stats,
                                const void* teacher, const void* teacher_idx, void* dlogits, int64_t ldd, int64_t rows,
                                int32_t vocab, int32_t k, int32_t dtype, int32_t teacher_dtype, int32_t idx_bytes,
@@ -475,7 +479,7 @@ int dion_distill_topk_backward(const float* grad_loss, const void* logits, int64
 int dion_distill_topk_step(const void* logits, int64_t ldz, const void* teacher, const void* teacher_idx,
                            const float* grad_loss, float* loss, void* dlogits, int64_t ldd, int64_t rows,
                            int32_t vocab, int32_t k, int32_t dtype, int32_t teacher_dtype, int32_t idx_bytes,
-                           float temperature, void* stream);
+                           float temperature, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Useful floating-point operations of one dion_orth_batched call on this
  * batch, in the executed formulation, symmetric products counted once:

@@ -47,7 +47,7 @@ EXPORTS = (
     "dion_profile_get_algorithmic",
     "dion_rmsnorm", "dion_rmsnorm_int8", "dion_int8_quantize", "dion_int8_dequantize",
     "dion_rmsnorm_backward_workspace_size", "dion_rmsnorm_backward", "dion_int8_linear_workspace_size",
-    "dion_int8_linear", "dion_distill_topk", "dion_distill_topk_backward",
+    "dion_int8_linear", "dion_distill_topk_workspace_size", "dion_distill_topk", "dion_distill_topk_backward",
     "dion_distill_topk_step",
 )
 
@@ -144,11 +144,13 @@ def _load():
     lib.dion_int8_linear_workspace_size.restype = sz
     lib.dion_int8_linear.argtypes = mat + [vp] + mat + [vp, vp, i32] + mat + [i64, i64, i32, i32, vp, sz, vp]
     lib.dion_int8_linear.restype = ctypes.c_int
-    lib.dion_distill_topk.argtypes = mat + [vp, vp, vp, vp, i64, i32, i32, i32, i32, i32, f32, vp]
+    lib.dion_distill_topk_workspace_size.argtypes = [i64, i32, i32, i32, i32]
+    lib.dion_distill_topk_workspace_size.restype = sz
+    lib.dion_distill_topk.argtypes = mat + [vp, vp, vp, vp, i64, i32, i32, i32, i32, i32, f32, vp, sz, vp]
     lib.dion_distill_topk.restype = ctypes.c_int
     lib.dion_distill_topk_backward.argtypes = [vp] + mat + [vp, vp, vp] + mat + [i64, i32, i32, i32, i32, i32, f32, vp]
     lib.dion_distill_topk_backward.restype = ctypes.c_int
-    lib.dion_distill_topk_step.argtypes = mat + [vp, vp, vp, vp] + mat + [i64, i32, i32, i32, i32, i32, f32, vp]
+    lib.dion_distill_topk_step.argtypes = mat + [vp, vp, vp, vp] + mat + [i64, i32, i32, i32, i32, i32, f32, vp, sz, vp]
     lib.dion_distill_topk_step.restype = ctypes.c_int
     return lib
 

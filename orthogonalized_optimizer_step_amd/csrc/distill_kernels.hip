@@ -212,94 +212,167 @@ __device__ __forceinline__ void write_fixes(const DistillArgs& a, const Teacher<
   }
 }
 
+// The running largest value and sum of elements [lo, hi) of a row, by the
+// block's threads.
+template <typename Z, int NT>
+__device__ __forceinline__ void stream_sum(const Z* z, int lo, int hi, float c, float& m, float& s) {
+  typedef Chunk<Z> C;
+  m = NEG;
+  s = 0.f;
+#pragma unroll 4
+  for (int j = lo + (int)threadIdx.x * C::N; j < hi; j += NT * C::N) {
+    const uintx4 v = C::load(z, j, hi, NEG);
+    float f[C::N];
+    C::unpack(v, f);
+    const float cm = C::largest(m, v);
+    if (cm > m) {
+      s *= Ref(cm, c).of(Ref(m, c));
+      m = cm;
+    }
+    const Ref r(m, c);
+#pragma unroll
+    for (int i = 0; i < C::N; ++i) s += r(f[i]);
+  }
+}
+
+// A few rows over a large vocabulary: one share of a row to a block, its
+// statistics and the logits at the teacher's entries there into scratch, for
+// k_distill_rows.
+template <typename Z, int NT> __global__ __launch_bounds__(NT) void k_distill_part(DistillArgs a) {
+  __shared__ float wm[NT / 64], ws[NT / 64];
+  const float c = LOG2E / a.temp;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int64_t row = blockIdx.x;
+  const int lo = (int)((int64_t)a.vocab * blockIdx.y / a.shares), hi = (int)((int64_t)a.vocab * (blockIdx.y + 1) / a.shares);
+  const Z* z = (const Z*)a.z + row * a.ldz;
+  for (int k = tid; k < a.k; k += NT) {
+    const int64_t at = row * a.k + k;
+    const int64_t j = a.idx64 ? ((const int64_t*)a.idx)[at] : (int64_t)((const int32_t*)a.idx)[at];
+    if (j >= lo && j < hi) a.zi[at] = to_f(z[j]);
+  }
+  float m, s;
+  stream_sum<Z, NT>(z, lo, hi, c, m, s);
+  wave_join(m, s, c);
+  if (lane == 0) {
+    wm[tid >> 6] = m;
+    ws[tid >> 6] = s;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    m = NEG;
+#pragma unroll
+    for (int w = 0; w < NT / 64; ++w) m = fmaxf(m, wm[w]);
+    s = 0.f;
+#pragma unroll
+    for (int w = 0; w < NT / 64; ++w) s += ws[w] * Ref(m, c).of(Ref(wm[w], c));
+    a.parts[row * a.shares + blockIdx.y] = make_float2(m, s);
+  }
+}
+
 // Loss and statistics (FWD), gradient (BWD), or both with the row read a
-// second time while it is still in the caches.  One block a row; backward
-// alone may share a row between gridDim.y blocks.
+// second time while it is still in the caches; without FWD the statistics are
+// given, or (few rows) joined here from the shares' parts, and then the loss
+// is formed too.  A block walks rows gridDim.x apart, fetching the teacher's
+// entries and the logits at them a row ahead; few rows may be shared between
+// gridDim.y blocks each (rows <= gridDim.x then).
 template <typename Z, int NT, bool FWD, bool BWD>
 __global__ __launch_bounds__(NT) void k_distill_rows(DistillArgs a) {
   typedef Chunk<Z> C;
-  __shared__ Teacher<NT> T;
+  constexpr int W = NT / 64, KPT = kDistillMaxK / NT;
+  __shared__ Teacher<NT> both[2];   // rows in turn, so that one may be written while the last is still read
+  int turn = 0;
   const float c = LOG2E / a.temp;
-  const int tid = threadIdx.x, wave = tid >> 6;
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   // this block's columns: whole chunks of all threads
   const int per = (int)(((int64_t)a.vocab + gridDim.y - 1) / gridDim.y + NT * C::N - 1) / (NT * C::N) * (NT * C::N);
   const int lo = min(a.vocab, (int)blockIdx.y * per), hi = min(a.vocab, lo + per);
   if (lo >= hi) return;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+  const bool joins = FWD || a.parts;   // the loss is formed here
+  auto gather = [&](Row<Z, NT>& R, const Entries<NT>& E, int64_t row) {
+    if (a.parts) {
+#pragma unroll
+      for (int i = 0; i < KPT; ++i) R.zi[i] = E.idx[i] >= 0 ? a.zi[row * a.k + tid + i * NT] : 0.f;
+    } else {
+      R.gather(a, E, (const Z*)a.z + row * a.ldz, joins ? 0 : lo, joins ? a.vocab : hi);
+    }
+  };
+  Entries<NT> E, En;
+  Row<Z, NT> R, Rn;
+  int64_t row = blockIdx.x;
+  E.load(a, row);
+  const bool mine = __any(E.any());
+  if (lane == 0) both[1].live[wave] = mine;
+  lds_barrier();
+  bool live = __any(both[1].live[tid % W]);
+  if (!FWD && live) gather(R, E, row);
+  for (; row < a.rows; row += gridDim.x) {
+    Teacher<NT>& T = both[turn];
+    turn ^= 1;
     const Z* z = (const Z*)a.z + row * a.ldz;
     Z* dz = BWD ? (Z*)a.dz + row * a.ldd : nullptr;
-    Entries<NT> E;
-    E.load(a, row);
-    if (row != blockIdx.x) lds_barrier();   // T is free
-    const bool mine = __any(E.any());
-    if ((tid & 63) == 0) T.live[wave] = mine;
-    lds_barrier();
-    const bool live = __any(T.live[tid % (NT / 64)]);
+    const int64_t next = row + gridDim.x;
+    const bool more = next < a.rows;
+    if (more) En.load(a, next);
     const float g = BWD && a.gl ? a.gl[row] : 1.f;
-    if (FWD && !live && tid == 0) {
-      if (a.loss) a.loss[row] = 0.f;
-      if (a.stats) a.stats[row] = make_float2(0.f, 1.f);
+    const float gt = g * a.temp;
+    const bool work = live && (joins || g != 0.f);   // beyond writing zeros
+    if (work) {
+      if (FWD) {
+        gather(R, E, row);   // under way beside the row itself
+        stream_sum<Z, NT>(z, 0, a.vocab, c, R.m, R.s);
+      } else if (a.parts) {
+        const float2 p = lane < a.shares ? a.parts[row * a.shares + lane] : make_float2(NEG, 0.f);
+        R.m = p.x;
+        R.s = p.y;
+        wave_join(R.m, R.s, c);
+      } else {
+        const float2 st = a.stats[row];
+        R.m = st.x;
+        R.s = st.y;
+      }
+      R.template join<FWD>(a, E, T, c);
+      if (BWD) R.fix(a, E, T, c, gt);
+      if (joins) {
+        const float part = wave_sum(R.loss(a, c));
+        if (lane == 0) T.wl[wave] = part;
+      }
     }
-    if (!live || (!FWD && g == 0.f)) {
-      if (BWD) {
+    const bool some = __any(more && En.any());
+    if (lane == 0) T.live[wave] = some;
+    lds_barrier();
+    const bool live_next = __any(T.live[tid % W]);
+    if (joins && blockIdx.y == 0) {
+      const float l = work ? join_sum<W>(T.wl) : 0.f;
+      if (tid == 0) {
+        if (a.loss) a.loss[row] = a.temp * a.temp * l;
+        if (a.stats) a.stats[row] = work ? make_float2(R.m, R.s) : make_float2(0.f, 1.f);
+      }
+    }
+    if (!FWD && live_next) gather(Rn, En, next);
+    if (BWD) {
+      if (!live || g == 0.f) {
         const float zero[C::N] = {};
         for (int j = lo + tid * C::N; j < hi; j += NT * C::N) C::store(dz, j, hi, zero);
-      }
-      continue;
-    }
-    Row<Z, NT> R;
-    R.gather(a, E, z, FWD ? 0 : lo, FWD ? a.vocab : hi);
-    if (FWD) {
-      // running largest value and sum, one rescaling for each 16 bytes
-      float m = NEG, s = 0.f;
+      } else {
+        const float k = gt / R.s;
+        const Ref r(R.m, c);
 #pragma unroll 4
-      for (int j = tid * C::N; j < a.vocab; j += NT * C::N) {
-        const uintx4 v = C::load(z, j, a.vocab, NEG);
-        float f[C::N];
-        C::unpack(v, f);
-        const float cm = C::largest(m, v);
-        if (cm > m) {
-          s *= Ref(cm, c).of(Ref(m, c));
-          m = cm;
+        for (int j = lo + tid * C::N; j < hi; j += NT * C::N) {
+          float f[C::N];
+          C::unpack(C::load(z, j, hi, NEG), f);
+#pragma unroll
+          for (int i = 0; i < C::N; ++i) f[i] = r(f[i]) * k;
+          C::store(dz, j, hi, f);
         }
-        const Ref r(m, c);
-#pragma unroll
-        for (int i = 0; i < C::N; ++i) s += r(f[i]);
+        write_fixes<Z, NT>(a, T, dz, lo, hi);
       }
-      R.m = m;
-      R.s = s;
-    } else {
-      const float2 st = a.stats[row];
-      R.m = st.x;
-      R.s = st.y;
     }
-    R.template join<FWD>(a, E, T, c);
-    const float gt = g * a.temp;
-    if (BWD) R.fix(a, E, T, c, gt);
-    if (FWD) {
-      const float part = wave_sum(R.loss(a, c));
-      if ((tid & 63) == 0) T.wl[wave] = part;
-    }
-    lds_barrier();
-    const float l = FWD ? join_sum<NT / 64>(T.wl) : 0.f;
-    if (FWD && tid == 0) {
-      if (a.loss) a.loss[row] = a.temp * a.temp * l;
-      if (a.stats) a.stats[row] = make_float2(R.m, R.s);
-    }
-    if (BWD) {
-      const float k = gt / R.s;
-      const bool zero = g == 0.f;
-      const Ref r(R.m, c);
-#pragma unroll 4
-      for (int j = lo + tid * C::N; j < hi; j += NT * C::N) {
-        float f[C::N];
-        C::unpack(C::load(z, j, hi, NEG), f);
+    E = En;
+    if (!FWD) {
 #pragma unroll
-        for (int i = 0; i < C::N; ++i) f[i] = zero ? 0.f : r(f[i]) * k;
-        C::store(dz, j, hi, f);
-      }
-      if (!zero) write_fixes<Z, NT>(a, T, dz, lo, hi);
+      for (int i = 0; i < KPT; ++i) R.zi[i] = Rn.zi[i];
     }
+    live = live_next;
   }
 }
 
@@ -453,27 +526,61 @@ __global__ __launch_bounds__(NT, NT * BLOCKS / 256) void k_distill_step(DistillA
 
 }  // namespace
 
+// Shares of a row, where a few rows are split (0: they are not).  It costs a
+// launch, and pays from 128 KB a row with the gradient (4 x 129000 fp16: 31 us
+// on one CU a row, 18 split), from 320 KB without (5 x 50257 fp32: 10 on one
+// CU, 15 split).  Shares of 8192 logits at least, two blocks to a CU at most.
+static int distill_shares(int64_t rows, int vocab, int fmt, bool gradient) {
+  const int64_t bytes = (int64_t)vocab * (fmt == 1 ? 4 : 2);
+  if (rows > 128 || rows == 0 || bytes < (gradient ? 128 : 320) << 10) return 0;
+  return (int)std::min<int64_t>(std::min<int64_t>(64, vocab / 8192), 512 / rows);
+}
+
+size_t distill_scratch(int64_t rows, int vocab, int k, int fmt, bool gradient) {
+  const int shares = distill_shares(rows, vocab, fmt, gradient);
+  return shares ? ((size_t)rows * shares * 8 + (size_t)rows * k * 4 + 255) / 256 * 256 : 0;
+}
+
+template <typename Z> constexpr int format_of() { return sizeof(Z) == 4 ? 1 : 0; }   // by size: all that shares go by
+
 template <typename Z, bool FWD, bool BWD>
 static void launch_rows(const DistillArgs& a, hipStream_t s) {
-  // A block of 512 threads a row keeps three rows to a CU; where there are not
-  // that many rows, one of 1024, and the gradient's rows are shared out to
-  // fill the CUs.
-  const bool few = a.rows <= 256;
-  const int64_t share = !FWD && few ? std::min<int64_t>(256 / a.rows, (a.vocab + 16383) / 16384) : 1;
-  const dim3 grid((unsigned)std::min<int64_t>(a.rows, 1 << 20), (unsigned)share);
-  if (few) hipLaunchKernelGGL((k_distill_rows<Z, 1024, FWD, BWD>), grid, dim3(1024), 0, s, a);
-  else hipLaunchKernelGGL((k_distill_rows<Z, 512, FWD, BWD>), grid, dim3(512), 0, s, a);
+  // One row to a block: of 1024 threads where there are at most as many rows
+  // as CUs (the gradient's are shared out to fill the CUs), of 256 for short
+  // rows, eight of them to a CU, of 512 otherwise.  The gradient's blocks stay
+  // and walk their rows; the loss' rows each get a block of their own.
+  const int64_t most = BWD ? 1 : 1 << 10;
+  if (a.rows <= 256) {
+    const int64_t share = !FWD && BWD ? std::min<int64_t>(256 / a.rows, (a.vocab + 16383) / 16384) : 1;
+    hipLaunchKernelGGL((k_distill_rows<Z, 1024, FWD, BWD>), dim3((unsigned)a.rows, (unsigned)share), dim3(1024), 0, s, a);
+  } else if (a.vocab <= 256 * 8 * Chunk<Z>::N) {
+    hipLaunchKernelGGL((k_distill_rows<Z, 256, FWD, BWD>), dim3((unsigned)std::min<int64_t>(a.rows, 2048 * most)),
+                       dim3(256), 0, s, a);
+  } else {
+    hipLaunchKernelGGL((k_distill_rows<Z, 512, FWD, BWD>), dim3((unsigned)std::min<int64_t>(a.rows, 1024 * most)),
+                       dim3(512), 0, s, a);
+  }
 }
 
-template <bool FWD, bool BWD>
-static void launch_fmt(int fmt, const DistillArgs& a, hipStream_t s) {
-  if (fmt == 1) launch_rows<float, FWD, BWD>(a, s);
-  else if (fmt == 0) launch_rows<bf16_t, FWD, BWD>(a, s);
-  else launch_rows<fp16_t, FWD, BWD>(a, s);
+// A few rows in shares: the parts, then the loss (and the gradient).
+template <typename Z, bool BWD>
+static bool launch_shared(DistillArgs a, hipStream_t s) {
+  a.shares = distill_shares(a.rows, a.vocab, format_of<Z>(), BWD);
+  if (!a.shares || !a.parts) return false;   // (the entry points have checked the scratch)
+  a.zi = (float*)(a.parts + a.rows * a.shares);
+  const dim3 grid((unsigned)a.rows, (unsigned)a.shares);
+  hipLaunchKernelGGL((k_distill_part<Z, 256>), grid, dim3(256), 0, s, a);
+  hipLaunchKernelGGL((k_distill_rows<Z, 256, false, BWD>), BWD ? grid : dim3((unsigned)a.rows), dim3(256), 0, s, a);
+  return true;
 }
 
-void launch_distill_forward(int fmt, const DistillArgs& a, hipStream_t s) { launch_fmt<true, false>(fmt, a, s); }
-void launch_distill_backward(int fmt, const DistillArgs& a, hipStream_t s) { launch_fmt<false, true>(fmt, a, s); }
+template <typename Z>
+static void launch_forward(const DistillArgs& a, hipStream_t s) {
+  if (launch_shared<Z, false>(a, s)) return;
+  DistillArgs b = a;
+  b.parts = nullptr;
+  launch_rows<Z, true, false>(b, s);
+}
 
 template <typename Z, int NT, int NC, int BLOCKS>
 static void launch_held(const DistillArgs& a, hipStream_t s) {
@@ -484,17 +591,27 @@ static void launch_held(const DistillArgs& a, hipStream_t s) {
 template <typename Z>
 static void launch_step(const DistillArgs& a, hipStream_t s) {
   constexpr int N = Chunk<Z>::N;
-  if (a.vocab < 256 * 9 * N) launch_held<Z, 256, 8, 4>(a, s);
-  else if (a.vocab < 512 * 9 * N) launch_held<Z, 512, 8, 2>(a, s);
-  else if (a.vocab < 512 * 17 * N) launch_held<Z, 512, 16, 2>(a, s);
-  else if (a.vocab < 1024 * 17 * N) launch_held<Z, 1024, 16, 1>(a, s);
-  else launch_rows<Z, true, true>(a, s);
+  if (launch_shared<Z, true>(a, s)) return;
+  DistillArgs b = a;
+  b.parts = nullptr;
+  if (a.vocab < 256 * 9 * N) launch_held<Z, 256, 8, 4>(b, s);
+  else if (a.vocab < 512 * 9 * N) launch_held<Z, 512, 8, 2>(b, s);
+  else if (a.vocab < 512 * 17 * N) launch_held<Z, 512, 16, 2>(b, s);
+  else if (a.vocab < 1024 * 17 * N) launch_held<Z, 1024, 16, 1>(b, s);
+  else launch_rows<Z, true, true>(b, s);
 }
 
-void launch_distill_step(int fmt, const DistillArgs& a, hipStream_t s) {
-  if (fmt == 1) launch_step<float>(a, s);
-  else if (fmt == 0) launch_step<bf16_t>(a, s);
-  else launch_step<fp16_t>(a, s);
-}
+#define DION_DISTILL(F, fmt, a, s)            \
+  do {                                        \
+    if (fmt == 1) F<float>(a, s);             \
+    else if (fmt == 0) F<bf16_t>(a, s);       \
+    else F<fp16_t>(a, s);                     \
+  } while (0)
+
+template <typename Z> static void launch_gradient(const DistillArgs& a, hipStream_t s) { launch_rows<Z, false, true>(a, s); }
+
+void launch_distill_forward(int fmt, const DistillArgs& a, hipStream_t s) { DION_DISTILL(launch_forward, fmt, a, s); }
+void launch_distill_backward(int fmt, const DistillArgs& a, hipStream_t s) { DION_DISTILL(launch_gradient, fmt, a, s); }
+void launch_distill_step(int fmt, const DistillArgs& a, hipStream_t s) { DION_DISTILL(launch_step, fmt, a, s); }
 
 }  // namespace dion

@@ -285,6 +285,7 @@ struct DistillCheck : Check {
     need(std::isfinite(a.temp) && a.temp > 0.f, "temperature must be finite and positive");
     need(a.k >= 0, "k must not be negative");
     check_rows(*this, a.rows, a.vocab, "vocab must be positive");
+    if (a.vocab > (1 << 30)) fail(DION_E_UNSUPPORTED, "more than 2^30 logits a row");
     if (a.k > kDistillMaxK) fail(DION_E_UNSUPPORTED, "more than 1024 teacher logits a row");
     if (code != DION_OK) return;
     es = esize(dtype);
@@ -297,6 +298,12 @@ struct DistillCheck : Check {
     dz = View{a.dz, a.ldd, a.rows, a.vocab, es, "dlogits"};
     for (const View& v : {z, t, ix}) check_view(*this, v);
     if (a.gl) check_view(*this, gl);
+  }
+  void workspace(const void* ws, size_t have, size_t bytes) {   // a size of 256 means that none is used
+    if (bytes <= 256) return;
+    check_workspace(*this, ws, have, bytes);
+    const View v{ws, (int64_t)have, 1, (int64_t)have, 1, "workspace"};
+    for (const View& in : {z, t, ix, gl, loss, stats, dz}) check_apart(*this, v, in);
   }
   void output(const View& o, bool in_place = false) {
     check_view(*this, o);
@@ -313,18 +320,27 @@ double distill_bytes(const DistillArgs& a, int64_t es, int idx_bytes, bool grad)
 
 extern "C" {
 
+size_t dion_distill_topk_workspace_size(int64_t rows, int32_t vocab, int32_t k, int32_t dtype, int32_t gradient) {
+  if (rows < 0 || vocab <= 0 || k < 0 || k > kDistillMaxK || !valid_dtype(dtype)) {
+    (void)guarded([&]() { return set_error(DION_E_INVAL, "rows, vocab, k or dtype out of range"); });
+    return 0;
+  }
+  return std::max<size_t>(256, distill_scratch(rows, vocab, k, dtype, gradient != 0));
+}
+
 int dion_distill_topk(const void* logits, int64_t ldz, const void* teacher, const void* teacher_idx, float* loss,
                       float* stats, int64_t rows, int32_t vocab, int32_t k, int32_t dtype, int32_t teacher_dtype,
-                      int32_t idx_bytes, float temperature, void* stream) {
+                      int32_t idx_bytes, float temperature, void* workspace, size_t workspace_bytes, void* stream) {
   return guarded([&]() {
     const DistillArgs a{logits, teacher, teacher_idx, nullptr, loss, (float2*)stats, nullptr, ldz, 0, rows, vocab, k,
-                        teacher_dtype, idx_bytes == 8, temperature};
+                        teacher_dtype, idx_bytes == 8, temperature, (float2*)workspace, nullptr, 0};
     DistillCheck c(a, dtype, idx_bytes);
     if (c.code != DION_OK) return c.done();
     c.output(c.loss);
     c.output(c.stats);
     c.need((uintptr_t)stats % 8 == 0, "stats must be 8-byte aligned");
     check_apart(c, c.loss, c.stats);
+    c.workspace(workspace, workspace_bytes, dion_distill_topk_workspace_size(rows, vocab, k, dtype, 0));
     if (c.code != DION_OK || rows == 0) return c.done();
     const hipStream_t st = (hipStream_t)stream;
     return run_phase("distill_topk", "dion::k_distill_forward", 4.0 * rows * vocab,
@@ -338,7 +354,7 @@ int dion_distill_topk_backward(const float* grad_loss, const void* logits, int64
                                float temperature, void* stream) {
   return guarded([&]() {
     const DistillArgs a{logits, teacher, teacher_idx, grad_loss, nullptr, (float2*)stats, dlogits, ldz, ldd, rows,
-                        vocab, k, teacher_dtype, idx_bytes == 8, temperature};
+                        vocab, k, teacher_dtype, idx_bytes == 8, temperature, nullptr, nullptr, 0};
     DistillCheck c(a, dtype, idx_bytes);
     if (c.code != DION_OK) return c.done();
     check_view(c, c.stats);
@@ -355,15 +371,16 @@ int dion_distill_topk_backward(const float* grad_loss, const void* logits, int64
 int dion_distill_topk_step(const void* logits, int64_t ldz, const void* teacher, const void* teacher_idx,
                            const float* grad_loss, float* loss, void* dlogits, int64_t ldd, int64_t rows,
                            int32_t vocab, int32_t k, int32_t dtype, int32_t teacher_dtype, int32_t idx_bytes,
-                           float temperature, void* stream) {
+                           float temperature, void* workspace, size_t workspace_bytes, void* stream) {
   return guarded([&]() {
     const DistillArgs a{logits, teacher, teacher_idx, grad_loss, loss, nullptr, dlogits, ldz, ldd, rows,
-                        vocab, k, teacher_dtype, idx_bytes == 8, temperature};
+                        vocab, k, teacher_dtype, idx_bytes == 8, temperature, (float2*)workspace, nullptr, 0};
     DistillCheck c(a, dtype, idx_bytes);
     if (c.code != DION_OK) return c.done();
     c.output(c.loss);
     c.output(c.dz, true);
     check_apart(c, c.dz, c.loss);
+    c.workspace(workspace, workspace_bytes, dion_distill_topk_workspace_size(rows, vocab, k, dtype, 1));
     if (c.code != DION_OK || rows == 0) return c.done();
     const hipStream_t st = (hipStream_t)stream;
     return run_phase("distill_topk_step", "dion::k_distill_step", 8.0 * rows * vocab,

@@ -74,6 +74,9 @@ struct DistillArgs {
   int vocab, k;
   int t_fmt, idx64;
   float temp;
+  float2* parts;          // scratch of a few rows in shares: rows x shares statistics,
+  float* zi;              // and rows x k logits at the entries; NULL otherwise
+  int shares;
 };
 
 // rows of one dweight partial sum (fixed by the sizes alone, so that the
@@ -90,6 +93,8 @@ void launch_rmsnorm_backward(int fmt, int wfmt, const NormBackArgs& a, hipStream
 // the alignment of a and b)
 size_t int8_linear_scratch(const Int8Args& a);
 void launch_int8_linear(Int8Args a, hipStream_t s);
+// bytes of scratch (DistillArgs::parts) that the loss, or the loss with its gradient, needs
+size_t distill_scratch(int64_t rows, int vocab, int k, int fmt, bool gradient);
 void launch_distill_forward(int fmt, const DistillArgs& a, hipStream_t s);
 void launch_distill_backward(int fmt, const DistillArgs& a, hipStream_t s);
 void launch_distill_step(int fmt, const DistillArgs& a, hipStream_t s);

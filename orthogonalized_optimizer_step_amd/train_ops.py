@@ -129,6 +129,13 @@ def _workspace(nbytes, like, given, stream):
     return given, at + off, have
 
 
+def _scratch(nbytes, like, given, stream):
+    """the same where a size of 256 means that the call uses none"""
+    if nbytes == 256 and given is None:
+        return None, None, 0
+    return _workspace(nbytes, like, given, stream)
+
+
 def _used(stream, *tensors):
     if stream is not None:
         for t in tensors:
@@ -263,11 +270,7 @@ def int8_linear(a, a_scale, b, b_scale, bias=None, out_dtype=torch.bfloat16, wor
     if bias is not None:
         _vector(bias, "bias", n, _CODE, dev)
     pa, pb = a.data_ptr(), b.data_ptr()
-    need = lib.dion_int8_linear_workspace_size(pa, lda, pb, ldb, m, n, k)
-    if need <= 256 and workspace is None:   # these sizes use none
-        keep, ws, have = None, None, 0
-    else:
-        keep, ws, have = _workspace(need, a, workspace, stream)
+    keep, ws, have = _scratch(lib.dion_int8_linear_workspace_size(pa, lda, pb, ldb, m, n, k), a, workspace, stream)
     out = _new((*a.shape[:-1], n), out_dtype, a, stream)
     rc = lib.dion_int8_linear(pa, lda, a_scale.data_ptr(), pb, ldb, b_scale.data_ptr(),
                               _ptr(bias), 0 if bias is None else _CODE[bias.dtype], out.data_ptr(), n, m, n, k, code,
@@ -307,7 +310,7 @@ def _gradient(logits, rows, vocab, out, stream, dev):
     return out, _same(out, "out", logits, dev)
 
 
-def distill_topk(logits, teacher, teacher_idx, temperature=1.0, stream=None):
+def distill_topk(logits, teacher, teacher_idx, temperature=1.0, workspace=None, stream=None):
     """Loss of each row against a teacher's top logits: returns (loss, stats).
 
     ``logits``: rows x vocab; ``teacher`` and ``teacher_idx`` (int64 or int32):
@@ -316,13 +319,14 @@ def distill_topk(logits, teacher, teacher_idx, temperature=1.0, stream=None):
     outside the vocabulary or a logit of -inf are absent, and a row without any
     has loss and gradient 0.  ``stats`` is for ``distill_topk_backward``."""
     dev, rows, vocab, ldz, code, t, tcode, idx, ib, k = _distill_inputs(logits, teacher, teacher_idx)
+    keep, ws, have = _scratch(lib.dion_distill_topk_workspace_size(rows, vocab, k, code, 0), logits, workspace, stream)
     loss = _new(logits.shape[:-1], torch.float32, logits, stream)
     stats = _new((*logits.shape[:-1], 2), torch.float32, logits, stream)
     rc = lib.dion_distill_topk(logits.data_ptr(), ldz, t.data_ptr(), idx.data_ptr(), loss.data_ptr(), stats.data_ptr(),
-                               rows, vocab, k, code, tcode, ib, temperature, _handle(stream, dev))
+                               rows, vocab, k, code, tcode, ib, temperature, ws, have, _handle(stream, dev))
     if rc:
         check(rc)
-    _used(stream, logits, t, idx)
+    _used(stream, logits, t, idx, keep)
     return loss, stats
 
 
@@ -343,21 +347,23 @@ def distill_topk_backward(grad_loss, logits, stats, teacher, teacher_idx, temper
     return out
 
 
-def distill_topk_step(logits, teacher, teacher_idx, grad_loss=None, temperature=1.0, out=None, stream=None):
+def distill_topk_step(logits, teacher, teacher_idx, grad_loss=None, temperature=1.0, out=None, workspace=None,
+                      stream=None):
     """Loss and gradient in one call, for a ``grad_loss`` known ahead (such as
     one over the number of tokens; None: 1): returns (loss, dlogits).
     ``out`` may be the logits themselves."""
     dev, rows, vocab, ldz, code, t, tcode, idx, ib, k = _distill_inputs(logits, teacher, teacher_idx)
     if grad_loss is not None:
         _vector(grad_loss, "grad_loss", rows, _F32, dev)
+    keep, ws, have = _scratch(lib.dion_distill_topk_workspace_size(rows, vocab, k, code, 1), logits, workspace, stream)
     loss = _new(logits.shape[:-1], torch.float32, logits, stream)
     out, ldd = _gradient(logits, rows, vocab, out, stream, dev)
     rc = lib.dion_distill_topk_step(logits.data_ptr(), ldz, t.data_ptr(), idx.data_ptr(), _ptr(grad_loss),
                                     loss.data_ptr(), out.data_ptr(), ldd, rows, vocab, k, code, tcode, ib, temperature,
-                                    _handle(stream, dev))
+                                    ws, have, _handle(stream, dev))
     if rc:
         check(rc)
-    _used(stream, logits, t, idx, grad_loss, out)
+    _used(stream, logits, t, idx, grad_loss, out, keep)
     return loss, out
 
 

@@ -300,7 +300,8 @@ def distill_check(dion, z, t, idx, temp, gl, pad=0):
 
 
 DISTILL = [(1, 1, 1), (2, 3, 2), (1, 17, 5), (5, 1000, 1), (3, 1023, 64), (16, 4096, 100), (2, 50257, 32),
-           (1, 131072, 256), (7, 32001, 17), (300, 257, 8), (40, 8192, 1024)]
+           (1, 131072, 256), (7, 32001, 17), (300, 257, 8), (40, 8192, 1024),
+           (131, 70001, 20), (129, 140000, 5), (600, 20000, 40), (2100, 300, 33), (1100, 9000, 3)]
 
 
 @pytest.mark.parametrize("rows,vocab,k", DISTILL)
@@ -328,8 +329,8 @@ def test_distill_no_teacher_entries(dion):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
-@pytest.mark.parametrize("vocab", [200, 40000])
-def test_distill_masked_places(dion, dtype, vocab):
+@pytest.mark.parametrize("vocab,copies", [(200, 1), (40000, 1), (200, 30), (40000, 14)])
+def test_distill_masked_places(dion, dtype, vocab, copies):
     """-inf and the type's lowest value among the logits of both sides, NaN and
     infinities in rows without a teacher or gradient, indices out of range."""
     dt = DT[dtype]
@@ -364,6 +365,10 @@ def test_distill_masked_places(dion, dtype, vocab):
     d = dion.distill_topk_backward(gl, z, stats, t, idx)
     assert not d[5:8].any() and not d[0, hidden].any() and not d[1, hidden].any()
     z[7] = 0
+    z[8] = lowest                      # a student with nothing but masks, all equal
+    z[9, 5:] = float("-inf")           # almost nothing left of the student
+    idx[9] = torch.tensor([0, 1, 2, 3, 4, -1], device="cuda")
+    z, t, idx, gl = (v.repeat(copies, *[1] * (v.dim() - 1)) for v in (z, t, idx, gl))
     distill_check(dion, z, t, idx, 0.7, gl)
 
 
