@@ -318,8 +318,8 @@ __global__ __launch_bounds__(NT) void k_distill_rows(DistillArgs a) {
     const bool work = live && (joins || g != 0.f);   // beyond writing zeros
     if (work) {
       if (FWD) {
-        gather(R, E, row);   // under way beside the row itself
         stream_sum<Z, NT>(z, 0, a.vocab, c, R.m, R.s);
+        gather(R, E, row);   // in the caches now
       } else if (a.parts) {
         const float2 p = lane < a.shares ? a.parts[row * a.shares + lane] : make_float2(NEG, 0.f);
         R.m = p.x;

@@ -80,9 +80,12 @@ void check_workspace(Check& c, const void* ws, size_t have, size_t need) {
                                  std::to_string(have) + " given");
 }
 
+constexpr int64_t kMaxRows = (int64_t)1 << 40;   // more than any memory holds; sizes stay far from overflow
+
 void check_rows(Check& c, int64_t rows, int32_t cols, const char* what) {
   c.need(rows >= 0, "rows must not be negative");
   c.need(cols > 0, what);
+  if (rows > kMaxRows) c.fail(DION_E_UNSUPPORTED, "more than 2^40 rows");
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
@@ -176,7 +179,7 @@ int dion_int8_dequantize(const int8_t* q, int64_t ldq, const float* scale, void*
 }
 
 size_t dion_rmsnorm_backward_workspace_size(int64_t rows, int32_t cols, int32_t dtype) {
-  if (rows < 0 || cols <= 0 || cols > kNormMaxCols || !valid_dtype(dtype)) {
+  if (rows < 0 || rows > kMaxRows || cols <= 0 || cols > kNormMaxCols || !valid_dtype(dtype)) {
     (void)guarded([&]() { return set_error(DION_E_INVAL, "invalid rows, cols or dtype"); });
     return 0;
   }
@@ -321,7 +324,7 @@ double distill_bytes(const DistillArgs& a, int64_t es, int idx_bytes, bool grad)
 extern "C" {
 
 size_t dion_distill_topk_workspace_size(int64_t rows, int32_t vocab, int32_t k, int32_t dtype, int32_t gradient) {
-  if (rows < 0 || vocab <= 0 || k < 0 || k > kDistillMaxK || !valid_dtype(dtype)) {
+  if (rows < 0 || rows > kMaxRows || vocab <= 0 || k < 0 || k > kDistillMaxK || !valid_dtype(dtype)) {
     (void)guarded([&]() { return set_error(DION_E_INVAL, "rows, vocab, k or dtype out of range"); });
     return 0;
   }
