@@ -19,7 +19,7 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import orthogonalized_optimizer_step_amd as dion  # noqa: E402
 
 
-def main(steps=30, tokens=1024, dim=256, vocab=3001, k=48, temperature=2.0, seed=0):
+def main(steps=30, tokens=1024, dim=256, vocab=3001, k=48, temperature=2.0, seed=0, lr_layer=0.05, lr_head=0.2):
     """Trains for `steps` steps and returns the mean loss of each."""
     g = torch.Generator(device="cuda")
     g.manual_seed(seed)
@@ -34,7 +34,8 @@ def main(steps=30, tokens=1024, dim=256, vocab=3001, k=48, temperature=2.0, seed
     layer = torch.nn.Parameter(randn(dim, dim).mul_(0.2 / dim ** 0.5))
     head = torch.nn.Parameter(torch.zeros(vocab, dim, device="cuda", dtype=torch.bfloat16))
     norm = torch.nn.Parameter(torch.ones(dim, device="cuda", dtype=torch.bfloat16))
-    matrices = dion.Dion3([layer, head], lr=0.02, momentum=0.9, row_frac=1.0)
+    matrices = dion.Dion3([{"params": [layer], "lr": lr_layer}, {"params": [head], "lr": lr_head}], momentum=0.9,
+                          row_frac=1.0)
     vectors = torch.optim.SGD([norm], lr=0.1)
 
     losses = []
