@@ -396,24 +396,24 @@ __global__ __launch_bounds__(256) void k_rmsnorm_dw_long(NormBackArgs a) {
   a.partial[(int64_t)blockIdx.y * a.cols + j] = d;
 }
 
-// dweight from the parts' sums: 32 columns a block, the parts shared by 16
+// dweight from the parts' sums: 32 columns a block, the parts shared by 32
 // groups of threads, whose sums meet in LDS.
-template <typename W> __global__ __launch_bounds__(512) void k_rmsnorm_dw(NormBackArgs a) {
-  __shared__ float sum[16][33];
+template <typename W> __global__ __launch_bounds__(1024) void k_rmsnorm_dw(NormBackArgs a) {
+  __shared__ float sum[32][33];
   const int x = threadIdx.x & 31, g = threadIdx.x >> 5, j = blockIdx.x * 32 + x;
   float d = 0.f;
   if (j < a.cols) {
 #pragma unroll 8
-    for (int p = g; p < a.parts; p += 16) d += a.partial[(int64_t)p * a.cols + j];
+    for (int p = g; p < a.parts; p += 32) d += a.partial[(int64_t)p * a.cols + j];
   }
   sum[g][x] = d;
   __syncthreads();
-  if (g == 0 && j < a.cols) {
-    d = 0.f;
+  // thread (g, x) now holds part x of column g: a half wave joins a column
+  d = sum[x][g];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) d += sum[i][x];
-    ((W*)a.dweight)[j] = from_f<W>(d);
-  }
+  for (int o = 16; o > 0; o >>= 1) d += __shfl_xor(d, o, 32);
+  const int c = blockIdx.x * 32 + g;
+  if (x == 0 && c < a.cols) ((W*)a.dweight)[c] = from_f<W>(d);
 }
 
 template <typename T, bool INT8, int NT, int CH>
@@ -468,18 +468,20 @@ void launch_back(const NormBackArgs& a, bool w32, hipStream_t s) {
     }
   }
   const dim3 gw((unsigned)((a.cols + 31) / 32));
-  if (w32) hipLaunchKernelGGL((k_rmsnorm_dw<float>), gw, dim3(512), 0, s, a);
-  else hipLaunchKernelGGL((k_rmsnorm_dw<T>), gw, dim3(512), 0, s, a);
+  if (w32) hipLaunchKernelGGL((k_rmsnorm_dw<float>), gw, dim3(1024), 0, s, a);
+  else hipLaunchKernelGGL((k_rmsnorm_dw<T>), gw, dim3(1024), 0, s, a);
 }
 
 }  // namespace
 
-// Blocks of the backward pass, each with a partial sum of dweight.
+// Blocks of the backward pass, each with a partial sum of dweight: as many as
+// the CUs hold at once by the kernels' registers (16384 x 768 bf16: 768 blocks
+// of four rows).
 int norm_back_parts(int64_t rows, int cols, int fmt) {
   const int chunks = (cols + (fmt == 1 ? 3 : 7)) / (fmt == 1 ? 4 : 8);
   if (chunks > kHeldChunks) return (int)std::min<int64_t>(256, (rows + 31) / 32);
-  if (chunks <= 128) return (int)std::min<int64_t>(1024, (rows + 3) / 4);
-  return (int)std::min<int64_t>(chunks <= 256 ? 1024 : 512, rows);
+  if (chunks <= 128) return (int)std::min<int64_t>(chunks <= 64 ? 1536 : 768, (rows + 3) / 4);
+  return (int)std::min<int64_t>(chunks <= 256 ? 1536 : chunks <= 512 ? 768 : chunks <= 1024 ? 512 : 256, rows);
 }
 
 void launch_rmsnorm(int fmt, int wfmt, bool int8_out, const NormArgs& a, hipStream_t s) {
