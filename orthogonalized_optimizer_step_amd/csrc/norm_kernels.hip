@@ -8,8 +8,8 @@
 //   backward, with g = dy w and c = rstd^2 mean(g h):
 //     dx = rstd (g - h c) + dh        dw_j = sum over rows of dy_j h_j rstd
 //
-// A row is read once into registers, CH 16-byte chunks by each of its NT
-// threads (chunk i of thread t at element (i NT + t) N), and everything is
+// A row is read once into registers, CH 16-byte chunks by each of its NT (16
+// to 1024) threads (chunk i of thread t at element (i NT + t) N), and everything is
 // formed from there.  All of it is bound by memory; what it takes at 8192 x
 // 4096 and the like stands at the launch rules below.
 #include <algorithm>
@@ -30,13 +30,15 @@ __device__ __forceinline__ void row_scale(float a, float& scale, float& inv) {
   inv = bad || tiny ? 0.f : 127.f * (1.f / a);
 }
 
-// Threads of a block: rows of one wave go four to a block.
-constexpr int block_of(int nt) { return nt == 64 ? 256 : nt; }
+// Threads of a block: rows of up to a wave share one.
+constexpr int block_of(int nt) { return nt <= 64 ? 256 : nt; }
 
 // Over the NT threads of a row; `red`: 16 floats, one array for each of two
 // uses in turn.
 template <int NT, typename Op> __device__ __forceinline__ float row_join(float v, float* red, Op op) {
-  if constexpr (NT == 64) return wave_reduce(v, 0.f, op);
+  if constexpr (NT == 16) return row16_reduce(v, op);
+  else if constexpr (NT == 32) return pair_reduce(row16_reduce(v, op), op);
+  else if constexpr (NT == 64) return wave_reduce(v, 0.f, op);
   else return block_reduce<NT>(v, 0.f, red, op);
 }
 
@@ -144,7 +146,7 @@ __global__ __launch_bounds__(block_of(NT)) void k_rmsnorm(NormArgs a, bool w32) 
     }
     float scale = 0.f, inv = 0.f;
     if (INT8) {
-      if (NT > 64 && !a.weight) turn ^= 1;   // the only join of the row
+      if (!a.weight) turn ^= 1;   // the only join of the row
       row_scale(row_join<NT>(m, a.weight ? red[2] : red[turn], MaxAbs()), scale, inv);
       int8_t* q = (int8_t*)a.y + row * a.ldy;
 #pragma unroll
@@ -429,11 +431,14 @@ constexpr int kHeldChunks = 2048;   // longest row that is held, in 16-byte chun
 // bits (us): a row of 4096 41 on 512 threads, 46 on 256; of 8192 49 on 512
 // threads, 61 on 1024; of 16384 54 on 1024 threads, 65 on 512.  Many threads
 // with little each hide memory best, until the waves of a row wait for one
-// another at its two joins.
+// another at its two joins.  2^24 elements in rows of 64: 30 on 16 threads, 106
+// on 64; in rows of 256: 23 on 32, 31 on 64.
 template <typename T, bool INT8>
 void launch_norm(const NormArgs& a, bool w32, hipStream_t s) {
   const int chunks = (a.cols + Chunk<T>::N - 1) / Chunk<T>::N;
-  if (chunks <= 64) launch_forward<T, INT8, 64, 1>(a, w32, s);
+  if (chunks <= 16) launch_forward<T, INT8, 16, 1>(a, w32, s);
+  else if (chunks <= 32) launch_forward<T, INT8, 32, 1>(a, w32, s);
+  else if (chunks <= 64) launch_forward<T, INT8, 64, 1>(a, w32, s);
   else if (chunks <= 128) launch_forward<T, INT8, 64, 2>(a, w32, s);
   else if (chunks <= 256) launch_forward<T, INT8, 256, 1>(a, w32, s);
   else if (chunks <= 512) launch_forward<T, INT8, 512, 1>(a, w32, s);
@@ -453,7 +458,9 @@ template <typename T>
 void launch_back(const NormBackArgs& a, bool w32, hipStream_t s) {
   const int chunks = (a.cols + Chunk<T>::N - 1) / Chunk<T>::N;
   if (a.rows > 0) {
-    if (chunks <= 64) launch_backward<T, 64, 1>(a, w32, s);
+    if (chunks <= 16) launch_backward<T, 16, 1>(a, w32, s);
+    else if (chunks <= 32) launch_backward<T, 32, 1>(a, w32, s);
+    else if (chunks <= 64) launch_backward<T, 64, 1>(a, w32, s);
     else if (chunks <= 128) launch_backward<T, 64, 2>(a, w32, s);
     else if (chunks <= 256) launch_backward<T, 256, 1>(a, w32, s);
     else if (chunks <= 512) launch_backward<T, 512, 1>(a, w32, s);
@@ -480,6 +487,8 @@ void launch_back(const NormBackArgs& a, bool w32, hipStream_t s) {
 int norm_back_parts(int64_t rows, int cols, int fmt) {
   const int chunks = (cols + (fmt == 1 ? 3 : 7)) / (fmt == 1 ? 4 : 8);
   if (chunks > kHeldChunks) return (int)std::min<int64_t>(256, (rows + 31) / 32);
+  if (chunks <= 16) return (int)std::min<int64_t>(1536, (rows + 15) / 16);
+  if (chunks <= 32) return (int)std::min<int64_t>(1536, (rows + 7) / 8);
   if (chunks <= 128) return (int)std::min<int64_t>(chunks <= 64 ? 1536 : 768, (rows + 3) / 4);
   return (int)std::min<int64_t>(chunks <= 256 ? 1536 : chunks <= 512 ? 768 : chunks <= 1024 ? 512 : 256, rows);
 }

@@ -21,11 +21,6 @@ __device__ __forceinline__ float load_fmt(const void* p, int64_t i, int fmt) {
   if (fmt == 0) return (float)((const bf16_t*)p)[i];
   return (float)((const fp16_t*)p)[i];
 }
-__device__ __forceinline__ void store_fmt(void* p, int64_t i, int fmt, float v) {
-  if (fmt == 1) ((float*)p)[i] = v;
-  else if (fmt == 0) ((bf16_t*)p)[i] = (bf16_t)v;
-  else ((fp16_t*)p)[i] = (fp16_t)v;
-}
 
 typedef int intx4 __attribute__((ext_vector_type(4)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
@@ -118,6 +113,19 @@ template <int W, typename Op> __device__ __forceinline__ float row_reduce(float 
   if (W > 4) v = op(v, lane_move<0x114, 0xf>(none, v));
   if (W > 8) v = op(v, lane_move<0x118, 0xf>(none, v));
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), W - 1));
+}
+
+// op over each row of 16 lanes by itself, the same in all of them
+template <typename Op> __device__ __forceinline__ float row16_reduce(float v, Op op) {
+  v = op(v, lane_move<0x128, 0xf>(v, v));   // rotated by 8, 4, 2, 1
+  v = op(v, lane_move<0x124, 0xf>(v, v));
+  v = op(v, lane_move<0x122, 0xf>(v, v));
+  return op(v, lane_move<0x121, 0xf>(v, v));
+}
+
+// and over two such rows, which ds_swizzle exchanges (lane xor 16)
+template <typename Op> __device__ __forceinline__ float pair_reduce(float v, Op op) {
+  return op(v, __int_as_float(__builtin_amdgcn_ds_swizzle(__float_as_int(v), 0x401f)));
 }
 
 struct Add {
