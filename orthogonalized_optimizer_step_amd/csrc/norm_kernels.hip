@@ -481,16 +481,19 @@ void launch_back(const NormBackArgs& a, bool w32, hipStream_t s) {
 
 }  // namespace
 
-// Blocks of the backward pass, each with a partial sum of dweight: as many as
-// the CUs hold at once by the kernels' registers (16384 x 768 bf16: 768 blocks
-// of four rows).
+// Blocks of the backward pass, each with a partial sum of dweight: as many for
+// every CU, which counts more than as many rows for every block.  More blocks hide memory better; fewer have less
+// to write and read again (4 bytes a column each).  2^24 elements, 256 / 512 /
+// 1024 blocks (us): bf16 rows of 256 30.2 / 25.4 / 25.7, of 1024 26.7 / 26.0 /
+// 28.7, of 2048 33.4 / 28.3 / 30.2, of 4096 27.6 / 29.0 / 33.9; fp32 rows of 64
+// 88 / 56 / 46, of 1024 80 / 59 / 49, of 2048 63 / 48 / 49, of 4096 44 / 46 / 52.  bf16 rows of
+// 768 take 768 blocks: 43.6 with the forward pass, 45.5 on 512.
 int norm_back_parts(int64_t rows, int cols, int fmt) {
   const int chunks = (cols + (fmt == 1 ? 3 : 7)) / (fmt == 1 ? 4 : 8);
   if (chunks > kHeldChunks) return (int)std::min<int64_t>(256, (rows + 31) / 32);
-  if (chunks <= 16) return (int)std::min<int64_t>(1536, (rows + 15) / 16);
-  if (chunks <= 32) return (int)std::min<int64_t>(1536, (rows + 7) / 8);
-  if (chunks <= 128) return (int)std::min<int64_t>(chunks <= 64 ? 1536 : 768, (rows + 3) / 4);
-  return (int)std::min<int64_t>(chunks <= 256 ? 1536 : chunks <= 512 ? 768 : chunks <= 1024 ? 512 : 256, rows);
+  const int64_t most = cols <= (fmt == 1 ? 1024 : 512) ? 1024 : cols <= 1024 ? 768 : cols <= 2048 ? 512 : 256;
+  const int64_t per = chunks <= 16 ? 16 : chunks <= 32 ? 8 : chunks <= 128 ? 4 : 1;   // rows at once
+  return (int)std::min(most, (rows + per - 1) / per);
 }
 
 void launch_rmsnorm(int fmt, int wfmt, bool int8_out, const NormArgs& a, hipStream_t s) {
