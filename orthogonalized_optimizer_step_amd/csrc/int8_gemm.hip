@@ -52,14 +52,37 @@ __device__ __forceinline__ intx4 raw_buffer(const void* p, uint32_t bytes) {
   return r;
 }
 
-// 16 bytes of a row from k on, zeros from `ks` on
+// 16 bytes of a row from k on, zeros from `ks` on: at the row's end its last
+// 16 bytes, moved down
 __device__ __forceinline__ intx4 load_chunk(const int8_t* row, int k, int ks) {
   if (k + 16 <= ks) return *(const intx4u*)(row + k);
   intx4 v = {0, 0, 0, 0};
+  if (k >= ks) return v;
+  if (ks >= 16) {
+    union { intx4 v; uint64_t u[2]; } c;
+    c.v = *(const intx4u*)(row + ks - 16);
+    const int bits = 8 * (k + 16 - ks);   // 8 .. 120
+    if (bits < 64) c.u[0] = c.u[0] >> bits | c.u[1] << (64 - bits);
+    else c.u[0] = c.u[1] >> (bits - 64);
+    c.u[1] = bits < 64 ? c.u[1] >> bits : 0;
+    return c.v;
+  }
 #pragma unroll
   for (int i = 0; i < 16; ++i)
     if (k + i < ks) v[i >> 2] |= (int)(uint8_t)row[k + i] << (8 * (i & 3));
   return v;
+}
+
+// 32 bytes at p + shift (p at a whole dword, shift 0 .. 3) from the 36 at p
+typedef intx4 intx4d __attribute__((aligned(4)));
+__device__ __forceinline__ void load_shifted(const int8_t* p, uint32_t shift, intx4& lo, intx4& hi) {
+  const intx4 u = *(const intx4d*)p, v = *(const intx4d*)(p + 16);
+  const int w = *(const int*)(p + 32);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    lo[i] = (int)__builtin_amdgcn_alignbyte((uint32_t)(i < 3 ? u[(i + 1) & 3] : v[0]), (uint32_t)u[i], shift);
+    hi[i] = (int)__builtin_amdgcn_alignbyte((uint32_t)(i < 3 ? v[(i + 1) & 3] : w), (uint32_t)v[i], shift);
+  }
 }
 
 // an output before its rounding
@@ -314,7 +337,13 @@ void launch_mma(const Int8Args& a, int splits, hipStream_t s) {
 // block l / 16; result element e of lane l is row 4 (l / 16) + e of the first
 // operand and row l % 16 of the second), at any alignment.  Rows past the end
 // repeat the last one and are not written.
-template <int NW, int KW, typename O>
+//
+// SHIFT: rows that start inside a dword, in matrices that start at one.
+// Loads of 16 bytes inside dwords take twice the time (6 x 14336 x 12277: 98
+// us; 56 this way, and rows of 12284 53 on the plain loads); so whole dwords are
+// loaded and moved together, 32 bytes of k a lane.  They hold up to three bytes before the lane's own (of the row
+// before, or the gap) and four after, which the loop keeps inside the row.
+template <int NW, int KW, bool SHIFT, typename O>
 __global__ __launch_bounds__(64 * NW * KW) void k_int8_rows(Int8Args g, int* partial) {
   __shared__ __attribute__((aligned(16))) int sum[KW * NW * 256];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -328,14 +357,26 @@ __global__ __launch_bounds__(64 * NW * KW) void k_int8_rows(Int8Args g, int* par
   const int p0 = (int)((int64_t)pieces * blockIdx.y / gridDim.y);
   const int kend = min(g.k, (int)((int64_t)pieces * (blockIdx.y + 1) / gridDim.y) * 128);
   int k0 = (p0 + kw) * 128;
+  if (SHIFT) {
+    const uint32_t sa = (uint32_t)(uintptr_t)a & 3, sb = (uint32_t)(uintptr_t)b & 3;
+    const int8_t *aw = a - sa + 2 * kc, *bw = b - sb + 2 * kc;
 #pragma unroll 4
-  for (; k0 + 128 <= kend; k0 += KW * 128) {
+    for (; k0 + 128 <= kend && k0 + 132 <= g.k; k0 += KW * 128) {
+      intx4 a0, a1, b0, b1;
+      load_shifted(bw + k0, sb, b0, b1);
+      load_shifted(aw + k0, sa, a0, a1);
+      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(b0, a0, acc, 0, 0, 0);
+      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(b1, a1, acc, 0, 0, 0);
+    }
+  }
+#pragma unroll 4
+  for (; !SHIFT && k0 + 128 <= kend; k0 += KW * 128) {
 #pragma unroll
     for (int h = 0; h < 128; h += 64)
       acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(*(const intx4u*)(b + k0 + kc + h), *(const intx4u*)(a + k0 + kc + h),
                                                   acc, 0, 0, 0);
   }
-  if (k0 < kend) {   // the last piece, in part
+  if (k0 < kend) {   // the last piece, in part or up to the row's end
     for (int h = 0; h < 128; h += 64)
       acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(load_chunk(b, k0 + kc + h, kend), load_chunk(a, k0 + kc + h, kend),
                                                   acc, 0, 0, 0);
@@ -355,14 +396,22 @@ __global__ __launch_bounds__(64 * NW * KW) void k_int8_rows(Int8Args g, int* par
   }
 }
 
-template <int NW, int KW>
-void launch_rows(const Int8Args& a, int splits, hipStream_t s) {
+template <int NW, int KW, bool SHIFT>
+void launch_rows_as(const Int8Args& a, int splits, hipStream_t s) {
   const dim3 grid((unsigned)((a.n + 16 * NW - 1) / (16 * NW)), splits), block(64 * NW * KW);
   int* part = splits > 1 ? a.partial : nullptr;
-  if (a.out_fmt == 1) hipLaunchKernelGGL((k_int8_rows<NW, KW, float>), grid, block, 0, s, a, part);
-  else if (a.out_fmt == 0) hipLaunchKernelGGL((k_int8_rows<NW, KW, bf16_t>), grid, block, 0, s, a, part);
-  else hipLaunchKernelGGL((k_int8_rows<NW, KW, fp16_t>), grid, block, 0, s, a, part);
+  if (a.out_fmt == 1) hipLaunchKernelGGL((k_int8_rows<NW, KW, SHIFT, float>), grid, block, 0, s, a, part);
+  else if (a.out_fmt == 0) hipLaunchKernelGGL((k_int8_rows<NW, KW, SHIFT, bf16_t>), grid, block, 0, s, a, part);
+  else hipLaunchKernelGGL((k_int8_rows<NW, KW, SHIFT, fp16_t>), grid, block, 0, s, a, part);
   if (part) launch_join(a, splits, s);
+}
+
+template <int NW, int KW>
+void launch_rows(const Int8Args& a, int splits, hipStream_t s) {
+  const bool inside = (a.m > 1 && a.lda % 4) || (a.n > 1 && a.ldb % 4);   // a dword
+  const bool start = ((uintptr_t)a.a | (uintptr_t)a.b) % 4 == 0;
+  if (inside && start) launch_rows_as<NW, KW, true>(a, splits, s);
+  else launch_rows_as<NW, KW, false>(a, splits, s);
 }
 
 // Rows of a and b at multiples of 16 bytes, zeros past k: 16 bytes a thread.

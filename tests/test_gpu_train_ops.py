@@ -229,6 +229,26 @@ def test_int8_linear_extremes(dion):
     assert torch.equal(y[0].cpu(), want.float()) and torch.equal(y[2].cpu(), (2 * want).float())
 
 
+@pytest.mark.parametrize("m,n", [(1, 37), (5, 300), (16, 21), (3, 14001), (40, 70)])
+@pytest.mark.parametrize("k,gap", [(5, 2), (127, 0), (130, 3), (131, 0), (133, 0), (128, 1), (132, 5), (2051, 0), (2048, 7),
+                                   (14339, 0)])
+@pytest.mark.parametrize("start", [0, 1, 4])
+def test_int8_linear_rows_inside_dwords(dion, m, n, k, gap, start):
+    """Rows at any byte, between other bytes that must not count: with scales of one the output is the exact sum,
+    rounded once."""
+    def matrix(rows, seed):
+        g = torch.Generator(device="cuda")
+        g.manual_seed(seed)
+        whole = torch.full((start + rows * (k + gap),), -128, dtype=torch.int8, device="cuda")
+        v = whole[start:].view(rows, k + gap)[:, :k]
+        v.copy_(torch.randint(-128, 128, (rows, k), generator=g, device="cuda"))
+        return v
+    a, b = matrix(m, k), matrix(n, k + 1)
+    one = torch.ones(max(m, n), device="cuda")
+    y = dion.int8_linear(a, one[:m], b, one[:n], out_dtype=torch.float32)
+    assert torch.equal(y, (a.double() @ b.double().t()).float())
+
+
 def test_int8_linear_leading_dimensions_and_order(dion):
     """Tokens with leading dimensions; every row is computed as it is alone."""
     a = torch.randint(-127, 128, (4, 10, 192), device="cuda").to(torch.int8)
