@@ -487,11 +487,19 @@ void launch_back(const NormBackArgs& a, bool w32, hipStream_t s) {
 // 1024 blocks (us): bf16 rows of 256 30.2 / 25.4 / 25.7, of 1024 26.7 / 26.0 /
 // 28.7, of 2048 33.4 / 28.3 / 30.2, of 4096 27.6 / 29.0 / 33.9; fp32 rows of 64
 // 88 / 56 / 46, of 1024 80 / 59 / 49, of 2048 63 / 48 / 49, of 4096 44 / 46 / 52.  bf16 rows of
-// 768 take 768 blocks: 43.6 with the forward pass, 45.5 on 512.
+// 768, four to a block: 43.6 on 768 blocks with the forward pass, 45.5 on 512.
+// One row to a block whose threads it does not fill, 512 / 1024: bf16 16000 x
+// 1066 67 / 45, fp32 83 / 60.  Rows that start inside 16 bytes wait longer for
+// memory, 256 / 512: bf16 4000 x 4001 45 / 39, fp32 57 / 50.
 int norm_back_parts(int64_t rows, int cols, int fmt) {
   const int chunks = (cols + (fmt == 1 ? 3 : 7)) / (fmt == 1 ? 4 : 8);
   if (chunks > kHeldChunks) return (int)std::min<int64_t>(256, (rows + 31) / 32);
-  const int64_t most = cols <= (fmt == 1 ? 1024 : 512) ? 1024 : cols <= 1024 ? 768 : cols <= 2048 ? 512 : 256;
+  const bool whole = cols % (fmt == 1 ? 4 : 8) == 0;
+  const int64_t most = cols <= (fmt == 1 ? 1536 : 512)               ? 1024
+                       : chunks <= 128                               ? 768
+                       : cols <= 1536                                ? 1024
+                       : cols <= 2048 || (cols <= 4096 && !whole)    ? 512
+                                                                     : 256;
   const int64_t per = chunks <= 16 ? 16 : chunks <= 32 ? 8 : chunks <= 128 ? 4 : 1;   // rows at once
   return (int)std::min(most, (rows + per - 1) / per);
 }
