@@ -440,7 +440,8 @@ int dion_rmsnorm_backward(const void* dy, int64_t lddy, const void* h, int64_t l
  * The workspace holds the sums of splits of k, and copies of a or b where
  * their rows do not start at multiples of 16 bytes (a k that is not a multiple
  * of 16, an unaligned pointer or stride) and m > 16; its size depends on the
- * pointers' alignment.  Products whose size is 256 use none: it may be NULL. */
+ * pointers' alignment.  Products whose size is 256 use none (it may be NULL);
+ * the others' is 512 at least. */
 size_t dion_int8_linear_workspace_size(const int8_t* a, int64_t lda, const int8_t* b, int64_t ldb, int64_t m,
                                        int64_t n, int32_t k);
 int dion_int8_linear(const int8_t* a, int64_t lda, const float* a_scale, const int8_t* b, int64_t ldb,

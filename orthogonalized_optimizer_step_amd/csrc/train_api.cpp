@@ -90,6 +90,11 @@ void check_rows(Check& c, int64_t rows, int32_t cols, const char* what) {
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
+// The size that an entry point reports for `scratch` bytes: kNone where it uses
+// none, and more than that for any that it does use, however little.
+constexpr size_t kNone = 256;
+size_t reported_size(size_t scratch) { return scratch ? std::max(2 * kNone, align256(scratch)) : kNone; }
+
 // The forward norm and the codes of plain rows share a kernel and its checks.
 int norm_call(const char* name, bool int8_out, NormArgs a, int dtype, int wdtype, hipStream_t stream) {
   Check c;
@@ -228,7 +233,7 @@ size_t dion_int8_linear_workspace_size(const int8_t* a, int64_t lda, const int8_
     (void)guarded([&]() { return set_error(DION_E_INVAL, "m, n or k out of range"); });
     return 0;
   }
-  if (m == 0 || n == 0) return 256;
+  if (m == 0 || n == 0) return kNone;
   Int8Args g{};
   g.a = a;
   g.b = b;
@@ -237,7 +242,7 @@ size_t dion_int8_linear_workspace_size(const int8_t* a, int64_t lda, const int8_
   g.m = m;
   g.n = n;
   g.k = k;
-  return std::max<size_t>(256, int8_linear_scratch(g));
+  return reported_size(int8_linear_scratch(g));
 }
 
 int dion_int8_linear(const int8_t* a, int64_t lda, const float* a_scale, const int8_t* b, int64_t ldb,
@@ -258,7 +263,7 @@ int dion_int8_linear(const int8_t* a, int64_t lda, const float* a_scale, const i
     if (bias) check_view(c, vbias);
     for (const View& in : {va, vb, vsa, vsb, vbias}) check_apart(c, vo, in);
     const size_t need = dion_int8_linear_workspace_size(a, lda, b, ldb, m, n, k);
-    if (need > 256) {   // 256: none is used
+    if (need > kNone) {
       check_workspace(c, workspace, workspace_bytes, need);
       const View vws{workspace, (int64_t)workspace_bytes, 1, (int64_t)workspace_bytes, 1, "workspace"};
       for (const View& in : {va, vb, vsa, vsb, vbias, vo}) check_apart(c, vws, in);
@@ -266,7 +271,7 @@ int dion_int8_linear(const int8_t* a, int64_t lda, const float* a_scale, const i
     if (c.code != DION_OK || m == 0 || n == 0) return c.done();
     const hipStream_t st = (hipStream_t)stream;
     const Int8Args g{a, b, a_scale, b_scale, bias, out, lda, ldb, ldo, m, n, k, bias_dtype, out_dtype,
-                     (int*)workspace};
+                     need > kNone ? (int*)workspace : nullptr};
     return run_phase("int8_linear", "dion::k_int8", 2.0 * m * n * k,
                      (double)m * k + (double)n * k + (double)m * n * esize(out_dtype), st,
                      [&]() { launch_int8_linear(g, st); });

@@ -1,0 +1,52 @@
+"""Calls of the training-step operators at the edges of their plans, on the GPU: the smallest uses of scratch, masks
+anywhere in a row, teacher tensors that are views on other streams, the longest and the emptiest shapes.
+
+Tolerances are those of the operators' other tests: u is the largest relative rounding error of the output's type, and
+an fp32 sum is allowed ACC = 2^-15 of its magnitudes' sum.
+"""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from oracle import train_oracle as O  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+U = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}
+ACC = 2.0 ** -15
+
+
+@pytest.fixture(scope="module")
+def dion():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import orthogonalized_optimizer_step_amd as d
+    return d
+
+
+def n64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def generator(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def codes(seed, shape):
+    return torch.randint(-128, 128, shape, generator=generator(seed), device="cuda").to(torch.int8)
+
+
+# ------------------------------------------------------------- 8-bit products
+@pytest.mark.parametrize("m,n,k,start", [(1, 1, 7168, 0), (1, 32, 7168, 0), (2, 16, 7168, 0), (16, 2, 7168, 0),
+                                         (1, 8, 14336, 0), (1, 16, 14336, 0), (17, 1, 128, 3), (32, 4, 64, 1)])
+def test_int8_linear_with_little_scratch(dion, m, n, k, start):
+    """The sums of the splits, or the aligned copy of b, take 256 bytes at most.  With scales of one the output is the
+    exact sum, rounded once."""
+    a = codes(m, (m, k))
+    b = codes(n + 100, (start + n * k,))[start:].view(n, k)
+    one = torch.ones(max(m, n), device="cuda")
+    y = dion.int8_linear(a, one[:m], b, one[:n], out_dtype=torch.float32)
+    assert torch.equal(y, (a.double() @ b.double().t()).float())

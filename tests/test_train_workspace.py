@@ -1,0 +1,27 @@
+"""Workspaces of the training-step operators without a GPU: a size of 256 bytes says that a call uses none, so no call
+that uses some may report it, however little that is."""
+import pytest
+
+import orthogonalized_optimizer_step_amd as dion  # noqa: F401
+from orthogonalized_optimizer_step_amd import _lib
+
+lib = _lib.lib
+BF16, FP32 = 0, 1
+A, B, C, D, E, H = (0x10000000 * i for i in range(1, 7))   # far apart; nothing dereferences them
+WORKSPACE, INVAL = -3, -1
+
+
+# k in splits whose sums fit 256 bytes, and copies of a few unaligned rows
+@pytest.mark.parametrize("m,n,k,b,ldb", [(1, 1, 7168, B, 7168), (1, 32, 7168, B, 7168), (2, 16, 7168, B, 7168),
+                                         (16, 2, 7168, B, 7168), (1, 8, 14336, B, 14336), (1, 16, 14336, B, 14336),
+                                         (17, 1, 128, B + 3, 128), (32, 4, 64, B + 1, 64), (17, 1, 128, B, 129)])
+def test_little_scratch_of_a_product_is_asked_for_and_checked(m, n, k, b, ldb):
+    need = lib.dion_int8_linear_workspace_size(A, k, b, ldb, m, n, k)
+    assert need > 256
+
+    def call(ws, have):
+        return lib.dion_int8_linear(A, k, C, b, ldb, D, None, 0, E, n, m, n, k, BF16, ws, have, None)
+
+    assert call(None, 0) == WORKSPACE and call(None, need) == WORKSPACE
+    assert call(H, 0) == WORKSPACE and call(H, need - 1) == WORKSPACE and call(H + 16, need) == WORKSPACE
+    assert call(A, need) == INVAL   # on top of an operand
