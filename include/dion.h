@@ -467,8 +467,8 @@ int dion_int8_linear(const int8_t* a, int64_t lda, const float* a_scale, const i
  * dion_distill_topk_step computes the loss and the gradient in one call, for
  * a grad_loss known ahead of it.  The workspace holds parts of a few rows that
  * are shared out between blocks (gradient: 1 for dion_distill_topk_step, 0
- * for dion_distill_topk); sizes whose workspace size is 256 use none, and it
- * may be NULL. */
+ * for dion_distill_topk); sizes whose workspace size is 256 use none (it may
+ * be NULL), the others' is 512 at least. */
 size_t dion_distill_topk_workspace_size(int64_t rows, int32_t vocab, int32_t k, int32_t dtype, int32_t gradient);
 int dion_distill_topk(const void* logits, int64_t ldz, const void* teacher, const void* teacher_idx, float* loss,
                       float* stats, int64_t rows, int32_t vocab, int32_t k, int32_t dtype, int32_t teacher_dtype,

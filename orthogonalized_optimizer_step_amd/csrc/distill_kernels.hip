@@ -566,7 +566,7 @@ static void launch_rows(const DistillArgs& a, hipStream_t s) {
 template <typename Z, bool BWD>
 static bool launch_shared(DistillArgs a, hipStream_t s) {
   a.shares = distill_shares(a.rows, a.vocab, format_of<Z>(), BWD);
-  if (!a.shares || !a.parts) return false;   // (the entry points have checked the scratch)
+  if (!a.shares || !a.parts) return false;   // parts: checked scratch, wherever there are shares
   a.zi = (float*)(a.parts + a.rows * a.shares);
   const dim3 grid((unsigned)a.rows, (unsigned)a.shares);
   hipLaunchKernelGGL((k_distill_part<Z, 256>), grid, dim3(256), 0, s, a);

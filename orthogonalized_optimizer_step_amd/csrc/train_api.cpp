@@ -307,11 +307,13 @@ struct DistillCheck : Check {
     for (const View& v : {z, t, ix}) check_view(*this, v);
     if (a.gl) check_view(*this, gl);
   }
-  void workspace(const void* ws, size_t have, size_t bytes) {   // a size of 256 means that none is used
-    if (bytes <= 256) return;
+  // the workspace as the launcher gets it: NULL where none is used, whatever was given
+  float2* workspace(void* ws, size_t have, size_t bytes) {
+    if (bytes <= kNone) return nullptr;
     check_workspace(*this, ws, have, bytes);
     const View v{ws, (int64_t)have, 1, (int64_t)have, 1, "workspace"};
     for (const View& in : {z, t, ix, gl, loss, stats, dz}) check_apart(*this, v, in);
+    return (float2*)ws;
   }
   void output(const View& o, bool in_place = false) {
     check_view(*this, o);
@@ -333,22 +335,22 @@ size_t dion_distill_topk_workspace_size(int64_t rows, int32_t vocab, int32_t k, 
     (void)guarded([&]() { return set_error(DION_E_INVAL, "rows, vocab, k or dtype out of range"); });
     return 0;
   }
-  return std::max<size_t>(256, distill_scratch(rows, vocab, k, dtype, gradient != 0));
+  return reported_size(distill_scratch(rows, vocab, k, dtype, gradient != 0));
 }
 
 int dion_distill_topk(const void* logits, int64_t ldz, const void* teacher, const void* teacher_idx, float* loss,
                       float* stats, int64_t rows, int32_t vocab, int32_t k, int32_t dtype, int32_t teacher_dtype,
                       int32_t idx_bytes, float temperature, void* workspace, size_t workspace_bytes, void* stream) {
   return guarded([&]() {
-    const DistillArgs a{logits, teacher, teacher_idx, nullptr, loss, (float2*)stats, nullptr, ldz, 0, rows, vocab, k,
-                        teacher_dtype, idx_bytes == 8, temperature, (float2*)workspace, nullptr, 0};
+    DistillArgs a{logits, teacher, teacher_idx, nullptr, loss, (float2*)stats, nullptr, ldz, 0, rows, vocab, k,
+                  teacher_dtype, idx_bytes == 8, temperature, nullptr, nullptr, 0};
     DistillCheck c(a, dtype, idx_bytes);
     if (c.code != DION_OK) return c.done();
     c.output(c.loss);
     c.output(c.stats);
     c.need((uintptr_t)stats % 8 == 0, "stats must be 8-byte aligned");
     check_apart(c, c.loss, c.stats);
-    c.workspace(workspace, workspace_bytes, dion_distill_topk_workspace_size(rows, vocab, k, dtype, 0));
+    a.parts = c.workspace(workspace, workspace_bytes, dion_distill_topk_workspace_size(rows, vocab, k, dtype, 0));
     if (c.code != DION_OK || rows == 0) return c.done();
     const hipStream_t st = (hipStream_t)stream;
     return run_phase("distill_topk", "dion::k_distill_forward", 4.0 * rows * vocab,
@@ -381,14 +383,14 @@ int dion_distill_topk_step(const void* logits, int64_t ldz, const void* teacher,
                            int32_t vocab, int32_t k, int32_t dtype, int32_t teacher_dtype, int32_t idx_bytes,
                            float temperature, void* workspace, size_t workspace_bytes, void* stream) {
   return guarded([&]() {
-    const DistillArgs a{logits, teacher, teacher_idx, grad_loss, loss, nullptr, dlogits, ldz, ldd, rows,
-                        vocab, k, teacher_dtype, idx_bytes == 8, temperature, (float2*)workspace, nullptr, 0};
+    DistillArgs a{logits, teacher, teacher_idx, grad_loss, loss, nullptr, dlogits, ldz, ldd, rows,
+                  vocab, k, teacher_dtype, idx_bytes == 8, temperature, nullptr, nullptr, 0};
     DistillCheck c(a, dtype, idx_bytes);
     if (c.code != DION_OK) return c.done();
     c.output(c.loss);
     c.output(c.dz, true);
     check_apart(c, c.dz, c.loss);
-    c.workspace(workspace, workspace_bytes, dion_distill_topk_workspace_size(rows, vocab, k, dtype, 1));
+    a.parts = c.workspace(workspace, workspace_bytes, dion_distill_topk_workspace_size(rows, vocab, k, dtype, 1));
     if (c.code != DION_OK || rows == 0) return c.done();
     const hipStream_t st = (hipStream_t)stream;
     return run_phase("distill_topk_step", "dion::k_distill_step", 8.0 * rows * vocab,

@@ -10,6 +10,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from oracle import train_oracle as O  # noqa: E402
+from test_gpu_train_ops import distill_case, distill_check  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -50,3 +51,13 @@ def test_int8_linear_with_little_scratch(dion, m, n, k, start):
     one = torch.ones(max(m, n), device="cuda")
     y = dion.int8_linear(a, one[:m], b, one[:n], out_dtype=torch.float32)
     assert torch.equal(y, (a.double() @ b.double().t()).float())
+
+
+# ---------------------------------------------------------------- distillation
+@pytest.mark.parametrize("rows,vocab,k,dt", [(1, 128256, 32, torch.bfloat16), (2, 128256, 1, torch.float16),
+                                             (1, 70001, 8, torch.float32), (1, 90000, 4, torch.float32)])
+def test_distill_with_little_scratch(dion, rows, vocab, k, dt):
+    """The parts of the shared rows take 256 bytes at most."""
+    z, t, idx = distill_case(rows, vocab, k, dt, torch.float32)
+    idx[0, 0] = 5
+    distill_check(dion, z, t, idx, 1.5, torch.rand(rows, device="cuda") + 0.5)

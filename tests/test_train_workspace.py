@@ -25,3 +25,31 @@ def test_little_scratch_of_a_product_is_asked_for_and_checked(m, n, k, b, ldb):
     assert call(None, 0) == WORKSPACE and call(None, need) == WORKSPACE
     assert call(H, 0) == WORKSPACE and call(H, need - 1) == WORKSPACE and call(H + 16, need) == WORKSPACE
     assert call(A, need) == INVAL   # on top of an operand
+
+
+# a few long rows in shares, whose parts fit 256 bytes
+@pytest.mark.parametrize("rows,vocab,k,dt", [(1, 128256, 32, BF16), (1, 131072, 32, BF16), (2, 128256, 1, BF16),
+                                             (1, 70001, 8, FP32)])
+def test_little_scratch_of_a_distillation_step_is_asked_for_and_checked(rows, vocab, k, dt):
+    need = lib.dion_distill_topk_workspace_size(rows, vocab, k, dt, 1)
+    assert need > 256
+
+    def call(ws, have):
+        return lib.dion_distill_topk_step(A, vocab, B, C, None, D, E, vocab, rows, vocab, k, dt, BF16, 8, 1.0, ws, have,
+                                          None)
+
+    assert call(None, 0) == WORKSPACE and call(None, need) == WORKSPACE
+    assert call(H, 0) == WORKSPACE and call(H, need - 1) == WORKSPACE and call(H + 16, need) == WORKSPACE
+    assert call(A, need) == INVAL   # on top of the logits
+
+
+def test_little_scratch_of_a_distillation_loss_is_asked_for_and_checked():
+    rows, vocab, k = 1, 90000, 4
+    need = lib.dion_distill_topk_workspace_size(rows, vocab, k, FP32, 0)
+    assert need > 256
+
+    def call(ws, have):
+        return lib.dion_distill_topk(A, vocab, B, C, D, E, rows, vocab, k, FP32, BF16, 8, 1.0, ws, have, None)
+
+    assert call(None, 0) == WORKSPACE and call(H, need - 1) == WORKSPACE and call(H + 16, need) == WORKSPACE
+    assert call(A, need) == INVAL
