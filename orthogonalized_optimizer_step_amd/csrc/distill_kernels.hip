@@ -10,11 +10,12 @@
 // A row with no present entry has loss 0 and gradient 0, whatever z holds; a
 // row whose loss has gradient gl = 0 has gradient 0.
 //
-// With c = log2(e) / T an exponential is 2^(z c - R), R = fl(m c), one fma and
-// one v_exp_f32: m need only be near the largest logit, and the rounding of R
-// is the same in every term and cancels in q and in the loss.  Where |m c|
-// reaches 2^20 (a row whose largest is a mask's value) that rounding would
-// not stay small, and 2^((z - m) c) is formed instead.
+// With c = log2(e) / T an exponential is 2^(z c - R), R = fl(m c): a fma and a
+// v_exp_f32.  m need only be near the largest logit, and the rounding of R is
+// the same in every term and cancels in q and in the loss.  Where |m c|
+// reaches 2^20 (the largest of a row, or of what a thread has seen of it, is a
+// mask's value) that rounding would not stay small: it would make infinite
+// terms.  2^((z - m) c) is formed there instead.
 #include <algorithm>
 
 #include "train_device.h"
@@ -29,22 +30,26 @@ constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// Exponentials relative to the reference m.
+// Exponentials relative to the reference m: 2^((z - a) c - b), with a = 0 and
+// b = R where R is small, a = m and b = 0 where it is not.  Sums relative to
+// either kind meet exactly in of().
 struct Ref {
-  float m, c, R;
+  float m, c, a, b;
   bool wide, none;   // none: of nothing but -inf (a sum of 0)
   __device__ __forceinline__ Ref(float m_, float c_) : m(m_ == NEG ? 0.f : m_), c(c_), none(m_ == NEG) {
-    R = m * c;
+    const float R = m * c;
     wide = !(fabsf(R) < 0x1p20f);
+    a = wide ? m : 0.f;
+    b = wide ? 0.f : R;
   }
-  __device__ __forceinline__ float far(float z) const { return exp2_fast((z - m) * c); }   // any m
-  __device__ __forceinline__ float near(float z) const { return exp2_fast(fmaf(z, c, -R)); }   // !wide
-  __device__ __forceinline__ float operator()(float z) const { return wide ? far(z) : near(z); }
+  __device__ __forceinline__ float exponent(float z) const { return fmaf(z - a, c, -b); }
+  __device__ __forceinline__ float operator()(float z) const { return exp2_fast(exponent(z)); }
+  __device__ __forceinline__ float near(float z) const { return exp2_fast(fmaf(z, c, -b)); }   // the same where !wide
   // log of the same
-  __device__ __forceinline__ float log(float z) const { return (wide ? (z - m) * c : fmaf(z, c, -R)) * LN2; }
+  __device__ __forceinline__ float log(float z) const { return exponent(z) * LN2; }
   // what a sum relative to `o` is worth here
   __device__ __forceinline__ float of(const Ref& o) const {
-    return o.none ? 0.f : exp2_fast(wide ? (o.m - m) * c : o.R - R);
+    return o.none ? 0.f : exp2_fast(fmaf(o.a - a, c, o.b - b));
   }
 };
 
@@ -213,13 +218,13 @@ __device__ __forceinline__ void write_fixes(const DistillArgs& a, const Teacher<
 }
 
 // The running largest value and sum of elements [lo, hi) of a row, by the
-// block's threads.
-template <typename Z, int NT>
+// block's threads, AHEAD chunks at once.
+template <typename Z, int NT, int AHEAD = 4>
 __device__ __forceinline__ void stream_sum(const Z* z, int lo, int hi, float c, float& m, float& s) {
   typedef Chunk<Z> C;
   m = NEG;
   s = 0.f;
-#pragma unroll 4
+#pragma unroll AHEAD
   for (int j = lo + (int)threadIdx.x * C::N; j < hi; j += NT * C::N) {
     const uintx4 v = C::load(z, j, hi, NEG);
     float f[C::N];
@@ -406,8 +411,12 @@ __global__ __launch_bounds__(NT, NT * BLOCKS / 256) void k_distill_step(DistillA
     if (i < NC) data[i] = *(const uintx4u*)(z + i * STEP + j0);
     else tail = C::load(z, jt, a.vocab, NEG);
   };
-  // the running largest value and the sum relative to it
-  float m = NEG, s = 0.f;
+  // The running largest value and the sum relative to it, from a floor on: a
+  // thread whose first chunks are masked starts from the floor's reference, by
+  // which they are 0, and not from one of the mask's size.  (8192 x 128256 bf16:
+  // 887 us; 901 with a Ref's way for such sizes in every term.)
+  const auto floor = [&]() { return fmaxf(-(0x1p19f * LN2) * a.temp, -3.402823466e+38f); };
+  float m = floor(), mR = m * c, s = 0.f;
   auto absorb = [&](uintx4& d) {
     float v[C::N];
     values(d, v);
@@ -415,12 +424,14 @@ __global__ __launch_bounds__(NT, NT * BLOCKS / 256) void k_distill_step(DistillA
 #pragma unroll
     for (int e = 0; e < C::N; e += 2) cm = max3(cm, v[e], v[e + 1]);
     if (cm > m) {
-      s *= Ref(cm, c).of(Ref(m, c));
+#pragma clang fp contract(off)   // R is rounded first
+      const float R = cm * c;
+      s *= exp2_fast(mR - R);
+      mR = R;
       m = cm;
     }
-    const Ref r(m, c);
 #pragma unroll
-    for (int e = 0; e < C::N; ++e) s += r.near(v[e]);
+    for (int e = 0; e < C::N; ++e) s += exp2_fast(fmaf(v[e], c, -mR));
   };
   Entries<NT> E, En;
   int64_t row = blockIdx.x;
@@ -456,17 +467,11 @@ __global__ __launch_bounds__(NT, NT * BLOCKS / 256) void k_distill_step(DistillA
     float k = 0.f;
     bool zero = true;
     if (live) {
-      const Ref r(m, c);
-      if (__any(r.wide)) {   // a largest of a mask's value: rare, so from memory again
-        R.s = 0.f;
-        for (int j = j0; j < a.vocab; j += STEP) {
-          float v[C::N];
-          C::unpack(C::load(z, j, a.vocab, NEG), v);
-#pragma unroll
-          for (int e = 0; e < C::N; ++e) R.s += r(v[e]);
-        }
-      }
       R.template join<true>(a, E, T, c);
+      if (R.m == floor() || Ref(R.m, c).wide) {   // of masks' values alone, or as large: rare, so from memory again
+        stream_sum<Z, NT, 1>(z, 0, a.vocab, c, R.m, R.s);
+        R.template join<true>(a, E, T, c);
+      }
       R.fix(a, E, T, c, g * a.temp);
       const float part = wave_sum(R.loss(a, c));
       if ((tid & 63) == 0) T.wl[wave] = part;
@@ -487,12 +492,13 @@ __global__ __launch_bounds__(NT, NT * BLOCKS / 256) void k_distill_step(DistillA
         float v[C::N] = {};
         if (!zero) C::unpack(C::load(z, j, a.vocab, NEG), v);
 #pragma unroll
-        for (int e = 0; e < C::N; ++e) v[e] = zero ? 0.f : r.far(v[e]) * k;
+        for (int e = 0; e < C::N; ++e) v[e] = zero ? 0.f : r(v[e]) * k;
         C::store(dz, j, a.vocab, v);
       }
     }
     if (live_next) Rn.gather(a, En, zn, 0, a.vocab);
-    m = NEG;
+    m = floor();
+    mR = m * c;
     s = 0.f;
     auto write = [&](uintx4& d, int i) {
       float v[C::N];

@@ -61,3 +61,34 @@ def test_distill_with_little_scratch(dion, rows, vocab, k, dt):
     z, t, idx = distill_case(rows, vocab, k, dt, torch.float32)
     idx[0, 0] = 5
     distill_check(dion, z, t, idx, 1.5, torch.rand(rows, device="cuda") + 0.5)
+
+
+# one vocabulary for each way of holding a row, and one too long to hold
+MASKED = [(1001, 6, torch.bfloat16), (17001, 6, torch.bfloat16), (30000, 6, torch.float16), (60000, 6, torch.bfloat16),
+          (90000, 130, torch.bfloat16), (140001, 130, torch.bfloat16), (9000, 6, torch.float32),
+          (20001, 6, torch.float32), (31000, 6, torch.float32), (50000, 130, torch.float32)]
+
+
+@pytest.mark.parametrize("vocab,rows,dt", MASKED)
+@pytest.mark.parametrize("mask", ["lowest", -1e30, -1e20, -1e9, "-inf"])
+@pytest.mark.parametrize("temp", [0.5, 1.0, 4.0])
+def test_distill_masks_anywhere(dion, vocab, rows, dt, mask, temp):
+    """Masked runs at the front, in the middle, in every other 16 bytes, and everywhere but at the end of a row.  Their
+    exponentials are exactly 0 beside ordinary logits, in 64 bits as in 32."""
+    value = {"lowest": torch.finfo(dt).min, "-inf": float("-inf")}.get(mask, mask)
+    if isinstance(value, float) and value < torch.finfo(dt).min and mask != "-inf":
+        value = torch.finfo(dt).min
+    z, t, _ = distill_case(rows, vocab, 5, dt, torch.float32, seed=3)
+    chunk = 16 // z.element_size()
+    at = torch.arange(vocab, device="cuda")
+    hidden = [at < chunk, at < vocab // 2, (at >= vocab // 3) & (at < vocab // 3 + 40 * chunk), (at // chunk) % 2 == 0,
+              at < vocab - 7, (at >= chunk) & (at < vocab - chunk)]
+    idx = torch.empty((rows, 5), dtype=torch.int64, device="cuda")
+    for r in range(rows):
+        if r < 6 or r >= rows - 6:   # the rows between stay as they are
+            z[r, hidden[r % 6]] = value
+            idx[r] = at[~hidden[r % 6]][-5:]
+        else:
+            idx[r] = torch.randperm(vocab, device="cuda")[:5]
+    loss, d = distill_check(dion, z, t, idx, temp, torch.rand(rows, device="cuda") + 0.5)
+    assert torch.isfinite(loss).all() and torch.isfinite(d.float()).all()
