@@ -47,8 +47,11 @@ struct Ref {
   __device__ __forceinline__ float near(float z) const { return exp2_fast(fmaf(z, c, -b)); }   // the same where !wide
   // log of the same
   __device__ __forceinline__ float log(float z) const { return exponent(z) * LN2; }
-  // what a sum relative to `o` is worth here
+  // What a sum relative to `o` is worth here: by the rounded references, as its
+  // terms were formed.  (One fused from the products, m c - R, would be off by
+  // the rounding of R: 2^-5 where R is near 2^19, 2^-20 where it is near 20.)
   __device__ __forceinline__ float of(const Ref& o) const {
+#pragma clang fp contract(off)
     return o.none ? 0.f : exp2_fast(fmaf(o.a - a, c, o.b - b));
   }
 };

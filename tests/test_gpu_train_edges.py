@@ -92,3 +92,30 @@ def test_distill_masks_anywhere(dion, vocab, rows, dt, mask, temp):
             idx[r] = torch.randperm(vocab, device="cuda")[:5]
     loss, d = distill_check(dion, z, t, idx, temp, torch.rand(rows, device="cuda") + 0.5)
     assert torch.isfinite(loss).all() and torch.isfinite(d.float()).all()
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_distill_far_from_zero(dion, dt):
+    """A row's logits around a large value of either sign, so that the reference is on one side of 2^20 or the other:
+    they are exact in the type, and only their differences count."""
+    step = 4096.0 if dt == torch.bfloat16 else 1.0
+    base = torch.tensor([0.0, 2.0 ** 19, -2.0 ** 19, 2.0 ** 20 - 2 * step, 2.0 ** 20 + 2 * step, -2.0 ** 20 + 2 * step,
+                         -2.0 ** 20 - 2 * step, 2.0 ** 22], device="cuda")
+    vocab, k, temp = 9001, 6, 3.0 * step
+    steps = torch.randint(-3, 4, (8, vocab), generator=generator(5), device="cuda").float()
+    z = (base[:, None] + steps * step).to(dt)
+    assert torch.equal(z.float(), base[:, None] + steps * step) or dt == torch.bfloat16
+    t, idx = z.float().topk(k)
+    # D of the tolerance is a few units for all rows: the exponents are within 2 of one another
+    Z, T, I = n64(z), n64(t), idx.cpu().numpy()
+    ref, dz, _ = O.distill(Z, T, I, temp)
+    tol = temp ** 2 * (ACC + 2.0 ** -21 * 16)
+    loss, stats = dion.distill_topk(z, t, idx, temperature=temp)
+    step_loss, d = dion.distill_topk_step(z, t, idx, temperature=temp)
+    back = dion.distill_topk_backward(None, z, stats, t, idx, temperature=temp)
+    q = np.exp((Z - Z.max(1, keepdims=True)) / temp)
+    q /= q.sum(1, keepdims=True)
+    P = np.abs(q * temp - dz) / temp
+    dtol = U[dt] * np.abs(dz) + temp * (q * (ACC + 2.0 ** -21 * 16) + 2.0 ** -20 * P + 2.0 ** -21 * 4 * P)
+    for got, want, by in ((loss, ref, tol), (step_loss, ref, tol), (d, dz, dtol), (back, dz, dtol)):
+        assert (np.abs(n64(got) - want) <= by).all()
