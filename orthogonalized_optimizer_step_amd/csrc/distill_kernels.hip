@@ -119,7 +119,7 @@ template <typename Z, int NT> struct Row {
   static __device__ __forceinline__ bool has(const DistillArgs& a, int i) {
     return i * NT + (int)(threadIdx.x & ~63u) < a.k;
   }
-  float lp[KPT];     // log p of the thread's entries (NEG where p is 0)
+  float u[KPT];      // (t - top) / T of the thread's entries (NEG where absent)
   float zi[KPT];     // the student's logit there
 
   // Joins the threads' (m, s) (when FWD) and forms the teacher's distribution:
@@ -147,12 +147,11 @@ template <typename Z, int NT> struct Row {
       s = row_reduce<W>(lane < W ? T.ws[lane] * Ref(m, c).of(Ref(T.wm[lane], c)) : 0.f, 0.f, Add());
     }
     float es = 0.f;
-    const float it = 1.f / a.temp;
 #pragma unroll
     for (int i = 0; i < KPT; ++i) {
       if (has(a, i)) {
-        lp[i] = E.idx[i] >= 0 ? (E.t[i] - top) * it : NEG;
-        const float e = expf(lp[i]);
+        u[i] = E.idx[i] >= 0 ? (E.t[i] - top) / a.temp : NEG;
+        const float e = expf(u[i]);
         es += e;
         const int k = tid + i * NT;
         T.idx[k] = E.idx[i];
@@ -162,23 +161,22 @@ template <typename Z, int NT> struct Row {
     es = wave_sum(es);
     if ((tid & 63) == 0) T.we[wave] = es;
     lds_barrier();
-    es = join_sum<W>(T.we);
-    const float ls = logf(es);
-#pragma unroll
-    for (int i = 0; i < KPT; ++i)
-      if (has(a, i)) lp[i] = expf(lp[i] - ls) == 0.f ? NEG : lp[i] - ls;
-    inv_es = 1.f / es;
+    inv_es = 1.f / join_sum<W>(T.we);
   }
   float inv_es;
 
-  // this thread's share of the loss
-  __device__ __forceinline__ float loss(const DistillArgs& a, float c) const {
+  // This thread's share of the loss over T^2.  With u the exponents of either
+  // side it is sum p (u_t - u_z) + log(s / es): the logarithms of the two sums
+  // enter once, as one, and not rounded into every entry's.
+  __device__ __forceinline__ float loss(const DistillArgs& a, const Teacher<NT>& T, float c) const {
     const Ref r(m, c);
-    const float ls = logf(s);
-    float l = 0.f;
+    float l = threadIdx.x == 0 ? logf(s * inv_es) : 0.f;
 #pragma unroll
     for (int i = 0; i < KPT; ++i)
-      if (has(a, i) && lp[i] != NEG) l += expf(lp[i]) * (lp[i] - (r.log(zi[i]) - ls));
+      if (has(a, i)) {
+        const float p = T.e[threadIdx.x + i * NT] * inv_es;
+        if (p != 0.f) l += p * (u[i] - r.log(zi[i]));
+      }
     return l;
   }
 
@@ -341,7 +339,7 @@ __global__ __launch_bounds__(NT) void k_distill_rows(DistillArgs a) {
       R.template join<FWD>(a, E, T, c);
       if (BWD) R.fix(a, E, T, c, gt);
       if (joins) {
-        const float part = wave_sum(R.loss(a, c));
+        const float part = wave_sum(R.loss(a, T, c));
         if (lane == 0) T.wl[wave] = part;
       }
     }
@@ -476,7 +474,7 @@ __global__ __launch_bounds__(NT, NT * BLOCKS / 256) void k_distill_step(DistillA
         R.template join<true>(a, E, T, c);
       }
       R.fix(a, E, T, c, g * a.temp);
-      const float part = wave_sum(R.loss(a, c));
+      const float part = wave_sum(R.loss(a, T, c));
       if ((tid & 63) == 0) T.wl[wave] = part;
       k = g * a.temp / R.s;
       zero = g == 0.f;

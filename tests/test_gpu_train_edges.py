@@ -119,3 +119,34 @@ def test_distill_far_from_zero(dion, dt):
     dtol = U[dt] * np.abs(dz) + temp * (q * (ACC + 2.0 ** -21 * 16) + 2.0 ** -20 * P + 2.0 ** -21 * 4 * P)
     for got, want, by in ((loss, ref, tol), (step_loss, ref, tol), (d, dz, dtol), (back, dz, dtol)):
         assert (np.abs(n64(got) - want) <= by).all()
+
+
+@pytest.mark.parametrize("rows,vocab,k,temp,dt", [(1021, 32001, 100, 1.5, torch.float32), (700, 1499, 43, 1.0, torch.float16),
+                                                  (2000, 1461, 5, 0.5, torch.bfloat16), (900, 2449, 253, 1.0, torch.float32),
+                                                  (500, 50257, 64, 2.0, torch.bfloat16)])
+def test_distill_is_as_exact_as_elementary_operations_in_fp32(dion, rows, vocab, k, temp, dt):
+    """The error against 64 bits over all rows (2-norm) of the loss, and of an fp32 gradient, is no larger than 1.5 times
+    that of the formula in torch's fp32 operations, which round every step once: the kernels round no more often."""
+    g = generator(7)
+    z = torch.randn((rows, vocab), generator=g, device="cuda") * 2
+    idx = torch.rand((rows, vocab), generator=g, device="cuda").topk(k).indices
+    t = 14 - torch.rand((rows, k), generator=g, device="cuda").mul(1.2 * 12 / k).cumsum(1)
+    z.scatter_(1, idx, t - 3 + torch.randn((rows, k), generator=g, device="cuda"))
+    z = z.to(dt)
+
+    def formula(z, t):
+        u, v = (t - t.amax(1, keepdim=True)) / temp, (z - z.amax(1, keepdim=True)) / temp
+        p, logs = torch.softmax(u, 1), torch.log(torch.exp(v).sum(1, keepdim=True))
+        logp = u - torch.log(torch.exp(u).sum(1, keepdim=True))
+        loss = temp ** 2 * (p * (logp - (v.gather(1, idx) - logs))).sum(1)
+        return loss, temp * torch.exp(v - logs).scatter_add_(1, idx, -p)
+
+    exact, plain = formula(z.double(), t.double()), formula(z.float(), t)
+    loss, stats = dion.distill_topk(z, t, idx, temperature=temp)
+    step = dion.distill_topk_step(z, t, idx, temperature=temp)
+    got = [(loss, 0), (step[0], 0)]
+    if dt == torch.float32:
+        got += [(step[1], 1), (dion.distill_topk_backward(None, z, stats, t, idx, temperature=temp), 1)]
+    for value, i in got:
+        far = float((value.double() - exact[i]).norm())
+        assert far <= 1.5 * float((plain[i].double() - exact[i]).norm()), (i, far)
