@@ -285,7 +285,17 @@ def int8_linear(a, a_scale, b, b_scale, bias=None, out_dtype=torch.bfloat16, wor
 
 
 # ---------------------------------------------------------------- distillation
-def _distill_inputs(logits, teacher, teacher_idx):
+def _dense(t, stream):
+    """t itself, or a contiguous copy made on the stream that reads it"""
+    if stream is None or t.is_contiguous():
+        return t.contiguous()
+    with torch.cuda.stream(stream):
+        copy = t.contiguous()
+    t.record_stream(stream)
+    return copy
+
+
+def _distill_inputs(logits, teacher, teacher_idx, stream):
     dev = _device(logits, "logits")
     rows, vocab, ldz = _matrix(logits, "logits")
     code = _code(logits.dtype, "logits")
@@ -298,7 +308,7 @@ def _distill_inputs(logits, teacher, teacher_idx):
     tcode = _code(teacher.dtype, "teacher logits")
     if teacher_idx.dtype not in (torch.int64, torch.int32):
         _fail(f"teacher indices: unsupported dtype {teacher_idx.dtype}")
-    return (dev, rows, vocab, ldz, code, teacher.contiguous(), tcode, teacher_idx.contiguous(),
+    return (dev, rows, vocab, ldz, code, _dense(teacher, stream), tcode, _dense(teacher_idx, stream),
             teacher_idx.element_size(), shape[-1])
 
 
@@ -321,7 +331,7 @@ def distill_topk(logits, teacher, teacher_idx, temperature=1.0, workspace=None, 
     entries and q that of logits / T over the vocabulary; entries with an index
     outside the vocabulary or a logit of -inf are absent, and a row without any
     has loss and gradient 0.  ``stats`` is for ``distill_topk_backward``."""
-    dev, rows, vocab, ldz, code, t, tcode, idx, ib, k = _distill_inputs(logits, teacher, teacher_idx)
+    dev, rows, vocab, ldz, code, t, tcode, idx, ib, k = _distill_inputs(logits, teacher, teacher_idx, stream)
     keep, ws, have = _scratch(lib.dion_distill_topk_workspace_size(rows, vocab, k, code, 0), logits, workspace, stream)
     loss = _new(logits.shape[:-1], torch.float32, logits, stream)
     stats = _new((*logits.shape[:-1], 2), torch.float32, logits, stream)
@@ -336,7 +346,7 @@ def distill_topk(logits, teacher, teacher_idx, temperature=1.0, workspace=None, 
 def distill_topk_backward(grad_loss, logits, stats, teacher, teacher_idx, temperature=1.0, out=None, stream=None):
     """Gradient of the logits from ``distill_topk``'s stats and the gradient of
     each row's loss (None: 1).  ``out`` may be the logits themselves."""
-    dev, rows, vocab, ldz, code, t, tcode, idx, ib, k = _distill_inputs(logits, teacher, teacher_idx)
+    dev, rows, vocab, ldz, code, t, tcode, idx, ib, k = _distill_inputs(logits, teacher, teacher_idx, stream)
     if grad_loss is not None:
         _vector(grad_loss, "grad_loss", rows, _F32, dev)
     _vector(stats, "stats", 2 * rows, _F32, dev)
@@ -355,7 +365,7 @@ def distill_topk_step(logits, teacher, teacher_idx, grad_loss=None, temperature=
     """Loss and gradient in one call, for a ``grad_loss`` known ahead (such as
     one over the number of tokens; None: 1): returns (loss, dlogits).
     ``out`` may be the logits themselves."""
-    dev, rows, vocab, ldz, code, t, tcode, idx, ib, k = _distill_inputs(logits, teacher, teacher_idx)
+    dev, rows, vocab, ldz, code, t, tcode, idx, ib, k = _distill_inputs(logits, teacher, teacher_idx, stream)
     if grad_loss is not None:
         _vector(grad_loss, "grad_loss", rows, _F32, dev)
     keep, ws, have = _scratch(lib.dion_distill_topk_workspace_size(rows, vocab, k, code, 1), logits, workspace, stream)

@@ -150,3 +150,25 @@ def test_distill_is_as_exact_as_elementary_operations_in_fp32(dion, rows, vocab,
     for value, i in got:
         far = float((value.double() - exact[i]).norm())
         assert far <= 1.5 * float((plain[i].double() - exact[i]).norm()), (i, far)
+
+
+def test_distill_teacher_views_on_another_stream(dion):
+    """Teacher tensors that are slices are copied on the stream that reads them: the call orders itself after nothing
+    that the caller's own stream still has before it."""
+    rows, vocab, k = 64, 5000, 7
+    z, t, idx = distill_case(rows, vocab, 2 * k, torch.bfloat16, torch.float32)
+    tc, ic = t[:, :k].contiguous(), idx[:, :k].contiguous()
+    stats = dion.distill_topk(z, tc, ic)[1]
+    busy = torch.randn(8192, 8192, device="cuda")
+    side = torch.cuda.Stream()
+    calls = (lambda t, i, s: dion.distill_topk_step(z, t, i, stream=s),
+             lambda t, i, s: (*dion.distill_topk(z, t, i, stream=s),
+                              dion.distill_topk_backward(None, z, stats, t, i, stream=s)))
+    for call in calls:
+        want = call(tc, ic, None)
+        torch.cuda.synchronize()   # the inputs are there for every stream
+        for _ in range(20):   # 20 ms and more on the current stream
+            busy = busy @ busy * 1e-3
+        got = call(t[:, :k], idx[:, :k], side)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))

@@ -1,0 +1,48 @@
+"""The Python binding of the training-step operators without a GPU: what it does around its calls."""
+import contextlib
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import orthogonalized_optimizer_step_amd.train_ops as T  # noqa: E402
+
+
+class Sliced:
+    """A tensor that is not contiguous, and says on which stream it is copied and which streams use it."""
+
+    def __init__(self, dtype, streams, log):
+        self.shape, self.dtype, self.streams, self.log = (4, 3), dtype, streams, log
+
+    def is_contiguous(self):
+        return False
+
+    def contiguous(self):
+        self.log.append(("copied", self.streams[-1]))
+        return self
+
+    def record_stream(self, stream):
+        self.log.append(("used", stream))
+
+    def element_size(self):
+        return 8
+
+
+@pytest.mark.parametrize("stream", [None, "side"])
+def test_teacher_copies_are_made_on_the_stream_that_reads_them(monkeypatch, stream):
+    streams, log = ["current"], []
+
+    @contextlib.contextmanager
+    def on(s):
+        streams.append(s)
+        yield
+        streams.pop()
+
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(T, "_device", lambda *a: 0)
+    monkeypatch.setattr(T, "_beside", lambda *a: None)
+    monkeypatch.setattr(T, "_matrix", lambda *a: (4, 9, 9))
+    T._distill_inputs(torch.zeros(4, 9), Sliced(torch.float32, streams, log), Sliced(torch.int64, streams, log), stream)
+    where = stream or "current"
+    assert [s for what, s in log if what == "copied"] == [where, where]
+    assert [s for what, s in log if what == "used"] == ([] if stream is None else [stream, stream])
