@@ -381,6 +381,24 @@ def distill_topk_step(logits, teacher, teacher_idx, grad_loss=None, temperature=
 
 
 # ------------------------------------------------------------------- autograd
+class _Gradient(torch.autograd.Function):
+    """A gradient as a function of what it depends on, whose own derivative is refused."""
+
+    @staticmethod
+    def forward(ctx, compute, *tensors):
+        return compute(*tensors)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("trying to differentiate twice: rms_norm and distill_loss have first derivatives only")
+
+
+def _once(compute, *tensors):
+    """compute(*tensors), the gradients of a backward pass.  Where a graph of that pass is asked for (create_graph),
+    they carry one that raises: without it a second derivative would be missing silently."""
+    return _Gradient.apply(compute, *tensors) if torch.is_grad_enabled() else compute(*tensors)
+
+
 class _RmsNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, residual, eps):
@@ -392,12 +410,14 @@ class _RmsNorm(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dy, dh=None):
         h, weight, rstd = ctx.saved_tensors
-        dx, dw = rmsnorm_backward(dy.contiguous(), h, weight, rstd, None if dh is None else dh.contiguous())
+        dx, dw = _once(lambda dy, h, weight, dh: rmsnorm_backward(dy.contiguous(), h, weight, rstd,
+                                                                  None if dh is None else dh.contiguous()),
+                       dy, h, weight, dh)
         return dx, dw, (dx if ctx.residual else None), None
 
 
 def rms_norm(x, weight, residual=None, eps=1e-6):
-    """``rmsnorm`` for automatic differentiation: returns y, or (y, h) with a residual."""
+    """``rmsnorm`` for automatic differentiation, once: returns y, or (y, h) with a residual."""
     return _RmsNorm.apply(x, weight, residual, eps)
 
 
@@ -412,10 +432,12 @@ class _DistillLoss(torch.autograd.Function):
     @staticmethod
     def backward(ctx, grad):
         logits, stats, teacher, idx = ctx.saved_tensors
-        return (distill_topk_backward(grad.contiguous(), logits, stats, teacher, idx, ctx.temperature), None, None,
-                None)
+        dlogits = _once(lambda grad, logits: distill_topk_backward(grad.contiguous(), logits, stats, teacher, idx,
+                                                                   ctx.temperature), grad, logits)
+        return dlogits, None, None, None
 
 
 def distill_loss(logits, teacher, teacher_idx, temperature=1.0):
-    """``distill_topk`` for automatic differentiation: the loss of each row."""
+    """``distill_topk`` for automatic differentiation, once: the loss of each row.
+    The logits get a gradient, the teacher's do not."""
     return _DistillLoss.apply(logits, teacher, teacher_idx, temperature)

@@ -172,3 +172,19 @@ def test_distill_teacher_views_on_another_stream(dion):
         got = call(t[:, :k], idx[:, :k], side)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ------------------------------------------------------- automatic differentiation
+def test_second_derivatives_are_refused(dion):
+    """A penalty on a gradient beside another path: it must not train without the penalty, silently."""
+    x = torch.randn(4, 64, device="cuda", requires_grad=True)
+    w = torch.ones(64, device="cuda", requires_grad=True)
+    r = torch.randn(4, 64, device="cuda", requires_grad=True)
+    t, idx = torch.randn(4, 64, device="cuda").topk(5)
+    for f in (lambda: dion.distill_loss(x, t, idx).sum(), lambda: dion.rms_norm(x, w).pow(2).sum(),
+              lambda: sum(v.pow(2).sum() for v in dion.rms_norm(x, w, r))):
+        loss = f() + (x ** 3).sum()
+        grad, = torch.autograd.grad(loss, x, create_graph=True)
+        with pytest.raises(RuntimeError, match="differentiate twice"):
+            (loss + grad.pow(2).sum()).backward()
+        f().backward()   # once is as before
