@@ -303,17 +303,20 @@ __global__ __launch_bounds__(64 * WM * WN) void k_int8_mma(Int8Args g, int* part
   }
 }
 
-// The splits' sums, scaled.
+// The splits' sums, scaled.  Tokens lie along y and z of the grid, which have
+// 65536 blocks at most each.
 template <typename O> __global__ __launch_bounds__(256) void k_int8_join(Int8Args g, const int* partial, int splits) {
-  const int64_t row = blockIdx.y, col = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (col >= g.n) return;
+  const int64_t col = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t row = (int64_t)blockIdx.z * gridDim.y + blockIdx.y;
+  if (col >= g.n || row >= g.m) return;
   int v = 0;
   for (int s = 0; s < splits; ++s) v += partial[((int64_t)s * g.m + row) * g.n + col];
   ((O*)g.out)[row * g.ldo + col] = from_f<O>(scaled(g, row, col, v));
 }
 
 void launch_join(const Int8Args& a, int splits, hipStream_t s) {
-  const dim3 grid((unsigned)((a.n + 255) / 256), (unsigned)a.m);
+  const int64_t y = std::min<int64_t>(a.m, 1 << 15);
+  const dim3 grid((unsigned)((a.n + 255) / 256), (unsigned)y, (unsigned)((a.m + y - 1) / y));
   if (a.out_fmt == 1) hipLaunchKernelGGL((k_int8_join<float>), grid, dim3(256), 0, s, a, a.partial, splits);
   else if (a.out_fmt == 0) hipLaunchKernelGGL((k_int8_join<bf16_t>), grid, dim3(256), 0, s, a, a.partial, splits);
   else hipLaunchKernelGGL((k_int8_join<fp16_t>), grid, dim3(256), 0, s, a, a.partial, splits);

@@ -53,6 +53,16 @@ def test_int8_linear_with_little_scratch(dion, m, n, k, start):
     assert torch.equal(y, (a.double() @ b.double().t()).float())
 
 
+@pytest.mark.parametrize("m,n,k", [(70000, 64, 14336), (70001, 3, 8192)])
+def test_int8_linear_joins_the_splits_of_many_tokens(dion, m, n, k):
+    """More tokens than a grid has rows of blocks, k in splits."""
+    a, b = codes(1, (m, k)), codes(2, (n, k))
+    one = torch.ones(m, device="cuda")
+    y = dion.int8_linear(a, one, b, one[:n], out_dtype=torch.float32)
+    for rows in (slice(0, 100), slice(32700, 32800), slice(65500, 65600), slice(m - 100, m)):
+        assert torch.equal(y[rows], (a[rows].double() @ b.double().t()).float())
+
+
 # ---------------------------------------------------------------- distillation
 @pytest.mark.parametrize("rows,vocab,k,dt", [(1, 128256, 32, torch.bfloat16), (2, 128256, 1, torch.float16),
                                              (1, 70001, 8, torch.float32), (1, 90000, 4, torch.float32)])
