@@ -218,29 +218,32 @@ __global__ __launch_bounds__(1024) void k_rmsnorm_long(NormArgs a, bool w32) {
   }
 }
 
-// y = q scale, 16 codes a thread
+// y = q scale, 16 codes a thread.  A row's blocks lie along y and z of the grid,
+// which have 65536 at most each; offsets are taken from the thread's first
+// element, where they stay small at any length of row.
 template <typename T>
 __global__ __launch_bounds__(256) void k_int8_dequantize(const int8_t* q, int64_t ldq, const float* scale, T* y,
                                                          int64_t ldy, int64_t rows, int cols) {
   typedef Chunk<T> C;
-  const int j = ((int)blockIdx.y * 256 + (int)threadIdx.x) * 16;
+  const int64_t j = (((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * 256 + threadIdx.x) * 16;
   if (j >= cols) return;
+  const int left = cols - (int)j;   // of the row
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
-    const int8_t* src = q + row * ldq;
+    const int8_t* src = q + row * ldq + j;
     const float s = scale[row];
     int8_t c[16];
-    if (j + 16 <= cols) {
-      __builtin_memcpy(c, src + j, 16);
+    if (left >= 16) {
+      __builtin_memcpy(c, src, 16);
     } else {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) c[e] = j + e < cols ? src[j + e] : 0;
+      for (int e = 0; e < 16; ++e) c[e] = e < left ? src[e] : 0;
     }
     float f[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) f[e] = (float)c[e] * s;
 #pragma unroll
     for (int e = 0; e < 16; e += C::N)
-      if (j + e < cols) C::store_near(y + row * ldy, j + e, cols, f + e);
+      if (e < left) C::store_near(y + row * ldy + j, e, left, f + e);
   }
 }
 
@@ -526,7 +529,8 @@ void launch_rmsnorm_backward(int fmt, int wfmt, const NormBackArgs& a, hipStream
 
 void launch_int8_dequantize(int fmt, const int8_t* q, int64_t ldq, const float* scale, void* y, int64_t ldy,
                             int64_t rows, int cols, hipStream_t s) {
-  const dim3 g((unsigned)std::min<int64_t>(rows, 1 << 20), (unsigned)((cols + 4095) / 4096)), b(256);
+  const int64_t blocks = ((int64_t)cols + 4095) / 4096, gy = std::min<int64_t>(blocks, 1 << 15);
+  const dim3 g((unsigned)std::min<int64_t>(rows, 1 << 20), (unsigned)gy, (unsigned)((blocks + gy - 1) / gy)), b(256);
   if (fmt == 1) hipLaunchKernelGGL((k_int8_dequantize<float>), g, b, 0, s, q, ldq, scale, (float*)y, ldy, rows, cols);
   else if (fmt == 0) hipLaunchKernelGGL((k_int8_dequantize<bf16_t>), g, b, 0, s, q, ldq, scale, (bf16_t*)y, ldy, rows, cols);
   else hipLaunchKernelGGL((k_int8_dequantize<fp16_t>), g, b, 0, s, q, ldq, scale, (fp16_t*)y, ldy, rows, cols);

@@ -63,6 +63,15 @@ def test_int8_linear_joins_the_splits_of_many_tokens(dion, m, n, k):
         assert torch.equal(y[rows], (a[rows].double() @ b.double().t()).float())
 
 
+@pytest.mark.parametrize("cols", [(1 << 28) + 5, (1 << 31) - 1])
+def test_dequantize_the_longest_rows(dion, cols):
+    """More blocks than a grid has along one dimension, and the last elements that 32-bit indexes reach."""
+    q = codes(3, (1, cols))
+    y = dion.int8_dequantize(q, torch.full((1,), 0.5, device="cuda"))
+    for lo in (0, (1 << 27) - 50, (1 << 28) - 50, cols // 2, cols - 5000):
+        assert torch.equal(y[0, lo:lo + 5000].float(), q[0, lo:lo + 5000].float() * 0.5)
+
+
 # ---------------------------------------------------------------- distillation
 @pytest.mark.parametrize("rows,vocab,k,dt", [(1, 128256, 32, torch.bfloat16), (2, 128256, 1, torch.float16),
                                              (1, 70001, 8, torch.float32), (1, 90000, 4, torch.float32)])
