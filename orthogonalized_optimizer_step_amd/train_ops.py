@@ -399,6 +399,17 @@ def _once(compute, *tensors):
     return _Gradient.apply(compute, *tensors) if torch.is_grad_enabled() else compute(*tensors)
 
 
+def _rows(t):
+    """t, or a contiguous copy where it is no matrix of rows that the operators take (transposed, expanded)"""
+    if not isinstance(t, torch.Tensor) or t.is_contiguous():
+        return t
+    try:
+        _, cols, ld = _matrix(t, "")
+    except DionError:
+        return t.contiguous()
+    return t if ld >= cols else t.contiguous()
+
+
 class _RmsNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, residual, eps):
@@ -417,8 +428,9 @@ class _RmsNorm(torch.autograd.Function):
 
 
 def rms_norm(x, weight, residual=None, eps=1e-6):
-    """``rmsnorm`` for automatic differentiation, once: returns y, or (y, h) with a residual."""
-    return _RmsNorm.apply(x, weight, residual, eps)
+    """``rmsnorm`` for automatic differentiation, once: returns y, or (y, h) with a residual.
+    Tensors of any strides; what does not lie in rows is copied first."""
+    return _RmsNorm.apply(_rows(x), _rows(weight), _rows(residual), eps)
 
 
 class _DistillLoss(torch.autograd.Function):
@@ -439,5 +451,6 @@ class _DistillLoss(torch.autograd.Function):
 
 def distill_loss(logits, teacher, teacher_idx, temperature=1.0):
     """``distill_topk`` for automatic differentiation, once: the loss of each row.
-    The logits get a gradient, the teacher's do not."""
-    return _DistillLoss.apply(logits, teacher, teacher_idx, temperature)
+    The logits get a gradient, the teacher's do not.  Tensors of any strides, as
+    for ``rms_norm``."""
+    return _DistillLoss.apply(_rows(logits), teacher, teacher_idx, temperature)

@@ -207,3 +207,26 @@ def test_second_derivatives_are_refused(dion):
         with pytest.raises(RuntimeError, match="differentiate twice"):
             (loss + grad.pow(2).sum()).backward()
         f().backward()   # once is as before
+
+
+def test_autograd_functions_take_any_strides(dion):
+    """Transposed, permuted, expanded and sliced activations give what their contiguous copies give, gradients included."""
+    base = torch.randn(6, 10, 64, device="cuda")
+    w = torch.randn(128, device="cuda")[::2]
+    views = [lambda b: b[0, :, :].t(), lambda b: b.permute(1, 0, 2), lambda b: b[:, :1, :].expand(6, 10, 64),
+             lambda b: b[..., ::2], lambda b: b[:, 3, :40], lambda b: b]
+    for view in views:
+        t, idx = torch.randn(view(base).shape, device="cuda").topk(3)
+        for f in (lambda x, w: dion.rms_norm(x, w).pow(2).sum(),
+                  lambda x, w: sum(v.pow(2).sum() for v in dion.rms_norm(x, w, (x * 0.5).contiguous())),
+                  lambda x, w: sum(v.pow(2).sum() for v in dion.rms_norm(x.contiguous(), w, x)),
+                  lambda x, w: dion.distill_loss(x, t, idx, 2.0).sum()):
+            got = []
+            for dense in (False, True):
+                b, v = base.clone().requires_grad_(), w[:view(base).shape[-1]]
+                v = v if v.numel() == view(base).shape[-1] else torch.ones(view(base).shape[-1], device="cuda")
+                x = view(b)
+                y = f(x.contiguous() if dense else x, v.contiguous() if dense else v)
+                y.backward()
+                got.append((y.detach(), b.grad))
+            assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
