@@ -416,11 +416,14 @@ class _RmsNorm(torch.autograd.Function):
         y, h, rstd = rmsnorm(x, weight, residual, eps)
         ctx.save_for_backward(h, weight, rstd)
         ctx.residual = residual is not None
+        ctx.set_materialize_grads(False)   # an output that nothing used sends None, not zeros to be read
         return (y, h) if ctx.residual else y
 
     @staticmethod
     def backward(ctx, dy, dh=None):
         h, weight, rstd = ctx.saved_tensors
+        if dy is None:
+            return dh, None, dh, None
         dx, dw = _once(lambda dy, h, weight, dh: rmsnorm_backward(dy.contiguous(), h, weight, rstd,
                                                                   None if dh is None else dh.contiguous()),
                        dy, h, weight, dh)

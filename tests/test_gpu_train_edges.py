@@ -230,3 +230,18 @@ def test_autograd_functions_take_any_strides(dion):
                 y.backward()
                 got.append((y.detach(), b.grad))
             assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+def test_rms_norm_with_an_unused_output(dion, monkeypatch):
+    """Either output alone: the other's gradient is absent, not a tensor of zeros that the kernel reads."""
+    import orthogonalized_optimizer_step_amd.train_ops as T
+    seen, inner = [], T.rmsnorm_backward
+    monkeypatch.setattr(T, "rmsnorm_backward", lambda dy, h, w, rstd, dh=None: seen.append(dh is None) or inner(dy, h, w, rstd, dh))
+    x, r, w = (torch.randn(s, device="cuda", requires_grad=True) for s in ((5, 48), (5, 48), (48,)))
+    g = torch.randn(5, 48, device="cuda")
+    dx, dr, dw = torch.autograd.grad(dion.rms_norm(x, w, r)[0], (x, r, w), g)
+    _, h, rstd = dion.rmsnorm(x.detach(), w.detach(), residual=r.detach())
+    want = inner(g, h, w.detach(), rstd)
+    assert seen == [True] and torch.equal(dx, want[0]) and torch.equal(dr, want[0]) and torch.equal(dw, want[1])
+    dx, dr, dw = torch.autograd.grad(dion.rms_norm(x, w, r)[1], (x, r, w), g, allow_unused=True)
+    assert seen == [True] and torch.equal(dx, g) and torch.equal(dr, g) and dw is None
