@@ -67,7 +67,7 @@ def _matrix(t, what):
         if len(shape) == 0:
             _fail(f"{what} must have at least one dimension")
         try:
-            t = t.view(-1, shape[-1]) if t.numel() else t.reshape(t.numel() // max(1, shape[-1]), shape[-1])
+            t = t.view(-1, shape[-1]) if t.numel() else t.reshape(shape[:-1].numel(), shape[-1])
         except RuntimeError:
             _fail(f"{what}: the leading dimensions do not flatten into equally spaced rows")
     rows, cols = t.shape

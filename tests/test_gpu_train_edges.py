@@ -72,6 +72,17 @@ def test_dequantize_the_longest_rows(dion, cols):
         assert torch.equal(y[0, lo:lo + 5000].float(), q[0, lo:lo + 5000].float() * 0.5)
 
 
+@pytest.mark.parametrize("lead", [(2, 3), (6,), (2, 0), (), (1, 2, 3)])
+def test_int8_linear_of_nothing(dion, lead):
+    """k = 0: every token's row is the bias, with leading dimensions too."""
+    n = 5
+    bias = torch.randn(n, device="cuda")
+    a, b = (torch.zeros(s, dtype=torch.int8, device="cuda") for s in ((*lead, 0), (n, 0)))
+    y = dion.int8_linear(a, torch.ones(lead, device="cuda"), b, torch.ones(n, device="cuda"), bias=bias,
+                         out_dtype=torch.float32)
+    assert y.shape == (*lead, n) and torch.equal(y, bias.expand(*lead, n))
+
+
 # ---------------------------------------------------------------- distillation
 @pytest.mark.parametrize("rows,vocab,k,dt", [(1, 128256, 32, torch.bfloat16), (2, 128256, 1, torch.float16),
                                              (1, 70001, 8, torch.float32), (1, 90000, 4, torch.float32)])

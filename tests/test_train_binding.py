@@ -46,3 +46,10 @@ def test_teacher_copies_are_made_on_the_stream_that_reads_them(monkeypatch, stre
     where = stream or "current"
     assert [s for what, s in log if what == "copied"] == [where, where]
     assert [s for what, s in log if what == "used"] == ([] if stream is None else [stream, stream])
+
+
+@pytest.mark.parametrize("shape,rows", [((2, 3, 0), 6), ((5, 0), 5), ((0, 4, 7), 0), ((2, 0, 7), 0), ((0,), 1), ((4, 1, 0, 0), 0),
+                                        ((2, 3, 4), 6), ((7,), 1)])
+def test_rows_of_tensors_with_and_without_elements(shape, rows):
+    got, cols, ld = T._matrix(torch.zeros(shape), "x")
+    assert (got, cols) == (rows, shape[-1]) and ld >= cols
