@@ -418,9 +418,11 @@ void launch_rows(const Int8Args& a, int splits, hipStream_t s) {
 }
 
 // Rows of a and b at multiples of 16 bytes, zeros past k: 16 bytes a thread.
+// Blocks lie along x and y of the grid: one dimension has less than 2^32
+// threads, and 2^36 bytes of a have as many pieces.
 __global__ __launch_bounds__(256) void k_int8_align(Int8Args g, int8_t* a, int8_t* b, int pitch) {
   const int per = pitch / 16;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, na = a ? g.m * per : 0, nb = b ? g.n * per : 0;
+  const int64_t i = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x, na = a ? g.m * per : 0, nb = b ? g.n * per : 0;
   if (i < na) {
     const int64_t r = i / per;
     const int c = (int)(i % per) * 16;
@@ -519,7 +521,8 @@ void launch_int8_linear(Int8Args g, hipStream_t s) {
     int8_t* a = l.a ? (int8_t*)g.partial + l.partial : nullptr;
     int8_t* b = l.b ? (int8_t*)g.partial + l.partial + l.a : nullptr;
     const int64_t chunks = ((a ? g.m : 0) + (b ? g.n : 0)) * (l.pitch / 16);
-    hipLaunchKernelGGL(k_int8_align, dim3((unsigned)((chunks + 255) / 256)), dim3(256), 0, s, g, a, b, l.pitch);
+    const int64_t blocks = (chunks + 255) / 256, x = std::min<int64_t>(blocks, 1 << 20);
+    hipLaunchKernelGGL(k_int8_align, dim3((unsigned)x, (unsigned)((blocks + x - 1) / x)), dim3(256), 0, s, g, a, b, l.pitch);
     if (a) g.a = a, g.lda = l.pitch;
     if (b) g.b = b, g.ldb = l.pitch;
     g.k = l.pitch;   // the zeros of at least one of the two factors fill the rest

@@ -83,6 +83,23 @@ def test_int8_linear_of_nothing(dion, lead):
     assert y.shape == (*lead, n) and torch.equal(y, bias.expand(*lead, n))
 
 
+def test_int8_linear_copies_operands_of_any_size(dion):
+    """An unaligned operand of more than 2^32 pieces of 16 bytes (64 GiB)."""
+    m, k = 1 << 22, 16385
+    if torch.cuda.mem_get_info()[0] < 160 << 30:
+        pytest.skip("needs 160 GiB of free GPU memory")
+    a = torch.zeros((m, k), dtype=torch.int8, device="cuda")
+    rows = [0, 1, 12345, m // 2, m - 2, m - 1]
+    a[rows] = codes(5, (len(rows), k))
+    b = codes(6, (1, k))
+    y = dion.int8_linear(a, torch.ones(m, device="cuda"), b, torch.ones(1, device="cuda"), out_dtype=torch.float32)[:, 0]
+    want = torch.zeros(m, device="cuda")
+    want[rows] = (a[rows].double() @ b.double().t()).float()[:, 0]
+    assert torch.equal(y, want)
+    del a, y
+    torch.cuda.empty_cache()
+
+
 # ---------------------------------------------------------------- distillation
 @pytest.mark.parametrize("rows,vocab,k,dt", [(1, 128256, 32, torch.bfloat16), (2, 128256, 1, torch.float16),
                                              (1, 70001, 8, torch.float32), (1, 90000, 4, torch.float32)])
