@@ -403,6 +403,8 @@ int dion_apply_batched(const float* const* Q, const void* const* X, void* const*
  *   weight              cols values of weight_dtype: `dtype` or DION_FP32
  *   rstd                rows floats (dion_rmsnorm_backward reads them)
  *   cols                1 .. 65536 (DION_E_UNSUPPORTED above)
+ * The sum of squares is fp32: where it overflows (a root mean square of
+ * 2^64 / sqrt(cols) and more) rstd is 0, and so are y and the codes' scale.
  * dion_rmsnorm_int8 writes y as 8-bit codes q with a scale for each row,
  * for dion_int8_linear: scale = max|y| / 127, q = rint(y * (127 * (1 / max|y|))).
  * A row with max|y| below 2^-119 has scale 0 and codes 0; a row in which an

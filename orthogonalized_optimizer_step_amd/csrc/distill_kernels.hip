@@ -387,10 +387,11 @@ __global__ __launch_bounds__(NT) void k_distill_rows(DistillArgs a) {
 // for the rest of the row, -inf past its end.  A block walks rows gridDim.x
 // apart.  As it writes chunk i of one row's gradient it asks for chunk i of
 // its next row, and takes the chunk that it asked for LAG steps before into
-// that row's largest value and sum: each logit is read once, and the
+// that row's largest value and sum: a logit is read once (a block whose next
+// row is not there or has no teacher loads its own again, for nothing), and the
 // arithmetic of both passes runs while memory is busy.  The teacher's entries
 // and the logits at them are fetched a row ahead too, for between two rows
-// nothing else is under way.  8192 x 128256 bf16 takes 880 us (4.6 TB/s over
+// nothing else is under way.  8192 x 128256 bf16 takes 884 us (4.6 TB/s over
 // the logits read and the gradients written); a plain pass that reads and
 // writes rows in the same order takes 810, one in the order of addresses 670.
 // Reading the row twice (k_distill_rows) takes 1218.
@@ -415,7 +416,7 @@ __global__ __launch_bounds__(NT, NT * BLOCKS / 256) void k_distill_step(DistillA
   // The running largest value and the sum relative to it, from a floor on: a
   // thread whose first chunks are masked starts from the floor's reference, by
   // which they are 0, and not from one of the mask's size.  (8192 x 128256 bf16:
-  // 887 us; 901 with a Ref's way for such sizes in every term.)
+  // 887 us so, 901 with a Ref's way for such sizes in every term.)
   const auto floor = [&]() { return fmaxf(-(0x1p19f * LN2) * a.temp, -3.402823466e+38f); };
   float m = floor(), mR = m * c, s = 0.f;
   auto absorb = [&](uintx4& d) {
