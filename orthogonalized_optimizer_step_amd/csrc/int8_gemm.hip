@@ -1,8 +1,9 @@
 // Product of 8-bit integers with a scale for each token and channel:
 //   out[i][j] = round(float(sum_k a[i][k] b[j][k]) * sa[i] * sb[j] + bias[j])
 // The sum is exact in int32 (k < 2^17), so the only roundings are the fp32
-// conversion of the sum, the scales' products and the output's own, and the
-// result does not depend on how the sum is split.
+// conversion of the sum, the scales' products, the bias' addition and the
+// output's own, and the result does not depend on how the sum is split or on
+// which kernel takes it.
 //
 // v_mfma_i32_32x32x32_i8: lane l holds 16 consecutive k of row l % 32 (k block
 // l / 32) of each operand; result element e of lane l is row
@@ -85,11 +86,16 @@ __device__ __forceinline__ void load_shifted(const int8_t* p, uint32_t shift, in
   }
 }
 
-// an output before its rounding
+// An output before its rounding.  The bias is added to the rounded product
+// everywhere: fused in some kernels alone, a token's last bit would depend on
+// how many others come with it.
+__device__ __forceinline__ float scaled(int sum, float sa, float sb, bool biased, float bias) {
+#pragma clang fp contract(off)
+  const float v = (float)sum * sa * sb;
+  return biased ? v + bias : v;
+}
 __device__ __forceinline__ float scaled(const Int8Args& g, int64_t row, int64_t col, int sum) {
-  float v = (float)sum * g.sa[row] * g.sb[col];
-  if (g.bias) v += load_fmt(g.bias, col, g.bias_fmt);
-  return v;
+  return scaled(sum, g.sa[row], g.sb[col], g.bias, g.bias ? load_fmt(g.bias, col, g.bias_fmt) : 0.f);
 }
 
 template <typename O> struct OutVec;   // 16 bytes of output elements
@@ -280,9 +286,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_int8_mma(Int8Args g, int* part
         Ox4 v;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float f = (float)acc[i][j][q * 4 + e] * sa * sb[j][q * 4 + e];
-          if (g.bias) f += bias[j][q * 4 + e];
-          v[e] = from_f<O>(f);
+          v[e] = from_f<O>(scaled(acc[i][j][q * 4 + e], sa, sb[j][q * 4 + e], g.bias, bias[j][q * 4 + e]));
         }
         *(Ox4*)(st + r * SROW + j * 32 + q * 8 + (lane >> 5) * 4) = v;
       }

@@ -100,6 +100,23 @@ def test_int8_linear_copies_operands_of_any_size(dion):
     torch.cuda.empty_cache()
 
 
+@pytest.mark.parametrize("k", [64, 500, 4096])
+@pytest.mark.parametrize("bias", [torch.float32, torch.bfloat16, None])
+@pytest.mark.parametrize("out", [torch.float32, torch.float16])
+def test_int8_linear_of_a_token_does_not_depend_on_the_others(dion, k, bias, out):
+    """Every kernel rounds alike: the sum, its product with each scale, the bias' addition, the output."""
+    n = 300
+    a, b = codes(1, (600, k)), codes(2, (n, k))
+    sa, sb = (torch.rand(s, generator=generator(s), device="cuda") for s in (600, n))
+    v = None if bias is None else (torch.randn(n, generator=generator(3), device="cuda") * 1000).to(bias)
+    if out == torch.float16:
+        sb = sb * 1e-3   # inside its range
+    want = (a.double() @ b.double().t()).float() * sa[:, None] * sb
+    want = (want if v is None else want + v.float()).to(out)
+    for m in (1, 5, 16, 17, 40, 129, 600):
+        assert torch.equal(dion.int8_linear(a[:m], sa[:m], b, sb, bias=v, out_dtype=out), want[:m])
+
+
 # ---------------------------------------------------------------- distillation
 @pytest.mark.parametrize("rows,vocab,k,dt", [(1, 128256, 32, torch.bfloat16), (2, 128256, 1, torch.float16),
                                              (1, 70001, 8, torch.float32), (1, 90000, 4, torch.float32)])
