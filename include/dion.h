@@ -484,6 +484,97 @@ int dion_distill_topk_step(const void* logits, int64_t ldz, const void* teacher,
                            int32_t vocab, int32_t k, int32_t dtype, int32_t teacher_dtype, int32_t idx_bytes,
                            float temperature, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Layer norm of rows with the residual's addition:
+ *   s = x + residual (residual may be NULL)   h = s rounded to x's type
+ *   mean = sum s / cols     rstd = 1 / sqrt(sum (s - mean)^2 / cols + eps)
+ *   y = (s - mean) * rstd * weight + bias
+ *   x, residual, h, y   as of dion_rmsnorm (h may be x or residual in place)
+ *   weight, bias        cols values of weight_dtype: `dtype` or DION_FP32;
+ *                       bias may be NULL (0)
+ *   mean, rstd          rows floats (dion_layernorm_backward reads them)
+ *   cols                1 .. 65536 (DION_E_UNSUPPORTED above)
+ * The sums are fp32: a row whose squares overflow has rstd 0 and y = bias, one
+ * whose sum does is NaN, as is one that holds an infinity or a NaN, or (with
+ * eps = 0) equal elements only. */
+int dion_layernorm(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight, const void* bias,
+                   void* h, int64_t ldh, void* y, int64_t ldy, float* mean, float* rstd, int64_t rows, int32_t cols,
+                   int32_t dtype, int32_t weight_dtype, float eps, void* stream);
+
+/* Gradient of dion_layernorm.  With u = (h - mean) rstd and g = dy * weight:
+ *   dx = rstd * (g - mean(g) - u mean(g u)) + dh
+ *   dweight_j = sum over rows of dy_j u_j     dbias_j = sum over rows of dy_j
+ * h, mean and rstd are the forward's (h = x without a residual); dh and dx as
+ * of dion_rmsnorm_backward.  dweight and dbias (cols values of weight_dtype;
+ * dbias may be NULL) are summed in a fixed order. */
+size_t dion_layernorm_backward_workspace_size(int64_t rows, int32_t cols, int32_t dtype);
+int dion_layernorm_backward(const void* dy, int64_t lddy, const void* h, int64_t ldh, const void* weight,
+                            const float* mean, const float* rstd, const void* dh, int64_t lddh, void* dx, int64_t lddx,
+                            void* dweight, void* dbias, int64_t rows, int32_t cols, int32_t dtype, int32_t weight_dtype,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* Microscaled 4-bit floating point.  A code is a sign, two bits of exponent
+ * and one of mantissa (0, 0.5, 1, 1.5, 2, 3, 4, 6 in the order of the codes 0
+ * to 7); two lie in a byte, the even element in its low half.  Each 32
+ * consecutive elements of a row share a scale byte s that stands for
+ * 2^(s - 127); 255 stands for NaN.
+ *   q       rows of ceil(cols / 2) bytes (a missing last code is written as 0)
+ *   scale   rows of ceil(cols / 32) bytes
+ * both with a stride in bytes, at any alignment.  dion_mxfp4_quantize takes
+ * the least scale 2^e (e from -127 on) with max|x| < 7 2^e, and the nearest
+ * code, ties to the even one; a block of 32 that holds an infinity or a NaN
+ * gets the scale 255 and codes 0.  dion_mxfp4_dequantize writes the values,
+ * rounded to `dtype`. */
+int dion_mxfp4_quantize(const void* x, int64_t ldx, uint8_t* q, int64_t ldq, uint8_t* scale, int64_t lds, int64_t rows,
+                        int32_t cols, int32_t dtype, void* stream);
+int dion_mxfp4_dequantize(const uint8_t* q, int64_t ldq, const uint8_t* scale, int64_t lds, void* y, int64_t ldy,
+                          int64_t rows, int32_t cols, int32_t dtype, void* stream);
+
+/* Product of two such matrices:
+ *   out[i][j] = sum_l a[i][l] b[j][l] + bias[j]
+ * a: m x k activations, b: n x k weights (output channels as rows), any codes
+ * and scales; k even, up to 2^22 (codes of an odd number of columns count one
+ * more).  The products are exact and summed in fp32, in an order fixed by m, n
+ * and k.  bias, out and the workspace as of dion_int8_linear; the workspace
+ * also holds copies of rows that are not whole multiples of 16 bytes, the
+ * scales' among them (k not a multiple of 512), when m > 16. */
+size_t dion_mxfp4_linear_workspace_size(const uint8_t* a, int64_t lda, const uint8_t* a_scale, int64_t ldsa,
+                                        const uint8_t* b, int64_t ldb, const uint8_t* b_scale, int64_t ldsb, int64_t m,
+                                        int64_t n, int32_t k);
+int dion_mxfp4_linear(const uint8_t* a, int64_t lda, const uint8_t* a_scale, int64_t ldsa, const uint8_t* b,
+                      int64_t ldb, const uint8_t* b_scale, int64_t ldsb, const void* bias, int32_t bias_dtype,
+                      void* out, int64_t ldo, int64_t m, int64_t n, int32_t k, int32_t out_dtype, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/* Log probabilities of given tokens, with the entropy and the top
+ * alternatives.  For each row, with logits z (vocab values of `dtype`), a
+ * token t and temperature T > 0:
+ *   q = softmax(z / T)     logprob = log q_t     entropy = -sum_j q_j log q_j
+ *   tokens       rows of token_bytes 4 or 8, or NULL (logprob is not written).
+ *                A token outside [0, vocab) is left out: logprob 0
+ *   logprob, entropy   rows floats
+ *   stats        rows x 4 floats (16-byte aligned) that the backward call
+ *                reads; may be NULL
+ *   top_logprob, top_index   rows x top: log probabilities and tokens of the
+ *                largest logits, in descending order, equal logits by their
+ *                index.  Only logits above -infinity are alternatives: places
+ *                beyond them hold -infinity and -1
+ *   top          0 .. 1024, with vocab up to 2^19 where it is not 0
+ * A row that holds a NaN or +infinity has NaN statistics; a row of -infinity
+ * alone has entropy 0 and log probability -infinity. */
+int dion_token_logprobs(const void* logits, int64_t ldz, const void* tokens, float* logprob, float* entropy,
+                        float* stats, float* top_logprob, int64_t* top_index, int64_t rows, int32_t vocab, int32_t top,
+                        int32_t dtype, int32_t token_bytes, float temperature, void* stream);
+
+/* Gradient of the logits, from the gradients gl of each row's logprob and ge of
+ * its entropy (rows floats; NULL: 0):
+ *   d z_j = (gl ([j = t] - q_j) - ge q_j (log q_j + entropy)) / T
+ * without the first term where the token is left out.  A row in which neither
+ * term is left (gl and ge 0) has gradient 0 whatever its logits hold, and so has a row of
+ * -infinity alone.  dlogits may be the logits in place. */
+int dion_token_logprobs_backward(const float* grad_logprob, const float* grad_entropy, const void* logits, int64_t ldz,
+                                 const float* stats, const void* tokens, void* dlogits, int64_t ldd, int64_t rows,
+                                 int32_t vocab, int32_t dtype, int32_t token_bytes, float temperature, void* stream);
+
 /* Useful floating-point operations of one dion_orth_batched call on this
  * batch, in the executed formulation, symmetric products counted once:
  * per matrix and restart segment of length L,

@@ -16,7 +16,9 @@ __all__ = ["orth_batched", "rowsubset_step", "workspace_size", "useful_flops", "
            "apply", "rowsubset_step_update", "Dion3", "restart_points", "lowrank_step",
            "lowrank_workspace_size", "orth_batched_noalloc", "NOALLOC_SCRATCH_BYTES",
            "rmsnorm", "rmsnorm_int8", "rmsnorm_backward", "int8_quantize", "int8_dequantize", "int8_linear",
-           "distill_topk", "distill_topk_backward", "distill_topk_step", "rms_norm", "distill_loss"]
+           "distill_topk", "distill_topk_backward", "distill_topk_step", "rms_norm", "distill_loss",
+           "layernorm", "layernorm_backward", "layer_norm", "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_linear",
+           "token_logprobs", "top_logprobs", "token_logprobs_backward", "log_probs"]
 
 QUINTIC = (3.4445, -4.7750, 2.0315)
 
@@ -491,3 +493,5 @@ def profile_records():
 from .optim import Dion3  # noqa: E402
 from .train_ops import (distill_loss, distill_topk, distill_topk_backward, distill_topk_step, int8_dequantize,  # noqa: E402
                         int8_linear, int8_quantize, rms_norm, rmsnorm, rmsnorm_backward, rmsnorm_int8)
+from .model_ops import (layer_norm, layernorm, layernorm_backward, log_probs, mxfp4_dequantize, mxfp4_linear,  # noqa: E402
+                        mxfp4_quantize, token_logprobs, token_logprobs_backward, top_logprobs)

@@ -49,6 +49,9 @@ EXPORTS = (
     "dion_rmsnorm_backward_workspace_size", "dion_rmsnorm_backward", "dion_int8_linear_workspace_size",
     "dion_int8_linear", "dion_distill_topk_workspace_size", "dion_distill_topk", "dion_distill_topk_backward",
     "dion_distill_topk_step",
+    "dion_layernorm", "dion_layernorm_backward_workspace_size", "dion_layernorm_backward", "dion_mxfp4_quantize",
+    "dion_mxfp4_dequantize", "dion_mxfp4_linear_workspace_size", "dion_mxfp4_linear", "dion_token_logprobs",
+    "dion_token_logprobs_backward",
 )
 
 
@@ -152,6 +155,25 @@ def _load():
     lib.dion_distill_topk_backward.restype = ctypes.c_int
     lib.dion_distill_topk_step.argtypes = mat + [vp, vp, vp, vp] + mat + [i64, i32, i32, i32, i32, i32, f32, vp, sz, vp]
     lib.dion_distill_topk_step.restype = ctypes.c_int
+    lib.dion_layernorm.argtypes = mat + mat + [vp, vp] + mat + mat + [vp, vp, i64, i32, i32, i32, f32, vp]
+    lib.dion_layernorm.restype = ctypes.c_int
+    lib.dion_layernorm_backward_workspace_size.argtypes = [i64, i32, i32]
+    lib.dion_layernorm_backward_workspace_size.restype = sz
+    lib.dion_layernorm_backward.argtypes = (mat + mat + [vp, vp, vp] + mat + mat +
+                                            [vp, vp, i64, i32, i32, i32, vp, sz, vp])
+    lib.dion_layernorm_backward.restype = ctypes.c_int
+    lib.dion_mxfp4_quantize.argtypes = mat + mat + mat + [i64, i32, i32, vp]
+    lib.dion_mxfp4_quantize.restype = ctypes.c_int
+    lib.dion_mxfp4_dequantize.argtypes = lib.dion_mxfp4_quantize.argtypes
+    lib.dion_mxfp4_dequantize.restype = ctypes.c_int
+    lib.dion_mxfp4_linear_workspace_size.argtypes = mat + mat + mat + mat + [i64, i64, i32]
+    lib.dion_mxfp4_linear_workspace_size.restype = sz
+    lib.dion_mxfp4_linear.argtypes = mat + mat + mat + mat + [vp, i32] + mat + [i64, i64, i32, i32, vp, sz, vp]
+    lib.dion_mxfp4_linear.restype = ctypes.c_int
+    lib.dion_token_logprobs.argtypes = mat + [vp, vp, vp, vp, vp, vp, i64, i32, i32, i32, i32, f32, vp]
+    lib.dion_token_logprobs.restype = ctypes.c_int
+    lib.dion_token_logprobs_backward.argtypes = [vp, vp] + mat + [vp, vp] + mat + [i64, i32, i32, i32, f32, vp]
+    lib.dion_token_logprobs_backward.restype = ctypes.c_int
     return lib
 
 

@@ -30,8 +30,12 @@ SOURCES = [
     ("norm_kernels.hip", []),
     ("int8_gemm.hip", []),
     ("distill_kernels.hip", []),
+    ("layernorm_kernels.hip", []),
+    ("mxfp4_kernels.hip", []),
+    ("logprob_kernels.hip", []),
     ("dion_api.cpp", []),
     ("train_api.cpp", []),
+    ("model_api.cpp", []),
 ]
 
 BASE_FLAGS = [

@@ -1,0 +1,602 @@
+// Microscaled 4-bit floating point: codes of rows, the values they stand for,
+// and the product of two such matrices.
+//
+// A code is a sign, two bits of exponent and one of mantissa: 0, 0.5, 1, 1.5,
+// 2, 3, 4, 6.  Each 32 consecutive elements of a row share a scale 2^(s - 127).
+//   e = the least (from -127 on) with max|x| < 7 2^e      s = e + 127
+//   code = the nearest to x 2^-e, ties to the even code
+// 7 is where 6 and the next value of the same grid, 8, are equally near: below
+// it nothing is off by more than half a step of the grid.  (Relative error of
+// normal values 0.112 so; 0.115 with 8, by which what lies between 7 and 8 is cut to 6, and
+// with 6, by which more is left to the small steps.)  A block with an infinity or a NaN has
+// the scale 255, which stands for NaN.
+//
+//   out[i][j] = sum_k a[i][k] b[j][k] + bias[j]
+// by v_mfma_scale_f32_32x32x64_f8f6f4 and 16x16x128: lane l holds 32
+// consecutive k (16 bytes) of row l % 32 (l % 16), block l / 32 (l / 16) of
+// each operand, and their scale; result element e of lane l of the first is
+// row 8 (e / 4) + 4 (l / 32) + e % 4 of the first operand and row l % 32 of
+// the second, of the other row 4 (l / 16) + e and row l % 16.  b goes first,
+// so that a lane holds four consecutive channels of one token.  Products are
+// exact, sums are fp32; their order depends on the sizes alone.
+#include <algorithm>
+
+#include "mma_device.h"
+#include "model_internal.h"
+
+namespace dion {
+
+namespace {
+
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+typedef int intx8 __attribute__((ext_vector_type(8)));
+typedef floatx4 floatx4u __attribute__((aligned(4)));
+
+constexpr int MX = 32;   // elements of a scale
+
+// The largest over the 4 or 8 neighbouring lanes of a block.
+template <int LANES> __device__ __forceinline__ uint32_t block_max(uint32_t v) {
+  const auto move = [&](uint32_t x) { v = max(v, x); };
+  move(__builtin_amdgcn_update_dpp(v, v, 0xb1, 0xf, 0xf, false));   // lane xor 1
+  move(__builtin_amdgcn_update_dpp(v, v, 0x4e, 0xf, 0xf, false));   // lane xor 2
+  if (LANES == 8) move(__builtin_amdgcn_update_dpp(v, v, 0x141, 0xf, 0xf, false));   // the other half of 8
+  return v;
+}
+
+// Blocks of 256 threads, TX of them along a row; a thread takes 16 bytes of
+// values.  Grid: rows along x, the rest of long rows along y.
+template <typename T>
+__global__ __launch_bounds__(256) void k_mxfp4_quantize(MxCodesArgs a, int tx) {
+  typedef Chunk<T> C;
+  constexpr int N = C::N, L = MX / N;
+  const int t = threadIdx.x % tx, per = (a.cols + MX - 1) / MX * L;
+  const int64_t step = (int64_t)gridDim.x * (256 / tx);
+  for (int64_t row = (int64_t)blockIdx.x * (256 / tx) + threadIdx.x / tx; row < a.rows; row += step)
+    for (int64_t p = (int64_t)blockIdx.y * tx + t; p < per; p += (int64_t)gridDim.y * tx) {
+      const int64_t j = p * N;   // may lie behind the row's end, where values are 0
+      float f[N] = {};
+      if (j < a.cols) C::unpack(C::load((const T*)a.x + row * a.ldx, (int)j, a.cols, 0.f), f);
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i) top = max(top, __float_as_uint(f[i]) & 0x7fffffffu);
+      top = block_max<L>(top);
+      const bool bad = top >= 0x7f800000u;
+      const int s = bad ? 255 : max(0, (int)((top + 0x200000u) >> 23) - 2);   // 7 = 1.75 2^2: a carry from there on
+      const float inv = __uint_as_float((uint32_t)(254 - min(s, 253)) << 23);   // 2^-e
+      uint32_t q = 0;
+#pragma unroll
+      for (int i = 0; i < N; i += 2) {
+        const float x = bad ? 0.f : f[i] * inv, y = bad ? 0.f : f[i + 1] * inv;
+        if (i == 0) q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, x, y, 1.f, 0);
+        if (i == 2) q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, x, y, 1.f, 1);
+        if (i == 4) q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, x, y, 1.f, 2);
+        if (i == 6) q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, x, y, 1.f, 3);
+      }
+      uint8_t* o = a.q + row * a.ldq + j / 2;
+      if (j + N <= a.cols) __builtin_memcpy(o, &q, N / 2);
+      else
+        for (int i = 0; 2 * i < N; ++i)
+          if (j + 2 * i < a.cols) o[i] = (uint8_t)(q >> (8 * i));
+      if (t % L == 0) a.s[row * a.lds + p / L] = (uint8_t)s;
+    }
+}
+
+// The values: the same shares of the rows.
+template <typename T>
+__global__ __launch_bounds__(256) void k_mxfp4_dequantize(MxCodesArgs a, int tx) {
+  typedef Chunk<T> C;
+  constexpr int N = C::N, L = MX / N;
+  const int t = threadIdx.x % tx, per = (a.cols + N - 1) / N;
+  const int64_t step = (int64_t)gridDim.x * (256 / tx);
+  for (int64_t row = (int64_t)blockIdx.x * (256 / tx) + threadIdx.x / tx; row < a.rows; row += step)
+    for (int64_t p = (int64_t)blockIdx.y * tx + t; p < per; p += (int64_t)gridDim.y * tx) {
+      const int64_t j = p * N;
+      const uint8_t* c = a.q + row * a.ldq + j / 2;
+      uint32_t q = 0;
+      if (j + N <= a.cols) __builtin_memcpy(&q, c, N / 2);
+      else
+        for (int i = 0; 2 * i < N; ++i)
+          if (j + 2 * i < a.cols) q |= (uint32_t)c[i] << (8 * i);
+      const int s = a.s[row * a.lds + p / L];
+      float f[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const uint32_t code = q >> (4 * i) & 7;
+        // 0, 0.5 and the others, whose bits are an exponent's and a mantissa's
+        const float v = code < 2 ? 0.5f * code : __uint_as_float((code << 22) + (126u << 23));
+        f[i] = s == 255 ? __builtin_nanf("") : ldexpf(q >> (4 * i) & 8 ? -v : v, s - 127);
+      }
+      C::store_near((T*)a.x + row * a.ldx, (int)j, a.cols, f);
+    }
+}
+
+// Threads along a row: a power of two that covers it, whole blocks of 32 elements.
+int along(int64_t pieces) {
+  int tx = 8;
+  while (tx < 256 && tx < pieces) tx *= 2;
+  return tx;
+}
+dim3 codes_grid(const MxCodesArgs& a, int64_t pieces, int tx) {
+  return dim3((unsigned)std::min<int64_t>((a.rows + 256 / tx - 1) / (256 / tx), 1 << 20),
+              (unsigned)std::min<int64_t>((pieces + tx - 1) / tx, 1 << 15));
+}
+
+template <typename T> void launch_quantize(const MxCodesArgs& a, hipStream_t s) {
+  const int64_t pieces = ((int64_t)a.cols + MX - 1) / MX * (MX / Chunk<T>::N);
+  const int tx = along(pieces);
+  hipLaunchKernelGGL((k_mxfp4_quantize<T>), codes_grid(a, pieces, tx), dim3(256), 0, s, a, tx);
+}
+template <typename T> void launch_dequantize(const MxCodesArgs& a, hipStream_t s) {
+  const int64_t pieces = ((int64_t)a.cols + Chunk<T>::N - 1) / Chunk<T>::N;
+  const int tx = along(pieces);
+  hipLaunchKernelGGL((k_mxfp4_dequantize<T>), codes_grid(a, pieces, tx), dim3(256), 0, s, a, tx);
+}
+
+// ------------------------------------------------------------------ product
+__device__ __forceinline__ intx8 wide(intx4 v) { return intx8{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
+
+// The scales' bytes ks of sb and sa; 4: 4-bit floating point.
+__device__ __forceinline__ floatx16 mma32(intx4 b, intx4 a, floatx16 c, int sb, int sa, int ks) {
+  const intx8 x = wide(b), y = wide(a);
+  if (ks == 0) return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, 0, sb, 0, sa);
+  if (ks == 1) return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, 1, sb, 1, sa);
+  if (ks == 2) return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, 2, sb, 2, sa);
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, 3, sb, 3, sa);
+}
+__device__ __forceinline__ floatx4 mma16(intx4 b, intx4 a, floatx4 c, int sb, int sa) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(b), wide(a), c, 4, 4, 0, sb, 0, sa);
+}
+
+__device__ __forceinline__ float biased(const MxArgs& g, int64_t col, float v) {
+  return g.bias ? v + load_fmt(g.bias, col, g.bias_fmt) : v;
+}
+
+// One BM x BN tile of the output by WM x WN waves, as the 8-bit product's: S
+// stages of BK bytes of codes (256 k) in LDS, copied straight there S - 1
+// stages ahead, fragments of the next 32 bytes read while the present ones are
+// multiplied.  The scales come along in chunks of 16 bytes, those of two
+// stages for one row, into places of their own; a lane's four of a stage
+// (blocks l / 32, 2 + l / 32, ..) are picked into one register.  Codes and
+// scales lie in rows at multiples of 16 bytes, whole chunks of them.
+template <int BM, int BN, int WM, int WN, int S, typename O>
+__global__ __launch_bounds__(64 * WM * WN) void k_mxfp4_mma(MxArgs g, float* partial) {
+  constexpr int W = WM * WN, NT = 64 * W;
+  constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32;   // wave tile, its fragments
+  constexpr int STAGE = (BM + BN) * BK;
+  constexpr int NP = STAGE / 1024 / W;            // 1 KB pieces of a stage per wave
+  constexpr int PR = 1024 / BK, CR = BK / 16;     // rows of a piece, chunks of a row
+  constexpr int SCALES = (BM + BN) * 16, SP = SCALES / 1024, PAIRS = S <= 3 ? 2 : 4;   // pairs of stages in LDS
+  constexpr int OV = OutVec<O>::N, SROW = TN + OV;   // staged output row
+  constexpr int STAGED = W * 32 * SROW * (int)sizeof(O);
+  constexpr int HELD = S * STAGE + PAIRS * SCALES, LDS = HELD > STAGED ? HELD : STAGED;
+  constexpr int KS = BK / 32;
+  constexpr bool SPREAD = BM * BN >= 256 * 256;
+  constexpr int PW = NP / 2, EVERY = SPREAD ? FM * FN / PW : 1;
+  static_assert(!SPREAD || (PW * 2 == NP && EVERY * PW == FM * FN), "the copies divide the products");
+  static_assert(S <= 4 && NP * W * 1024 == STAGE && BM % PR == 0 && BM % 64 == 0 && SP <= W, "whole pieces");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[LDS];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  int ti, tj;
+  tile_of_block((int)((g.m + BM - 1) / BM), (int)((g.n + BN - 1) / BN), ti, tj);
+  const int64_t m0 = (int64_t)ti * BM, n0 = (int64_t)tj * BN;
+  const int rm = (int)min((int64_t)BM, g.m - m0), rn = (int)min((int64_t)BN, g.n - n0);   // valid rows of the tile
+  // this split's stages
+  const int all = (g.kb + BK - 1) / BK, sb16 = (g.kb + 255) / 256 * 16;   // (bytes of a row of scales, whole chunks)
+  const int kt0 = (int)((int64_t)all * blockIdx.y / gridDim.y);
+  const int nk = (int)((int64_t)all * (blockIdx.y + 1) / gridDim.y) - kt0;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)((__attribute__((address_space(3))) uint8_t*)smem);
+
+  // piece q = wave + i W of a stage: rows PR q .. of a, then of b; lane l has
+  // row l / CR and the chunk whose place is l % CR
+  uint32_t voff[NP];
+  int vk[NP];
+  const intx4 ra = raw_buffer(g.a + m0 * g.lda, (uint32_t)((rm - 1) * g.lda + g.kb));
+  const intx4 rb = raw_buffer(g.b + n0 * g.ldb, (uint32_t)((rn - 1) * g.ldb + g.kb));
+  const intx4 rsa = raw_buffer(g.sa + m0 * g.ldsa, (uint32_t)((rm - 1) * g.ldsa + sb16));
+  const intx4 rsb = raw_buffer(g.sb + n0 * g.ldsb, (uint32_t)((rn - 1) * g.ldsb + sb16));
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const int q = wave + i * W;
+    const bool isa = q < BM / PR;
+    const int r = (isa ? q : q - BM / PR) * PR + lane / CR;
+    vk[i] = swz(r, lane % CR) * 16;
+    voff[i] = r < (isa ? rm : rn) ? (uint32_t)(r * (isa ? g.lda : g.ldb)) + vk[i] : OUT_OF_RANGE;
+  }
+  // piece `wave` of a pair's scales: rows 64 wave .. of a, then of b, one to a lane
+  const bool sisa = wave < BM / 64;
+  const int sr = (sisa ? wave : wave - BM / 64) * 64 + lane;
+  const uint32_t soff = sr < (sisa ? rm : rn) ? (uint32_t)(sr * (sisa ? g.ldsa : g.ldsb)) : OUT_OF_RANGE;
+  auto issue = [&](int kt, int i) {   // piece i of stage kt
+    const int k0 = (kt0 + kt) * BK, q = wave + i * W;
+    const uint32_t v = k0 + vk[i] < g.kb ? voff[i] : OUT_OF_RANGE;
+    dma16(v, q < BM / PR ? ra : rb, (uint32_t)k0,
+          (uint32_t)__builtin_amdgcn_readfirstlane(lds0 + (kt % S) * STAGE + q * 1024));
+  };
+  auto issue_scales = [&](int kt) {   // with the first of a pair's stages
+    const int pair = (kt0 + kt) / 2;
+    if (((kt0 + kt) & 1 && kt > 0) || wave >= SP) return;
+    dma16(soff, sisa ? rsa : rsb, (uint32_t)(pair * 16),
+          (uint32_t)__builtin_amdgcn_readfirstlane(lds0 + S * STAGE + pair % PAIRS * SCALES + wave * 1024));
+  };
+
+  floatx16 acc[FM][FN] = {};
+  intx4 fa[2][FM], fb[2][FN];
+  int sa[FM], sb[FN], na[FM], nb_[FN];   // the scales of this stage and of the next
+  const int r = lane & 31;
+  const uint32_t pick = lane < 32 ? 0x06040200u : 0x07050301u;
+  auto fetch = [&](int kt, int ks, int set) {
+    const uint8_t* s = smem + (kt % S) * STAGE + swz(r, ks * 2 + (lane >> 5)) * 16;
+#pragma unroll
+    for (int f = 0; f < FM; ++f) fa[set][f] = *(const intx4*)(s + (wm * TM + f * 32 + r) * BK);
+#pragma unroll
+    for (int f = 0; f < FN; ++f) fb[set][f] = *(const intx4*)(s + (BM + wn * TN + f * 32 + r) * BK);
+  };
+  auto fetch_scales = [&](int kt) {
+    const uint8_t* s = smem + S * STAGE + (kt0 + kt) / 2 % PAIRS * SCALES + ((kt0 + kt) & 1) * 8;
+#pragma unroll
+    for (int f = 0; f < FM; ++f) {
+      const uint2 v = *(const uint2*)(s + (wm * TM + f * 32 + r) * 16);
+      na[f] = (int)__builtin_amdgcn_perm(v.y, v.x, pick);
+    }
+#pragma unroll
+    for (int f = 0; f < FN; ++f) {
+      const uint2 v = *(const uint2*)(s + (BM + wn * TN + f * 32 + r) * 16);
+      nb_[f] = (int)__builtin_amdgcn_perm(v.y, v.x, pick);
+    }
+  };
+  auto take_scales = [&]() {
+#pragma unroll
+    for (int f = 0; f < FM; ++f) sa[f] = na[f];
+#pragma unroll
+    for (int f = 0; f < FN; ++f) sb[f] = nb_[f];
+  };
+  // the stage that is needed next has landed, and every wave is done with the one before it
+  auto turn = [&](int kt) {
+    const int later = min(nk - 1, kt + S - 2) - kt;   // stages issued after kt, NP copies each or one more
+    if (S >= 4 && later >= 2) wait_vmcnt<2 * NP>();
+    else if (S >= 3 && later >= 1) wait_vmcnt<NP>();
+    else wait_vmcnt<0>();
+    lds_barrier();
+    if (kt + S - 1 < nk) {
+      issue_scales(kt + S - 1);
+      if (!SPREAD) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) issue(kt + S - 1, i);
+      }
+    }
+  };
+  if (nk > 0) {
+#pragma unroll
+    for (int t = 0; t < S - 1; ++t)
+      if (t < nk) {
+        issue_scales(t);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) issue(t, i);
+      }
+    turn(0);
+    if (SPREAD && S - 1 < nk) {
+#pragma unroll
+      for (int i = 0; i < PW; ++i) issue(S - 1, i);
+    }
+    fetch(0, 0, 0);
+    fetch_scales(0);
+    take_scales();
+    for (int kt = 0; kt < nk; ++kt) {
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        if (ks + 1 < KS) {
+          fetch(kt, ks + 1, (ks + 1) & 1);
+        } else if (kt + 1 < nk) {
+          turn(kt + 1);
+          fetch(kt + 1, 0, 0);
+          fetch_scales(kt + 1);
+        }
+        __builtin_amdgcn_sched_barrier(0);   // the reads above go out before the products, not beside their use
+        // spread copies, one after every EVERY products: half of a stage's
+        // right after its turn, half beside the next step's products
+        const int w = (ks + 1) % KS, st = ks + 1 < KS ? kt + S - 1 : kt + S;
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j) {
+            acc[i][j] = mma32(fb[ks & 1][j], fa[ks & 1][i], acc[i][j], sb[j], sa[i], ks);
+            const int t = i * FN + j;
+            if (SPREAD && w < 2 && t % EVERY == EVERY - 1) {
+              __builtin_amdgcn_sched_barrier(0);
+              if (st < nk) issue(st, w * PW + t / EVERY);
+              __builtin_amdgcn_sched_barrier(0);
+            }
+          }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      take_scales();
+    }
+  }
+  if (partial) {   // several splits: the sums as they are, for k_mxfp4_join
+    float* out = partial + (int64_t)blockIdx.y * g.m * g.n;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int64_t row = m0 + wm * TM + i * 32 + r;
+      if (row >= g.m) continue;
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int64_t col = n0 + wn * TN + j * 32 + q * 8 + (lane >> 5) * 4;
+          float* o = out + row * g.n + col;
+          const floatx4 v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+          if (col + 4 <= g.n) *(floatx4u*)o = v;
+          else
+            for (int e = 0; e < 4; ++e)
+              if (col + e < g.n) o[e] = v[e];
+        }
+    }
+    return;
+  }
+  __syncthreads();   // the stages are free: each wave stages 32 rows of its output at a time
+
+  O* st = (O*)smem + wave * 32 * SROW;
+  const int64_t cbase = n0 + wn * TN;
+  constexpr int CPR = TN / OV;   // 16-byte pieces of a staged row
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        typedef O Ox4 __attribute__((ext_vector_type(4)));
+        Ox4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {   // past the last channel its bias: not written
+          const int64_t col = min(cbase + j * 32 + q * 8 + (lane >> 5) * 4 + e, g.n - 1);
+          v[e] = from_f<O>(biased(g, col, acc[i][j][q * 4 + e]));
+        }
+        *(Ox4*)(st + r * SROW + j * 32 + q * 8 + (lane >> 5) * 4) = v;
+      }
+    asm volatile("" : : : "memory");   // a wave's LDS accesses execute in order
+#pragma unroll
+    for (int q0 = 0; q0 < 32 * CPR; q0 += 64) {
+      const int q = q0 + lane, rr = q / CPR, c = (q % CPR) * OV;
+      const int64_t orow = m0 + wm * TM + i * 32 + rr, col = cbase + c;
+      if (orow < g.m && col < g.n) {
+        const O* s = st + rr * SROW + c;
+        O* o = (O*)g.out + orow * g.ldo + col;
+        if (col + OV <= g.n) *(intx4u*)o = *(const intx4*)s;
+        else
+          for (int e = 0; col + e < g.n; ++e) o[e] = s[e];
+      }
+    }
+    asm volatile("" : : : "memory");
+  }
+}
+
+// The splits' sums, in their order.  Tokens lie along y and z of the grid,
+// which have 65536 blocks at most each.
+template <typename O> __global__ __launch_bounds__(256) void k_mxfp4_join(MxArgs g, const float* partial, int splits) {
+  const int64_t col = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t row = (int64_t)blockIdx.z * gridDim.y + blockIdx.y;
+  if (col >= g.n || row >= g.m) return;
+  float v = 0.f;
+  for (int s = 0; s < splits; ++s) v += partial[((int64_t)s * g.m + row) * g.n + col];
+  ((O*)g.out)[row * g.ldo + col] = from_f<O>(biased(g, col, v));
+}
+
+void launch_join(const MxArgs& a, int splits, hipStream_t s) {
+  const int64_t y = std::min<int64_t>(a.m, 1 << 15);
+  const dim3 grid((unsigned)((a.n + 255) / 256), (unsigned)y, (unsigned)((a.m + y - 1) / y));
+  if (a.out_fmt == 1) hipLaunchKernelGGL((k_mxfp4_join<float>), grid, dim3(256), 0, s, a, a.partial, splits);
+  else if (a.out_fmt == 0) hipLaunchKernelGGL((k_mxfp4_join<bf16_t>), grid, dim3(256), 0, s, a, a.partial, splits);
+  else hipLaunchKernelGGL((k_mxfp4_join<fp16_t>), grid, dim3(256), 0, s, a, a.partial, splits);
+}
+
+template <int BM, int BN, int WM, int WN, int S>
+void launch_mma(const MxArgs& a, int splits, hipStream_t s) {
+  const int64_t tiles = (a.m + BM - 1) / BM * ((a.n + BN - 1) / BN);
+  const dim3 grid((unsigned)tiles, splits), block(64 * WM * WN);
+  float* part = splits > 1 ? a.partial : nullptr;
+  if (a.out_fmt == 1) hipLaunchKernelGGL((k_mxfp4_mma<BM, BN, WM, WN, S, float>), grid, block, 0, s, a, part);
+  else if (a.out_fmt == 0) hipLaunchKernelGGL((k_mxfp4_mma<BM, BN, WM, WN, S, bf16_t>), grid, block, 0, s, a, part);
+  else hipLaunchKernelGGL((k_mxfp4_mma<BM, BN, WM, WN, S, fp16_t>), grid, block, 0, s, a, part);
+  if (part) launch_join(a, splits, s);
+}
+
+// Up to 16 tokens, as the 8-bit product's: the block takes 16 NW channels; its
+// waves take 16 of them and every KW-th 128-byte piece of the split's share of
+// k each, and the sums of the KW meet in LDS.  Codes and scales go from global
+// memory to registers, at any alignment.  Rows past the end repeat the last
+// one and are not written.
+template <int NW, int KW, typename O>
+__global__ __launch_bounds__(64 * NW * KW) void k_mxfp4_rows(MxArgs g, float* partial) {
+  __shared__ __attribute__((aligned(16))) float sum[KW * NW * 256];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int nw = wave % NW, kw = wave / NW;
+  const int64_t n0 = (int64_t)blockIdx.x * (16 * NW);
+  const int r = lane & 15, kc = lane >> 4;   // row, block of 32 in its 128
+  const int64_t rb = min(n0 + nw * 16 + r, g.n - 1), ra = min((int64_t)r, g.m - 1);
+  const uint8_t *b = g.b + rb * g.ldb, *a = g.a + ra * g.lda, *sb = g.sb + rb * g.ldsb, *sa = g.sa + ra * g.ldsa;
+  floatx4 acc = {0.f, 0.f, 0.f, 0.f};
+  const int pieces = (g.kb + 127) / 128, nb = (g.kb + 15) / 16;
+  const int p0 = (int)((int64_t)pieces * blockIdx.y / gridDim.y);
+  const int kend = min(g.kb, (int)((int64_t)pieces * (blockIdx.y + 1) / gridDim.y) * 128);
+  int k0 = (p0 + kw) * 128;
+#pragma unroll 4
+  for (; k0 + 128 <= kend; k0 += KW * 128) {
+    uint2 vb, va;   // the scales of 128 bytes
+    __builtin_memcpy(&vb, sb + k0 / 16, 8);
+    __builtin_memcpy(&va, sa + k0 / 16, 8);
+    acc = mma16(*(const intx4u*)(b + k0 + kc * 16), *(const intx4u*)(a + k0 + kc * 16), acc, (int)(vb.x >> (8 * kc)),
+                (int)(va.x >> (8 * kc)));
+    acc = mma16(*(const intx4u*)(b + k0 + kc * 16 + 64), *(const intx4u*)(a + k0 + kc * 16 + 64), acc,
+                (int)(vb.y >> (8 * kc)), (int)(va.y >> (8 * kc)));
+  }
+  if (k0 < kend) {   // the last piece, in part
+    for (int h = 0; h < 128; h += 64) {
+      const int k = k0 + kc * 16 + h, blk = k / 16;
+      const int xb = blk < nb ? sb[blk] : 0, xa = blk < nb ? sa[blk] : 0;
+      acc = mma16(load_chunk((const int8_t*)b, k, kend), load_chunk((const int8_t*)a, k, kend), acc, xb, xa);
+    }
+  }
+  // [kw][token][channel of the block]
+  *(floatx4*)(sum + (kw * 16 + r) * (16 * NW) + nw * 16 + kc * 4) = acc;
+  __syncthreads();
+  for (int i = tid; i < NW * 256; i += 64 * NW * KW) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < KW; ++w) v += sum[w * NW * 256 + i];
+    const int64_t row = i / (16 * NW), col = n0 + i % (16 * NW);
+    if (row < g.m && col < g.n) {
+      if (partial) partial[((int64_t)blockIdx.y * g.m + row) * g.n + col] = v;
+      else ((O*)g.out)[row * g.ldo + col] = from_f<O>(biased(g, col, v));
+    }
+  }
+}
+
+template <int NW, int KW>
+void launch_rows(const MxArgs& a, int splits, hipStream_t s) {
+  const dim3 grid((unsigned)((a.n + 16 * NW - 1) / (16 * NW)), splits), block(64 * NW * KW);
+  float* part = splits > 1 ? a.partial : nullptr;
+  if (a.out_fmt == 1) hipLaunchKernelGGL((k_mxfp4_rows<NW, KW, float>), grid, block, 0, s, a, part);
+  else if (a.out_fmt == 0) hipLaunchKernelGGL((k_mxfp4_rows<NW, KW, bf16_t>), grid, block, 0, s, a, part);
+  else hipLaunchKernelGGL((k_mxfp4_rows<NW, KW, fp16_t>), grid, block, 0, s, a, part);
+  if (part) launch_join(a, splits, s);
+}
+
+// Rows at multiples of 16 bytes, zeros past their ends, of up to four matrices
+// of bytes: 16 a thread.  Blocks lie along x and y of the grid.
+struct AlignJob {
+  const uint8_t* from;   // NULL: not copied
+  uint8_t* to;
+  int64_t ld, rows;
+  int bytes, pitch;
+};
+struct AlignJobs { AlignJob of[4]; };
+__global__ __launch_bounds__(256) void k_mxfp4_align(AlignJobs jobs) {
+  int64_t i = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const AlignJob& job = jobs.of[q];
+    if (!job.from) continue;
+    const int per = job.pitch / 16;
+    const int64_t n = job.rows * per;
+    if (i >= 0 && i < n) {
+      const int64_t r = i / per;
+      const int c = (int)(i % per) * 16;
+      *(intx4*)(job.to + r * job.pitch + c) = load_chunk((const int8_t*)job.from + r * job.ld, c, job.bytes);
+    }
+    i -= n;
+  }
+}
+
+// Which kernel takes a product, by its sizes alone: as the 8-bit product's,
+// whose stages have as many bytes.
+struct MxPlan {
+  enum { ROWS1, ROWS4, TILE64, TILE128, TILE256 } kind;
+  int splits;
+};
+
+MxPlan mx_plan(int64_t m, int64_t n, int kb) {
+  const int stages = (kb + 127) / 128;
+  if (m <= 16) {
+    if (n >= 64 * 208) return {MxPlan::ROWS4, 1};
+    const int64_t blocks = (n + 15) / 16;
+    return {MxPlan::ROWS1, (int)std::max<int64_t>(1, std::min<int64_t>(256 / blocks, stages / 28))};
+  }
+  const auto tiles = [&](int64_t t) { return (m + t - 1) / t * ((n + t - 1) / t); };
+  MxPlan best{MxPlan::TILE64, 1};
+  double least = 1e30;
+  const auto consider = [&](decltype(MxPlan::TILE64) kind, int64_t t, double alone, double two, double fixed) {
+    for (int s = 1; s <= 16; ++s) {
+      if (s > 1 && stages / s < 4) break;
+      const int64_t blocks = tiles(t) * s;
+      const double round = two > 0 ? (blocks <= 256 ? alone : two * (double)((blocks + 511) / 512))
+                                   : alone * (double)((blocks + 255) / 256);
+      const double us = round * ((stages + s - 1) / s) + fixed + (s > 1 ? 3.0 + 8e-6 * s * (double)m * (double)n / 4.0 : 0.0);
+      if (us < least) {
+        least = us;
+        best = {kind, s};
+      }
+    }
+  };
+  consider(MxPlan::TILE256, 256, 1.31, 0, 9);
+  consider(MxPlan::TILE128, 128, 0.70, 1.28, 5);
+  consider(MxPlan::TILE64, 64, 0.30, 0.55, 3);
+  return best;
+}
+
+// Scratch of a call: the splits' sums, then aligned copies of what is not
+// aligned (copies straight into LDS need rows of whole 16 bytes at multiples
+// of 16, and 31-bit offsets inside a tile).
+struct MxLayout {
+  MxPlan plan;
+  size_t partial, copy[4];   // bytes: sums; a, its scales, b, its scales
+  int pitch[2];              // of codes, of scales
+};
+
+MxLayout mx_layout(const MxArgs& g) {
+  const int nb = (g.kb + 15) / 16;
+  MxLayout l{mx_plan(g.m, g.n, g.kb), 0, {}, {nb * 16, (nb + 15) / 16 * 16}};
+  const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  if (l.plan.splits > 1) l.partial = up((size_t)l.plan.splits * g.m * g.n * 4);
+  if (l.plan.kind == MxPlan::ROWS1 || l.plan.kind == MxPlan::ROWS4 || g.kb == 0) return l;
+  const auto bad = [&](const uint8_t* p, int64_t ld, int bytes) {
+    return ((uintptr_t)p | (uint64_t)ld | (uint64_t)bytes) % 16 != 0 || ld >= (1 << 22);
+  };
+  if (bad(g.a, g.lda, g.kb)) l.copy[0] = up((size_t)g.m * l.pitch[0]);
+  if (bad(g.sa, g.ldsa, nb)) l.copy[1] = up((size_t)g.m * l.pitch[1]);
+  if (bad(g.b, g.ldb, g.kb)) l.copy[2] = up((size_t)g.n * l.pitch[0]);
+  if (bad(g.sb, g.ldsb, nb)) l.copy[3] = up((size_t)g.n * l.pitch[1]);
+  return l;
+}
+
+}  // namespace
+
+size_t mxfp4_linear_scratch(const MxArgs& g) {
+  const MxLayout l = mx_layout(g);
+  return l.partial + l.copy[0] + l.copy[1] + l.copy[2] + l.copy[3];
+}
+
+void launch_mxfp4_linear(MxArgs g, hipStream_t s) {
+  const MxLayout l = mx_layout(g);
+  const int nb = (g.kb + 15) / 16;
+  const uint8_t** at[4] = {&g.a, &g.sa, &g.b, &g.sb};
+  int64_t* ld[4] = {&g.lda, &g.ldsa, &g.ldb, &g.ldsb};
+  AlignJobs jobs{};
+  uint8_t* to = (uint8_t*)g.partial + l.partial;
+  int64_t chunks = 0;
+  for (int q = 0; q < 4; ++q) {
+    if (!l.copy[q]) continue;
+    AlignJob& job = jobs.of[q];
+    job = {*at[q], to, *ld[q], q < 2 ? g.m : g.n, q % 2 ? nb : g.kb, l.pitch[q % 2]};
+    chunks += job.rows * (job.pitch / 16);
+    *at[q] = to;
+    *ld[q] = job.pitch;
+    to += l.copy[q];
+  }
+  if (chunks) {
+    const int64_t blocks = (chunks + 255) / 256, x = std::min<int64_t>(blocks, 1 << 20);
+    hipLaunchKernelGGL(k_mxfp4_align, dim3((unsigned)x, (unsigned)((blocks + x - 1) / x)), dim3(256), 0, s, jobs);
+    if (l.copy[0] || l.copy[2]) g.kb = l.pitch[0];   // the zeros of at least one of the two factors fill the rest
+  }
+  switch (l.plan.kind) {
+    case MxPlan::ROWS1: return launch_rows<1, 16>(g, l.plan.splits, s);
+    case MxPlan::ROWS4: return launch_rows<4, 4>(g, l.plan.splits, s);
+    case MxPlan::TILE64: return launch_mma<64, 64, 2, 2, 4>(g, l.plan.splits, s);
+    case MxPlan::TILE128: return launch_mma<128, 128, 2, 2, 2>(g, l.plan.splits, s);
+    case MxPlan::TILE256: return launch_mma<256, 256, 2, 4, 2>(g, l.plan.splits, s);
+  }
+}
+
+void launch_mxfp4_quantize(int fmt, const MxCodesArgs& a, hipStream_t s) {
+  if (fmt == 1) launch_quantize<float>(a, s);
+  else if (fmt == 0) launch_quantize<bf16_t>(a, s);
+  else launch_quantize<fp16_t>(a, s);
+}
+
+void launch_mxfp4_dequantize(int fmt, const MxCodesArgs& a, hipStream_t s) {
+  if (fmt == 1) launch_dequantize<float>(a, s);
+  else if (fmt == 0) launch_dequantize<bf16_t>(a, s);
+  else launch_dequantize<fp16_t>(a, s);
+}
+
+}  // namespace dion

@@ -122,8 +122,8 @@ def _workspace(nbytes, like, given, stream):
         raise DionError(-1, lib.dion_last_error().decode())
     if given is None:
         given = _new((nbytes + 256,), torch.uint8, like, stream)
-    elif not given.is_cuda or not given.is_contiguous():
-        _fail("the workspace must be a contiguous tensor on the GPU")
+    elif given.get_device() != like.get_device() or not given.is_contiguous():
+        _fail("the workspace must be a contiguous tensor on the GPU of the others")
     at = given.data_ptr()
     off = -at % 256
     have = given.numel() * given.element_size() - off
@@ -390,7 +390,7 @@ class _Gradient(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, *grads):
-        raise RuntimeError("trying to differentiate twice: rms_norm and distill_loss have first derivatives only")
+        raise RuntimeError("trying to differentiate twice: the operators of a training step have first derivatives only")
 
 
 def _once(compute, *tensors):
