@@ -43,41 +43,57 @@ template <int LANES> __device__ __forceinline__ uint32_t block_max(uint32_t v) {
   return v;
 }
 
-// Blocks of 256 threads, TX of them along a row; a thread takes 16 bytes of
-// values.  Grid: rows along x, the rest of long rows along y.
+// Blocks of 256 threads, tx of them along a row; a thread takes 16 bytes of
+// values in each of ROWS rows, all asked for before the first is used.  Grid:
+// rows along x, the rest of long rows along y.
+constexpr int ROWS = 4;
+
 template <typename T>
 __global__ __launch_bounds__(256) void k_mxfp4_quantize(MxCodesArgs a, int tx) {
   typedef Chunk<T> C;
   constexpr int N = C::N, L = MX / N;
   const int t = threadIdx.x % tx, per = (a.cols + MX - 1) / MX * L;
   const int64_t step = (int64_t)gridDim.x * (256 / tx);
-  for (int64_t row = (int64_t)blockIdx.x * (256 / tx) + threadIdx.x / tx; row < a.rows; row += step)
+  for (int64_t row = (int64_t)blockIdx.x * (256 / tx) + threadIdx.x / tx; row < a.rows; row += ROWS * step)
     for (int64_t p = (int64_t)blockIdx.y * tx + t; p < per; p += (int64_t)gridDim.y * tx) {
       const int64_t j = p * N;   // may lie behind the row's end, where values are 0
-      float f[N] = {};
-      if (j < a.cols) C::unpack(C::load((const T*)a.x + row * a.ldx, (int)j, a.cols, 0.f), f);
-      uint32_t top = 0;
+      uintx4 v[ROWS];
 #pragma unroll
-      for (int i = 0; i < N; ++i) top = max(top, __float_as_uint(f[i]) & 0x7fffffffu);
-      top = block_max<L>(top);
-      const bool bad = top >= 0x7f800000u;
-      const int s = bad ? 255 : max(0, (int)((top + 0x200000u) >> 23) - 2);   // 7 = 1.75 2^2: a carry from there on
-      const float inv = __uint_as_float((uint32_t)(254 - min(s, 253)) << 23);   // 2^-e
-      uint32_t q = 0;
-#pragma unroll
-      for (int i = 0; i < N; i += 2) {
-        const float x = bad ? 0.f : f[i] * inv, y = bad ? 0.f : f[i + 1] * inv;
-        if (i == 0) q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, x, y, 1.f, 0);
-        if (i == 2) q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, x, y, 1.f, 1);
-        if (i == 4) q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, x, y, 1.f, 2);
-        if (i == 6) q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, x, y, 1.f, 3);
+      for (int u = 0; u < ROWS; ++u) {
+        v[u] = uintx4{0, 0, 0, 0};
+        if (row + u * step < a.rows && j < a.cols)
+          v[u] = C::load((const T*)a.x + (row + u * step) * a.ldx, (int)j, a.cols, 0.f);
       }
-      uint8_t* o = a.q + row * a.ldq + j / 2;
-      if (j + N <= a.cols) __builtin_memcpy(o, &q, N / 2);
-      else
-        for (int i = 0; 2 * i < N; ++i)
-          if (j + 2 * i < a.cols) o[i] = (uint8_t)(q >> (8 * i));
-      if (t % L == 0) a.s[row * a.lds + p / L] = (uint8_t)s;
+#pragma unroll
+      for (int u = 0; u < ROWS; ++u) {
+        const int64_t r = row + u * step;
+        if (r >= a.rows) break;
+        float f[N];
+        C::unpack(v[u], f);
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) top = max(top, __float_as_uint(f[i]) & 0x7fffffffu);
+        top = block_max<L>(top);
+        const bool bad = top >= 0x7f800000u;
+        const int s = bad ? 255 : max(0, (int)((top + 0x200000u) >> 23) - 2);   // 7 = 1.75 2^2: a carry from there on
+        const float inv = __uint_as_float((uint32_t)(254 - min(s, 253)) << 23);   // 2^-e
+        uint32_t q = 0;
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+          const float x = f[i] * inv, y = f[i + 1] * inv;
+          if (i == 0) q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, x, y, 1.f, 0);
+          if (i == 2) q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, x, y, 1.f, 1);
+          if (i == 4) q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, x, y, 1.f, 2);
+          if (i == 6) q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, x, y, 1.f, 3);
+        }
+        if (bad) q = 0;
+        uint8_t* o = a.q + r * a.ldq + j / 2;
+        if (j + N <= a.cols) __builtin_memcpy(o, &q, N / 2);
+        else
+          for (int i = 0; 2 * i < N; ++i)
+            if (j + 2 * i < a.cols) o[i] = (uint8_t)(q >> (8 * i));
+        if (t % L == 0) a.s[r * a.lds + p / L] = (uint8_t)s;
+      }
     }
 }
 
@@ -88,25 +104,37 @@ __global__ __launch_bounds__(256) void k_mxfp4_dequantize(MxCodesArgs a, int tx)
   constexpr int N = C::N, L = MX / N;
   const int t = threadIdx.x % tx, per = (a.cols + N - 1) / N;
   const int64_t step = (int64_t)gridDim.x * (256 / tx);
-  for (int64_t row = (int64_t)blockIdx.x * (256 / tx) + threadIdx.x / tx; row < a.rows; row += step)
+  for (int64_t row = (int64_t)blockIdx.x * (256 / tx) + threadIdx.x / tx; row < a.rows; row += ROWS * step)
     for (int64_t p = (int64_t)blockIdx.y * tx + t; p < per; p += (int64_t)gridDim.y * tx) {
       const int64_t j = p * N;
-      const uint8_t* c = a.q + row * a.ldq + j / 2;
-      uint32_t q = 0;
-      if (j + N <= a.cols) __builtin_memcpy(&q, c, N / 2);
-      else
-        for (int i = 0; 2 * i < N; ++i)
-          if (j + 2 * i < a.cols) q |= (uint32_t)c[i] << (8 * i);
-      const int s = a.s[row * a.lds + p / L];
-      float f[N];
+      uint32_t q[ROWS];
+      int s[ROWS];
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const uint32_t code = q >> (4 * i) & 7;
-        // 0, 0.5 and the others, whose bits are an exponent's and a mantissa's
-        const float v = code < 2 ? 0.5f * code : __uint_as_float((code << 22) + (126u << 23));
-        f[i] = s == 255 ? __builtin_nanf("") : ldexpf(q >> (4 * i) & 8 ? -v : v, s - 127);
+      for (int u = 0; u < ROWS; ++u) {
+        const int64_t r = row + u * step;
+        q[u] = 0, s[u] = 0;
+        if (r >= a.rows) break;
+        const uint8_t* c = a.q + r * a.ldq + j / 2;
+        if (j + N <= a.cols) __builtin_memcpy(&q[u], c, N / 2);
+        else
+          for (int i = 0; 2 * i < N; ++i)
+            if (j + 2 * i < a.cols) q[u] |= (uint32_t)c[i] << (8 * i);
+        s[u] = a.s[r * a.lds + p / L];
       }
-      C::store_near((T*)a.x + row * a.ldx, (int)j, a.cols, f);
+#pragma unroll
+      for (int u = 0; u < ROWS; ++u) {
+        const int64_t r = row + u * step;
+        if (r >= a.rows) break;
+        float f[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const uint32_t code = q[u] >> (4 * i) & 7;
+          // 0, 0.5 and the others, whose bits are an exponent's and a mantissa's
+          const float v = code < 2 ? 0.5f * code : __uint_as_float((code << 22) + (126u << 23));
+          f[i] = s[u] == 255 ? __builtin_nanf("") : ldexpf(q[u] >> (4 * i) & 8 ? -v : v, s[u] - 127);
+        }
+        C::store_near((T*)a.x + r * a.ldx, (int)j, a.cols, f);
+      }
     }
 }
 
@@ -116,9 +144,10 @@ int along(int64_t pieces) {
   while (tx < 256 && tx < pieces) tx *= 2;
   return tx;
 }
+// A row to a thread while there are no more than fill the CUs, ROWS otherwise.
 dim3 codes_grid(const MxCodesArgs& a, int64_t pieces, int tx) {
-  return dim3((unsigned)std::min<int64_t>((a.rows + 256 / tx - 1) / (256 / tx), 1 << 20),
-              (unsigned)std::min<int64_t>((pieces + tx - 1) / tx, 1 << 15));
+  const int64_t x = (a.rows + 256 / tx - 1) / (256 / tx), y = std::min<int64_t>((pieces + tx - 1) / tx, 1 << 15);
+  return dim3((unsigned)std::min<int64_t>(x * y <= 2048 ? x : (x + ROWS - 1) / ROWS, 1 << 20), (unsigned)y);
 }
 
 template <typename T> void launch_quantize(const MxCodesArgs& a, hipStream_t s) {
@@ -188,29 +217,25 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mxfp4_mma(MxArgs g, float* par
   const uint32_t lds0 = (uint32_t)(uintptr_t)((__attribute__((address_space(3))) uint8_t*)smem);
 
   // piece q = wave + i W of a stage: rows PR q .. of a, then of b; lane l has
-  // row l / CR and the chunk whose place is l % CR
-  uint32_t voff[NP];
-  int vk[NP];
+  // row l / CR and the chunk whose place is l % CR (the same chunk in all of
+  // its pieces: W PR is a multiple of 16).  Rows past the tile's last are
+  // behind the descriptors' ends.
+  static_assert(W * PR % 16 == 0 && BM / PR % W == 0, "a piece index is of one matrix and one swizzle");
   const intx4 ra = raw_buffer(g.a + m0 * g.lda, (uint32_t)((rm - 1) * g.lda + g.kb));
   const intx4 rb = raw_buffer(g.b + n0 * g.ldb, (uint32_t)((rn - 1) * g.ldb + g.kb));
   const intx4 rsa = raw_buffer(g.sa + m0 * g.ldsa, (uint32_t)((rm - 1) * g.ldsa + sb16));
   const intx4 rsb = raw_buffer(g.sb + n0 * g.ldsb, (uint32_t)((rn - 1) * g.ldsb + sb16));
-#pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    const int q = wave + i * W;
-    const bool isa = q < BM / PR;
-    const int r = (isa ? q : q - BM / PR) * PR + lane / CR;
-    vk[i] = swz(r, lane % CR) * 16;
-    voff[i] = r < (isa ? rm : rn) ? (uint32_t)(r * (isa ? g.lda : g.ldb)) + vk[i] : OUT_OF_RANGE;
-  }
+  const int prow = wave * PR + lane / CR, vk = swz(prow, lane % CR) * 16;
+  const uint32_t va = (uint32_t)(prow * (int)g.lda + vk), vb = (uint32_t)(prow * (int)g.ldb + vk);
   // piece `wave` of a pair's scales: rows 64 wave .. of a, then of b, one to a lane
   const bool sisa = wave < BM / 64;
   const int sr = (sisa ? wave : wave - BM / 64) * 64 + lane;
   const uint32_t soff = sr < (sisa ? rm : rn) ? (uint32_t)(sr * (sisa ? g.ldsa : g.ldsb)) : OUT_OF_RANGE;
   auto issue = [&](int kt, int i) {   // piece i of stage kt
+    constexpr int A = BM / PR / W;   // pieces of a
     const int k0 = (kt0 + kt) * BK, q = wave + i * W;
-    const uint32_t v = k0 + vk[i] < g.kb ? voff[i] : OUT_OF_RANGE;
-    dma16(v, q < BM / PR ? ra : rb, (uint32_t)k0,
+    const uint32_t v = i < A ? va + (uint32_t)(i * W * PR * (int)g.lda) : vb + (uint32_t)((i - A) * W * PR * (int)g.ldb);
+    dma16(k0 + vk < g.kb ? v : OUT_OF_RANGE, i < A ? ra : rb, (uint32_t)k0,
           (uint32_t)__builtin_amdgcn_readfirstlane(lds0 + (kt % S) * STAGE + q * 1024));
   };
   auto issue_scales = [&](int kt) {   // with the first of a pair's stages
@@ -301,6 +326,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mxfp4_mma(MxArgs g, float* par
 #pragma unroll
           for (int j = 0; j < FN; ++j) {
             acc[i][j] = mma32(fb[ks & 1][j], fa[ks & 1][i], acc[i][j], sb[j], sa[i], ks);
+            asm volatile("" : "+v"(acc[i][j]));   // here: the compiler would move products behind later branches
             const int t = i * FN + j;
             if (SPREAD && w < 2 && t % EVERY == EVERY - 1) {
               __builtin_amdgcn_sched_barrier(0);
