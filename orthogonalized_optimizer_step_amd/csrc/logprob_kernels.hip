@@ -23,26 +23,45 @@ constexpr float NEG = -__builtin_inff(), LOWEST = -3.402823466e+38f;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float r;
+  asm("v_min3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
 __device__ __forceinline__ float factor(float v) { return fmaxf(v, -200.f); }
 
-// Sums over what was seen of a row, relative to its largest value m (or the
-// lowest finite one, so that m is always finite or +inf): s of 2^v and w of
-// 2^v v, with v = (z - m) c, c = log2(e) / T.  A NaN or +inf makes s NaN.
-struct Sums {
-  float m, s, w;
-  __device__ __forceinline__ void clear() { m = LOWEST, s = w = 0.f; }
+// While a row is read exponents are powers of two, v = z c - R with c = log2(e)
+// / T and R = fl(m c), one fma each.  The rounding of R is the same in every
+// term, as long as sums go from one reference to another by the rounded R's,
+// and is taken out of the row's sums at their end.  References of a mask's
+// size (|m c| from WIDE on), for which it would not stay small, are taken by
+// differences instead: v = (z - m) c.
+constexpr float WIDE = 0x1.fp18f, FLOOR = 0x1p19f;
+
+// Sums over what was seen of a row, relative to its largest value m: s of 2^v
+// and w of 2^v v.  FAR sums go by differences and start from the lowest finite
+// value; the others from a floor (m c = -2^19), by which masked entries are 0:
+// a row with nothing above it, or that is wide, is summed again by the former.
+// A NaN or +inf makes s NaN.
+template <bool FAR> struct Sums {
+  float m, r, s, w;
+  __device__ __forceinline__ static float start(float temp) { return FAR ? LOWEST : fmaxf(-(FLOOR * LN2) * temp, LOWEST); }
+  __device__ __forceinline__ void clear(float temp, float c) { m = start(temp), r = m * c, s = w = 0.f; }
   __device__ __forceinline__ void to(float other, float c) {   // relative to another value, at least m
-    const float d = (m - other) * c, f = exp2_fast(d);
-    w = f * (w + s * factor(d));
+#pragma clang fp contract(off)   // R is rounded first
+    const float o = other * c, d = FAR ? (m - other) * c : r - o, f = exp2_fast(d);
+    w = f * (w + s * (FAR ? factor(d) : d));
     s *= f;
     m = other;
+    r = o;
   }
-  template <int N> __device__ __forceinline__ void add(const float* z, float c) {
+  // CLAMP: for chunks with elements so far below m that v would be -inf
+  template <bool CLAMP, int N> __device__ __forceinline__ void add(const float* z, float c) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float v = (z[i] - m) * c, e = exp2_fast(v);
+      const float v = FAR ? (z[i] - m) * c : fmaf(z[i], c, -r), e = exp2_fast(v);
       s += e;
-      w += e * factor(v);
+      w += e * (FAR || CLAMP ? factor(v) : v);
     }
   }
   // over the block, the same in every thread
@@ -54,13 +73,21 @@ struct Sums {
     const int lane = threadIdx.x & 63;
     if (lane == 0) red[0][threadIdx.x >> 6] = m, red[1][threadIdx.x >> 6] = s, red[2][threadIdx.x >> 6] = w;
     lds_barrier();
-    m = lane < W ? red[0][lane] : LOWEST;
+    m = red[0][lane % W];
+    r = m * c;
     s = lane < W ? red[1][lane] : 0.f;
     w = lane < W ? red[2][lane] : 0.f;
-    to(row_reduce<W>(m, LOWEST, MaxNan()), c);
+    to(row_reduce<W>(lane < W ? m : LOWEST, LOWEST, MaxNan()), c);
     s = row_reduce<W>(s, 0.f, Add());
     w = row_reduce<W>(w, 0.f, Add());
+    lds_barrier();   // red may be written again
+    if (!FAR) {   // every v is larger by what R was rounded by
+      const float off = fmaf(m, c, -r), f = exp2_fast(-off);
+      w = (w - off * s) * f;
+      s *= f;
+    }
   }
+  __device__ __forceinline__ bool wide(float c) const { return !(fabsf(m * c) < WIDE); }
 };
 
 // Logits as whole numbers in their order, -inf and NaN as 0 (no alternative), -0 as 0.
@@ -88,26 +115,29 @@ template <int NT> struct TopShared {
   __attribute__((aligned(16))) int count[2][NT / 64];
   int entry[KEYS * (NT / 64)];
   int total;
-  int id[2][kLogprobMaxTop];                 // the selected, ascending, of two levels in turn
-  uint32_t key[kLogprobMaxTop];
-  unsigned long long order[kLogprobMaxTop];   // key above, the lower index first
+  int id[2][NT];                  // the selected, ascending, of two levels in turn (k <= NT)
+  uint32_t key[NT];
+  unsigned long long order[NT];   // key above, the lower index first
+  uint32_t group[KEYS * NT];      // the largest of each group, as keys
 };
 
-// The k largest of n = K NT keys (key i of thread t has position i NT + t),
+// The k largest of n <= K NT keys (key i of thread t has position i NT + t),
 // equal ones by their position: put(i, o) is called for each with its place o
 // in the order of positions.  The k-th largest key is found bit by bit, by
-// counting the keys that are at least as large.  k <= the keys that count.
+// counting the keys that are at least as large.
 template <int NT, int K, int BITS, typename Put>
-__device__ __forceinline__ void select(const uint32_t (&key)[K], int k, TopShared<NT>& sh, Put put) {
+__device__ __forceinline__ void select(const uint32_t (&key)[K], int n, int k, TopShared<NT>& sh, Put put) {
   constexpr int W = NT / 64;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int used = (n + NT - 1) / NT;
   uint32_t least = 0;
   int turn = 0;
   for (int b = BITS - 1; b >= 0; --b) {
     const uint32_t cand = least | 1u << b;
     int c = 0;
 #pragma unroll
-    for (int i = 0; i < K; ++i) c += __popcll(__ballot(key[i] >= cand));
+    for (int i = 0; i < K; ++i)
+      if (i < used) c += __popcll(__ballot(key[i] >= cand));
     if (lane == 0) sh.count[turn][wave] = c;
     lds_barrier();
     int total = 0;
@@ -161,16 +191,32 @@ __device__ __forceinline__ void select(const uint32_t (&key)[K], int k, TopShare
   lds_barrier();
 }
 
-// One row to a block.  A thread's group i is the P chunks of 16 bytes from
-// chunk (i NT + t) P on: groups are in the order of the row.  With the
-// alternatives (TOP), the largest of each group is kept, for the k largest
-// logits lie in the k groups with the largest maxima (equal ones by their
-// order): k other groups' maxima come before anything in the rest.  The same
-// again for parts of those groups, down to single logits.
-template <typename Z, int NT, bool TOP>
-__global__ __launch_bounds__(NT) void k_logprobs(LogprobArgs a, int P) {
+// The rest of a row's chunks one by one, for sums by differences.
+template <typename Z, int NT>
+__device__ __forceinline__ void far_sums(const Z* z, int vocab, float temp, float c, Sums<true>& S) {
   typedef Chunk<Z> C;
-  constexpr int N = C::N, U = 4;
+  S.clear(temp, c);
+  for (int64_t j = threadIdx.x * C::N; j < vocab; j += NT * C::N) {
+    const uintx4 v = C::load(z, (int)j, vocab, NEG);
+    const float top = C::largest(S.m, v);
+    if (top > S.m) S.to(top, c);
+    float f[C::N];
+    C::unpack(v, f);
+    S.template add<true, C::N>(f, c);
+  }
+}
+
+// One row to a block, read once, chunk i NT + t of 16 bytes by thread t, U of
+// them at once and the next U asked for before they are used.  With the
+// alternatives (TOP), the largest of each group of 2^lg neighbouring chunks is
+// kept in LDS, for the k largest logits lie in the k groups with the largest
+// maxima (equal ones by their order): k other groups' maxima come before
+// anything in the rest.  The same again for parts of those groups, which are
+// in the caches, down to single logits.
+template <typename Z, int NT, bool TOP>
+__global__ __launch_bounds__(NT, 4) void k_logprobs(LogprobArgs a, int lg) {
+  typedef Chunk<Z> C;
+  constexpr int N = C::N, U = 4, STEP = NT * N;
   __shared__ float red[3][NT / 64];
   __shared__ TopShared<TOP ? NT : 64> sh;
   const float c = LOG2E / a.temp;
@@ -184,71 +230,98 @@ __global__ __launch_bounds__(NT) void k_logprobs(LogprobArgs a, int P) {
       if (token >= 0 && token < a.vocab) zt = to_f(z[token]);
       else token = -1;
     }
-    Sums S;
-    S.clear();
-    uint32_t key[TOP ? KEYS : 1];
-    // U groups at once, chunk p of each
-    auto absorb = [&](const uintx4 (&v)[U], float (&most)[U]) {
-      float top = S.m;
+    Sums<false> S;
+    S.clear(a.temp, c);
+    auto absorb = [&](const uintx4 (&v)[U], int step) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        most[u] = C::largest(most[u], v[u]);
-        top = fmaxf(top, most[u]);
-      }
-      if (top > S.m) S.to(top, c);
+      for (int h = 0; h < U; h += 2) {   // two chunks: as many values as there are registers for
+        float f[2][N], top = S.m, low = __builtin_inff();
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        float f[N];
-        C::unpack(v[u], f);
-        S.template add<N>(f, c);
-      }
-    };
-    auto groups = [&](int i, float (&most)[U]) {
-      for (int p = 0; p < P; ++p) {
-        uintx4 v[U];
+        for (int u = 0; u < 2; ++u) {
+          C::unpack(v[h + u], f[u]);
+          float most = NEG;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int64_t j = (((int64_t)(i + u) * NT + t) * P + p) * N;
-          v[u] = C::load(z, (int)min(j, (int64_t)a.vocab), a.vocab, NEG);
+          for (int i = 0; i < N; i += 2) {
+            most = max3(most, f[u][i], f[u][i + 1]);
+            low = min3(low, f[u][i], f[u][i + 1]);
+          }
+          top = fmaxf(top, most);
+          if (TOP) {
+            if (lg >= 2) {
+              most = fmaxf(most, lane_move<0xb1, 0xf>(most, most));   // lane xor 1
+              most = fmaxf(most, lane_move<0x4e, 0xf>(most, most));   // lane xor 2
+            }
+            if (lg == 3) most = fmaxf(most, lane_move<0x141, 0xf>(most, most));   // the other half of 8
+            if ((t & ((1 << lg) - 1)) == 0) sh.group[((step + h + u) * NT + t) >> lg] = Key<Z>::of(most);
+          }
         }
-        absorb(v, most);
+        if (top > S.m) S.to(top, c);
+        if (!(fmaf(low, c, -S.r) > -200.f)) {
+          S.template add<true, N>(f[0], c);
+          S.template add<true, N>(f[1], c);
+        } else {
+          S.template add<false, N>(f[0], c);
+          S.template add<false, N>(f[1], c);
+        }
       }
     };
-    if constexpr (TOP) {
+    const int whole = a.vocab / STEP / U * U;   // steps in batches of whole chunks
+    if (whole > 0) {
+      uintx4 v[U], next[U];
+      const Z* p = z + t * N;
 #pragma unroll
-      for (int i = 0; i < KEYS; i += U) {
-        float most[U] = {NEG, NEG, NEG, NEG};
-        if ((int64_t)i * NT * P * N < a.vocab) groups(i, most);
+      for (int u = 0; u < U; ++u) v[u] = *(const uintx4u*)(p + (int64_t)u * STEP);
+      for (int i = 0; i < whole; i += U) {
+        if (i + U < whole) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) key[i + u] = Key<Z>::of(most[u]);
-      }
-    } else {
-      for (int i = 0; (int64_t)i * NT * P * N < a.vocab; i += U) {
-        float most[U] = {NEG, NEG, NEG, NEG};
-        groups(i, most);
+          for (int u = 0; u < U; ++u) next[u] = *(const uintx4u*)(p + (int64_t)(i + U + u) * STEP);
+        }
+        absorb(v, i);
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = next[u];
       }
     }
+    if ((int64_t)whole * STEP < a.vocab) {   // fewer than U steps and a part of one
+      uintx4 v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t j = (int64_t)(whole + u) * STEP + t * N;
+        v[u] = C::load(z, (int)min(j, (int64_t)a.vocab), a.vocab, NEG);
+      }
+      absorb(v, whole);
+    }
     S.template join<NT>(c, red);
+    float m = S.m, s = S.s, w = S.w;
+    if (S.wide(c)) {   // rare: again, from the caches
+      Sums<true> F;
+      far_sums<Z, NT>(z, a.vocab, a.temp, c, F);
+      F.template join<NT>(c, red);
+      m = F.m, s = F.s, w = F.w;
+    }
     // a row with nothing but -inf has no distribution: logprob -inf, entropy 0
-    const bool none = S.s == 0.f;
-    const float logs = logf(S.s), entropy = none ? 0.f : logs - S.w / S.s * LN2;
-    auto logprob = [&](float v) { return none ? NEG : (v - S.m) / a.temp - logs; };
+    const bool none = s == 0.f;
+    const float logs = logf(s), entropy = none ? 0.f : logs - w / s * LN2;
+    auto logprob = [&](float v) { return none ? NEG : (v - m) / a.temp - logs; };
     if (t == 0) {
       if (a.tok) a.logprob[row] = token >= 0 ? logprob(zt) : 0.f;
       a.entropy[row] = entropy;
-      if (a.stats) a.stats[row] = make_float4(S.m, S.s, entropy, logs);
+      if (a.stats) a.stats[row] = make_float4(m, s, entropy, logs);
     }
     if constexpr (TOP) {
-      int size = P * N, n = (a.vocab + size - 1) / size, k = min(a.k, n), turn = 0;
-      select<NT, KEYS, Key<Z>::BITS>(key, k, sh, [&](int i, int o) {
-        sh.id[0][o] = i * NT + t;
-        sh.key[o] = key[i];
-      });
+      int size = N << lg, n = (a.vocab + size - 1) / size, k = min(a.k, n), turn = 0;
+      {
+        uint32_t key[KEYS];   // (written before the joins' barriers)
+#pragma unroll
+        for (int i = 0; i < KEYS; ++i) key[i] = i * NT + t < n ? sh.group[i * NT + t] : 0;
+        select<NT, KEYS, Key<Z>::BITS>(key, n, k, sh, [&](int i, int o) {
+          sh.id[0][o] = i * NT + t;
+          sh.key[o] = key[i];
+        });
+      }
       while (size > 1) {
         const int part = max(1, size / SUB), r = size / part;
         uint32_t sub[SUB];
         int id[SUB];
-        n = 0;
 #pragma unroll
         for (int i = 0; i < SUB; ++i) {
           const int q = i * NT + t;
@@ -257,10 +330,10 @@ __global__ __launch_bounds__(NT) void k_logprobs(LogprobArgs a, int P) {
           if (q < k * r) {
             id[i] = sh.id[turn][q / r] * r + q % r;
             const int j = id[i] * part;
-            float m = NEG;
+            float top = NEG;
             for (int e = 0; e < part; ++e)
-              if (j + e < a.vocab) m = fmaxf(m, to_f(z[j + e]));
-            sub[i] = Key<Z>::of(m);
+              if (j + e < a.vocab) top = fmaxf(top, to_f(z[j + e]));
+            sub[i] = Key<Z>::of(top);
           }
         }
         // the parts that lie in the row at all: only its last group may hold others, behind them
@@ -268,34 +341,41 @@ __global__ __launch_bounds__(NT) void k_logprobs(LogprobArgs a, int P) {
         n = k * r - max(0, (last + 1) * r - parts);
         k = min(a.k, n);
         turn ^= 1;
-        select<NT, SUB, Key<Z>::BITS>(sub, k, sh, [&](int i, int o) {
+        select<NT, SUB, Key<Z>::BITS>(sub, n, k, sh, [&](int i, int o) {
           sh.id[turn][o] = id[i];
           sh.key[o] = sub[i];
         });
         size = part;
       }
-      // in order: a bitonic sort of as many places as a power of two
+      // in order: a bitonic sort of as many places as a power of two, by one
+      // wave (whose accesses to LDS keep their order) where it has that many lanes
       int places = 2;
       while (places < k) places *= 2;
-      for (int i = t; i < places; i += NT)
-        sh.order[i] = i < k ? (unsigned long long)sh.key[i] << 32 | (0xffffffffu - (uint32_t)sh.id[turn][i]) : 0;
-      lds_barrier();
-      for (int len = 2; len <= places; len *= 2)
-        for (int d = len / 2; d > 0; d /= 2) {
-          for (int q = t; q < places / 2; q += NT) {
-            const int lo = q / d * 2 * d + q % d, hi = lo + d;
-            const unsigned long long x = sh.order[lo], y = sh.order[hi];
-            if ((x < y) == ((lo & len) == 0)) sh.order[lo] = y, sh.order[hi] = x;
+      const bool one = places <= 128;
+      if (!one || t < 64) {
+        const int step = one ? 64 : NT;
+        for (int i = t; i < places; i += step)
+          sh.order[i] = i < k ? (unsigned long long)sh.key[i] << 32 | (0xffffffffu - (uint32_t)sh.id[turn][i]) : 0;
+        if (!one) lds_barrier();
+        else asm volatile("" : : : "memory");
+        for (int len = 2; len <= places; len *= 2)
+          for (int d = len / 2; d > 0; d /= 2) {
+            for (int q = t; q < places / 2; q += step) {
+              const int lo = q / d * 2 * d + q % d, hi = lo + d;
+              const unsigned long long x = sh.order[lo], y = sh.order[hi];
+              if ((x < y) == ((lo & len) == 0)) sh.order[lo] = y, sh.order[hi] = x;
+            }
+            if (!one) lds_barrier();
+            else asm volatile("" : : : "memory");
           }
-          lds_barrier();
+        for (int i = t; i < a.k; i += step) {
+          const uint32_t best = i < k ? (uint32_t)(sh.order[i] >> 32) : 0;
+          a.top[row * a.k + i] = best ? logprob(Key<Z>::value(best)) : NEG;
+          a.index[row * a.k + i] = best ? (int64_t)(0xffffffffu - (uint32_t)sh.order[i]) : -1;
         }
-      for (int i = t; i < a.k; i += NT) {
-        const uint32_t best = i < k ? (uint32_t)(sh.order[i] >> 32) : 0;
-        a.top[row * a.k + i] = best ? logprob(Key<Z>::value(best)) : NEG;
-        a.index[row * a.k + i] = best ? (int64_t)(0xffffffffu - (uint32_t)sh.order[i]) : -1;
       }
+      lds_barrier();   // the next row's groups may be written
     }
-    lds_barrier();   // the next row's sums may be written
   }
 }
 
@@ -313,7 +393,7 @@ __global__ __launch_bounds__(NT) void k_logprobs_backward(LogprobArgs a) {
     const float gl = a.gl && token >= 0 ? a.gl[row] : 0.f, ge = a.ge ? a.ge[row] : 0.f;
     const float4 st = a.stats[row];   // m, s, entropy, log s
     const bool zero = (gl == 0.f && ge == 0.f) || st.y == 0.f;
-    // q (gl + ge (log q + entropy)) = exp2(v) (slope + rise v) / s
+    // q (gl + ge (log q + entropy)) = 2^v (slope + rise v) / s
     const float k = -it / st.y, rise = ge * LN2, slope = gl + ge * (st.z - st.w);
     for (int64_t j = ((int64_t)blockIdx.y * NT + threadIdx.x) * N; j < a.vocab; j += (int64_t)gridDim.y * NT * N) {
       float f[N] = {};
@@ -336,23 +416,22 @@ __global__ __launch_bounds__(NT) void k_logprobs_backward(LogprobArgs a) {
 }
 
 template <typename Z, int NT, bool TOP>
-void launch_rows(const LogprobArgs& a, int P, hipStream_t s) {
-  hipLaunchKernelGGL((k_logprobs<Z, NT, TOP>), dim3((unsigned)std::min<int64_t>(a.rows, 1 << 20)), dim3(NT), 0, s, a, P);
+void launch_rows(const LogprobArgs& a, int lg, hipStream_t s) {
+  hipLaunchKernelGGL((k_logprobs<Z, NT, TOP>), dim3((unsigned)std::min<int64_t>(a.rows, 1 << 20)), dim3(NT), 0, s, a, lg);
 }
 
 template <typename Z> void launch_forward(const LogprobArgs& a, hipStream_t s) {
   constexpr int N = Chunk<Z>::N;
   if (a.k == 0) {
-    if (a.vocab <= 256 * 8 * N) launch_rows<Z, 256, false>(a, 1, s);
-    else if (a.rows > 256) launch_rows<Z, 512, false>(a, 1, s);
-    else launch_rows<Z, 1024, false>(a, 1, s);
-  } else if (a.vocab <= 256 * KEYS * N && a.k <= 256) {
-    launch_rows<Z, 256, true>(a, 1, s);
-  } else {
-    int P = 1;
-    while ((int64_t)P * 1024 * KEYS * N < a.vocab) P *= 2;
-    launch_rows<Z, 1024, true>(a, P, s);
+    if (a.rows > 512 || a.vocab <= 256 * 8 * N) launch_rows<Z, 256, false>(a, 0, s);
+    else launch_rows<Z, 1024, false>(a, 0, s);
+    return;
   }
+  // groups of one, four or eight chunks, as many as the keys that the threads hold
+  const auto groups = [&](int64_t nt) { return a.vocab <= nt * KEYS * N ? 0 : a.vocab <= nt * KEYS * N * 4 ? 2 : 3; };
+  const bool small = a.k <= 256 && a.vocab <= 256 * KEYS * N * 8;
+  if (small && (a.rows > 512 || a.vocab <= 256 * 8 * N)) launch_rows<Z, 256, true>(a, groups(256), s);
+  else launch_rows<Z, 1024, true>(a, groups(1024), s);
 }
 
 template <typename Z> void launch_gradient(const LogprobArgs& a, hipStream_t s) {
