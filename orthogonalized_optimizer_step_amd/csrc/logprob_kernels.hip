@@ -92,7 +92,7 @@ template <bool FAR> struct Sums {
 
 // Logits as whole numbers in their order, -inf and NaN as 0 (no alternative), -0 as 0.
 template <typename Z> struct Key {
-  static constexpr int BITS = 8 * sizeof(Z);
+  static constexpr int BITS = 8 * sizeof(Z), MANTISSA = sizeof(Z) == 4 ? 23 : sizeof(Z) == 2 && (float)(Z)257.f == 257.f ? 10 : 7;
   static __device__ __forceinline__ uint32_t of(float z) {
     union { Z z; uint16_t h; uint32_t w; } c;
     c.w = 0;
@@ -113,20 +113,57 @@ constexpr int KEYS = 16, SUB = 8;   // keys a thread holds: of a row's groups, o
 
 template <int NT> struct TopShared {
   __attribute__((aligned(16))) int count[2][NT / 64];
-  int entry[KEYS * (NT / 64)];
-  int total;
-  int id[2][NT];                  // the selected, ascending, of two levels in turn (k <= NT)
-  uint32_t key[NT];
-  unsigned long long order[NT];   // key above, the lower index first
-  uint32_t group[KEYS * NT];      // the largest of each group, as keys
+  int total, listed[2];
+  union {
+    struct {   // of select()
+      int entry[KEYS * (NT / 64)];
+      int id[2][NT];                                            // the selected, ascending, of two levels in turn (k <= NT)
+      uint32_t key[NT];
+    };
+    int near[2 * NT];   // groups that may hold one of the largest
+  };
+  __attribute__((aligned(16))) unsigned long long order[2 * NT];   // key above, the lower index first
+  uint32_t group[KEYS * NT];                                    // the largest of each group, as keys
 };
+
+// How many of the block's n keys are at least `least`, the same in every thread.
+// (key(i): key i of the thread, the first `used` of K.)
+template <int NT, int K, typename Key>
+__device__ __forceinline__ int count_keys(Key key, int used, uint32_t least, TopShared<NT>& sh, int& turn) {
+  constexpr int W = NT / 64;
+  int c = 0;
+#pragma unroll
+  for (int i = 0; i < K; ++i)
+    if (i < used) c += __popcll(__ballot(key(i) >= least));
+  if ((threadIdx.x & 63) == 0) sh.count[turn][threadIdx.x >> 6] = c;
+  lds_barrier();
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < W; w += 4) {
+    const intx4 v = *(const intx4*)(sh.count[turn] + w);
+    total += v[0] + v[1] + v[2] + v[3];
+  }
+  turn ^= 1;
+  return total;
+}
+
+// Lanes with `yes` get places in a list in LDS, in no order that matters; the
+// others a place behind any list's end.
+__device__ __forceinline__ int place(bool yes, int* listed) {
+  const unsigned long long all = __ballot(yes);
+  if (!all) return 1 << 30;
+  int at = 0;
+  if ((threadIdx.x & 63) == 0) at = atomicAdd(listed, (int)__popcll(all));
+  at = __builtin_amdgcn_readfirstlane(at);
+  return yes ? at + (int)__popcll(all & ((1ull << (threadIdx.x & 63)) - 1)) : 1 << 30;
+}
 
 // The k largest of n <= K NT keys (key i of thread t has position i NT + t),
 // equal ones by their position: put(i, o) is called for each with its place o
 // in the order of positions.  The k-th largest key is found bit by bit, by
 // counting the keys that are at least as large.
-template <int NT, int K, int BITS, typename Put>
-__device__ __forceinline__ void select(const uint32_t (&key)[K], int n, int k, TopShared<NT>& sh, Put put) {
+template <int NT, int K, int BITS, typename Key, typename Put>
+__device__ __forceinline__ void select(Key key, int n, int k, TopShared<NT>& sh, Put put) {
   constexpr int W = NT / 64;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int used = (n + NT - 1) / NT;
@@ -134,26 +171,15 @@ __device__ __forceinline__ void select(const uint32_t (&key)[K], int n, int k, T
   int turn = 0;
   for (int b = BITS - 1; b >= 0; --b) {
     const uint32_t cand = least | 1u << b;
-    int c = 0;
-#pragma unroll
-    for (int i = 0; i < K; ++i)
-      if (i < used) c += __popcll(__ballot(key[i] >= cand));
-    if (lane == 0) sh.count[turn][wave] = c;
-    lds_barrier();
-    int total = 0;
-#pragma unroll
-    for (int w = 0; w < W; w += 4) {
-      const intx4 v = *(const intx4*)(sh.count[turn] + w);
-      total += v[0] + v[1] + v[2] + v[3];
-    }
-    turn ^= 1;
+    const int total = count_keys<NT, K>(key, used, cand, sh, turn);
     if (total >= k) least = cand;
     if (total == k) break;
   }
   // what lies above it, and the first of those equal to it
 #pragma unroll
   for (int i = 0; i < K; ++i) {
-    const int e = __popcll(__ballot(key[i] > least)) | __popcll(__ballot(key[i] == least)) << 16;
+    const uint32_t v = key(i);
+    const int e = __popcll(__ballot(v > least)) | __popcll(__ballot(v == least)) << 16;
     if (lane == 0) sh.entry[i * W + wave] = e;
   }
   lds_barrier();
@@ -183,10 +209,11 @@ __device__ __forceinline__ void select(const uint32_t (&key)[K], int n, int k, T
   const unsigned long long below = (1ull << lane) - 1;
 #pragma unroll
   for (int i = 0; i < K; ++i) {
-    const unsigned long long more = __ballot(key[i] > least), same = __ballot(key[i] == least);
+    const uint32_t v = key(i);
+    const unsigned long long more = __ballot(v > least), same = __ballot(v == least);
     const int e = sh.entry[i * W + wave];
     const int gt = (e & 0xffff) + __popcll(more & below), eq = (e >> 16) + __popcll(same & below);
-    if (key[i] > least || (key[i] == least && eq < need)) put(i, gt + min(eq, need));
+    if (v > least || (v == least && eq < need)) put(i, gt + min(eq, need));
   }
   lds_barrier();
 }
@@ -309,16 +336,82 @@ __global__ __launch_bounds__(NT, 4) void k_logprobs(LogprobArgs a, int lg) {
     }
     if constexpr (TOP) {
       int size = N << lg, n = (a.vocab + size - 1) / size, k = min(a.k, n), turn = 0;
+      auto output = [&](int i, unsigned long long v) {   // place i
+        const uint32_t best = (uint32_t)(v >> 32);
+        a.top[row * a.k + i] = best ? logprob(Key<Z>::value(best)) : NEG;
+        a.index[row * a.k + i] = best ? (int64_t)(0xffffffffu - (uint32_t)v) : -1;
+      };
+      auto pair = [&](uint32_t key, int id) { return (unsigned long long)key << 32 | (0xffffffffu - (uint32_t)id); };
+      bool done = false;
       {
-        uint32_t key[KEYS];   // (written before the joins' barriers)
+        const auto key = [&](int i) { return i * NT + t < n ? sh.group[i * NT + t] : 0u; };   // (written before the joins' barriers)
+        // A bound that few groups reach, k or more of them where there are as
+        // many: down from the largest in growing steps, then between the last two.
+        const int used = (n + NT - 1) / NT, few = min(2 * NT, 2 * a.k + 64);
+        const uint32_t top = Key<Z>::of(m);
+        uint32_t lo = top + 1, hi = top + 1, step = 1u << (Key<Z>::MANTISSA - 1);
+        int reach = 0;
+        while (reach < a.k && lo > 1) {
+          hi = lo;
+          lo = top > step ? top - step + 1 : 1;
+          step = step >> 31 ? ~0u : 2 * step;
+          reach = count_keys<NT, KEYS>(key, used, lo, sh, turn);
+        }
+        while (reach > few && hi - lo > 1) {
+          const uint32_t mid = lo + (hi - lo) / 2;
+          const int c = count_keys<NT, KEYS>(key, used, mid, sh, turn);
+          if (c >= a.k) lo = mid, reach = c;
+          else hi = mid;
+        }
+        if (reach <= few) {
+          // everything that reaches it lies in them; each is ranked against all others
+          if (t < 2) sh.listed[t] = 0;
+          lds_barrier();
 #pragma unroll
-        for (int i = 0; i < KEYS; ++i) key[i] = i * NT + t < n ? sh.group[i * NT + t] : 0;
-        select<NT, KEYS, Key<Z>::BITS>(key, n, k, sh, [&](int i, int o) {
-          sh.id[0][o] = i * NT + t;
-          sh.key[o] = key[i];
-        });
+          for (int i = 0; i < KEYS; ++i)
+            if (i < used) {
+              const int at = place(key(i) >= lo, &sh.listed[0]);
+              if (at < few) sh.near[at] = i * NT + t;
+            }
+          lds_barrier();
+          for (int q0 = 0; q0 < reach << lg; q0 += NT) {
+            const int q = q0 + t;
+            float f[N];
+            int j = a.vocab;
+            if (q < reach << lg) j = ((sh.near[q >> lg] << lg) + (q & ((1 << lg) - 1))) * N;
+            C::unpack(C::load(z, min(j, a.vocab), a.vocab, NEG), f);
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+              const uint32_t v = Key<Z>::of(f[e]);
+              const int at = place(v >= lo, &sh.listed[1]);
+              if (at < 2 * NT) sh.order[at] = pair(v, j + e);
+            }
+          }
+          lds_barrier();
+          const int found = sh.listed[1];
+          if (found <= 2 * NT) {
+            done = true;
+            if (t == 0 && found < 2 * NT) sh.order[found] = 0;   // pairs are read
+            lds_barrier();
+            for (int i = t; i < found; i += NT) {
+              const unsigned long long v = sh.order[i];
+              int rank = 0;
+              for (int o = 0; o < found; o += 2) {
+                const ulonglong2 w = *(const ulonglong2*)(sh.order + o);
+                rank += (w.x > v) + (w.y > v);
+              }
+              if (rank < a.k) output(rank, v);
+            }
+            for (int i = found + t; i < a.k; i += NT) output(i, 0);
+          }
+        }
+        if (!done) {   // many equal ones, or large ones side by side: exactly the k groups
+          lds_barrier();   // the counts may be written
+          select<NT, KEYS, Key<Z>::BITS>(key, n, k, sh, [&](int i, int o) { sh.id[0][o] = i * NT + t; });
+        }
+        turn = 0;
       }
-      while (size > 1) {
+      while (!done && size > 1) {
         const int part = max(1, size / SUB), r = size / part;
         uint32_t sub[SUB];
         int id[SUB];
@@ -341,38 +434,27 @@ __global__ __launch_bounds__(NT, 4) void k_logprobs(LogprobArgs a, int lg) {
         n = k * r - max(0, (last + 1) * r - parts);
         k = min(a.k, n);
         turn ^= 1;
-        select<NT, SUB, Key<Z>::BITS>(sub, n, k, sh, [&](int i, int o) {
+        select<NT, SUB, Key<Z>::BITS>([&](int i) { return sub[i]; }, n, k, sh, [&](int i, int o) {
           sh.id[turn][o] = id[i];
           sh.key[o] = sub[i];
         });
         size = part;
       }
-      // in order: a bitonic sort of as many places as a power of two, by one
-      // wave (whose accesses to LDS keep their order) where it has that many lanes
-      int places = 2;
-      while (places < k) places *= 2;
-      const bool one = places <= 128;
-      if (!one || t < 64) {
-        const int step = one ? 64 : NT;
-        for (int i = t; i < places; i += step)
-          sh.order[i] = i < k ? (unsigned long long)sh.key[i] << 32 | (0xffffffffu - (uint32_t)sh.id[turn][i]) : 0;
-        if (!one) lds_barrier();
-        else asm volatile("" : : : "memory");
+      if (!done) {   // in order: a bitonic sort of as many places as a power of two
+        int places = 2;
+        while (places < k) places *= 2;
+        for (int i = t; i < places; i += NT) sh.order[i] = i < k ? pair(sh.key[i], sh.id[turn][i]) : 0;
+        lds_barrier();
         for (int len = 2; len <= places; len *= 2)
           for (int d = len / 2; d > 0; d /= 2) {
-            for (int q = t; q < places / 2; q += step) {
+            for (int q = t; q < places / 2; q += NT) {
               const int lo = q / d * 2 * d + q % d, hi = lo + d;
               const unsigned long long x = sh.order[lo], y = sh.order[hi];
               if ((x < y) == ((lo & len) == 0)) sh.order[lo] = y, sh.order[hi] = x;
             }
-            if (!one) lds_barrier();
-            else asm volatile("" : : : "memory");
+            lds_barrier();
           }
-        for (int i = t; i < a.k; i += step) {
-          const uint32_t best = i < k ? (uint32_t)(sh.order[i] >> 32) : 0;
-          a.top[row * a.k + i] = best ? logprob(Key<Z>::value(best)) : NEG;
-          a.index[row * a.k + i] = best ? (int64_t)(0xffffffffu - (uint32_t)sh.order[i]) : -1;
-        }
+        for (int i = t; i < a.k; i += NT) output(i, i < k ? sh.order[i] : 0);
       }
       lds_barrier();   // the next row's groups may be written
     }
@@ -383,7 +465,7 @@ __global__ __launch_bounds__(NT, 4) void k_logprobs(LogprobArgs a, int lg) {
 template <typename Z, int NT>
 __global__ __launch_bounds__(NT) void k_logprobs_backward(LogprobArgs a) {
   typedef Chunk<Z> C;
-  constexpr int N = C::N;
+  constexpr int N = C::N, U = 4;
   const float c = LOG2E / a.temp, it = 1.f / a.temp;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const Z* z = (const Z*)a.z + row * a.ldz;
@@ -395,22 +477,32 @@ __global__ __launch_bounds__(NT) void k_logprobs_backward(LogprobArgs a) {
     const bool zero = (gl == 0.f && ge == 0.f) || st.y == 0.f;
     // q (gl + ge (log q + entropy)) = 2^v (slope + rise v) / s
     const float k = -it / st.y, rise = ge * LN2, slope = gl + ge * (st.z - st.w);
-    for (int64_t j = ((int64_t)blockIdx.y * NT + threadIdx.x) * N; j < a.vocab; j += (int64_t)gridDim.y * NT * N) {
-      float f[N] = {};
-      if (!zero) {
-        C::unpack(C::load(z, (int)j, a.vocab, NEG), f);
+    const int64_t all = (int64_t)gridDim.y * NT * N;
+    for (int64_t j0 = ((int64_t)blockIdx.y * NT + threadIdx.x) * N; j0 < a.vocab; j0 += U * all) {
+      uintx4 in[U];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float v = (f[i] - st.x) * c;
-          f[i] = exp2_fast(v) * k * fmaf(rise, factor(v), slope);
-        }
-        if (token >= j && token < j + N) {
+      for (int u = 0; u < U; ++u)
+        if (!zero && j0 + u * all < a.vocab) in[u] = C::load(z, (int)(j0 + u * all), a.vocab, NEG);
 #pragma unroll
-          for (int i = 0; i < N; ++i)
-            if (j + i == token) f[i] += gl * it;
+      for (int u = 0; u < U; ++u) {
+        const int64_t j = j0 + u * all;
+        if (j >= a.vocab) break;
+        float f[N] = {};
+        if (!zero) {
+          C::unpack(in[u], f);
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const float v = (f[i] - st.x) * c;
+            f[i] = exp2_fast(v) * k * fmaf(rise, factor(v), slope);
+          }
+          if (token >= j && token < j + N) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+              if (j + i == token) f[i] += gl * it;
+          }
         }
+        C::store(dz, (int)j, a.vocab, f);
       }
-      C::store(dz, (int)j, a.vocab, f);
     }
   }
 }
@@ -423,14 +515,14 @@ void launch_rows(const LogprobArgs& a, int lg, hipStream_t s) {
 template <typename Z> void launch_forward(const LogprobArgs& a, hipStream_t s) {
   constexpr int N = Chunk<Z>::N;
   if (a.k == 0) {
-    if (a.rows > 512 || a.vocab <= 256 * 8 * N) launch_rows<Z, 256, false>(a, 0, s);
+    if (a.rows > 256 || a.vocab <= 256 * 8 * N) launch_rows<Z, 256, false>(a, 0, s);
     else launch_rows<Z, 1024, false>(a, 0, s);
     return;
   }
   // groups of one, four or eight chunks, as many as the keys that the threads hold
   const auto groups = [&](int64_t nt) { return a.vocab <= nt * KEYS * N ? 0 : a.vocab <= nt * KEYS * N * 4 ? 2 : 3; };
   const bool small = a.k <= 256 && a.vocab <= 256 * KEYS * N * 8;
-  if (small && (a.rows > 512 || a.vocab <= 256 * 8 * N)) launch_rows<Z, 256, true>(a, groups(256), s);
+  if (small && (a.rows > 256 || a.vocab <= 256 * 8 * N)) launch_rows<Z, 256, true>(a, groups(256), s);
   else launch_rows<Z, 1024, true>(a, groups(1024), s);
 }
 
