@@ -90,24 +90,14 @@ template <bool FAR> struct Sums {
   __device__ __forceinline__ bool wide(float c) const { return !(fabsf(m * c) < WIDE); }
 };
 
-// Logits as whole numbers in their order, -inf and NaN as 0 (no alternative), -0 as 0.
-template <typename Z> struct Key {
-  static constexpr int BITS = 8 * sizeof(Z), MANTISSA = sizeof(Z) == 4 ? 23 : sizeof(Z) == 2 && (float)(Z)257.f == 257.f ? 10 : 7;
-  static __device__ __forceinline__ uint32_t of(float z) {
-    union { Z z; uint16_t h; uint32_t w; } c;
-    c.w = 0;
-    c.z = (Z)(z + 0.f);
-    const uint32_t u = sizeof(Z) == 2 ? c.h : c.w, sign = 1u << (BITS - 1), all = sign | (sign - 1);
-    return z > NEG ? (u & sign ? ~u & all : u | sign) : 0u;
-  }
-  static __device__ __forceinline__ float value(uint32_t k) {
-    const uint32_t sign = 1u << (BITS - 1), all = sign | (sign - 1), u = k & sign ? k ^ sign : ~k & all;
-    union { Z z; uint16_t h; uint32_t w; } c;
-    if (sizeof(Z) == 2) c.h = (uint16_t)u;
-    else c.w = u;
-    return (float)c.z;
-  }
-};
+// Logits as whole numbers in their order (-0 as 0).  What is no alternative,
+// -inf, lies below ABSENT; NaN is taken as -inf.
+constexpr uint32_t ABSENT = 0x00800000u;
+__device__ __forceinline__ uint32_t key_of(float z) {
+  const int u = __float_as_int(fmaxf(z, NEG) + 0.f);
+  return (uint32_t)(u ^ (u >> 31 | (int)0x80000000));
+}
+__device__ __forceinline__ float value_of(uint32_t k) { return __uint_as_float(k ^ (k >> 31 ? 0x80000000u : ~0u)); }
 
 constexpr int KEYS = 16, SUB = 8;   // keys a thread holds: of a row's groups, of a level below
 
@@ -117,24 +107,17 @@ template <int NT> struct TopShared {
   union {
     struct {   // of select()
       int entry[KEYS * (NT / 64)];
-      int id[2][NT];                                            // the selected, ascending, of two levels in turn (k <= NT)
-      uint32_t key[NT];
+      int id[2][NT];    // the selected, ascending, of two levels in turn (k <= NT)
     };
     int near[2 * NT];   // groups that may hold one of the largest
   };
   __attribute__((aligned(16))) unsigned long long order[2 * NT];   // key above, the lower index first
-  uint32_t group[KEYS * NT];                                    // the largest of each group, as keys
+  uint32_t group[KEYS * NT];   // the largest of each group (as they are, then as keys of a level)
 };
 
-// How many of the block's n keys are at least `least`, the same in every thread.
-// (key(i): key i of the thread, the first `used` of K.)
-template <int NT, int K, typename Key>
-__device__ __forceinline__ int count_keys(Key key, int used, uint32_t least, TopShared<NT>& sh, int& turn) {
+// The sum of the waves' counts c, the same in every thread.
+template <int NT> __device__ __forceinline__ int block_count(int c, TopShared<NT>& sh, int& turn) {
   constexpr int W = NT / 64;
-  int c = 0;
-#pragma unroll
-  for (int i = 0; i < K; ++i)
-    if (i < used) c += __popcll(__ballot(key(i) >= least));
   if ((threadIdx.x & 63) == 0) sh.count[turn][threadIdx.x >> 6] = c;
   lds_barrier();
   int total = 0;
@@ -147,44 +130,55 @@ __device__ __forceinline__ int count_keys(Key key, int used, uint32_t least, Top
   return total;
 }
 
-// Lanes with `yes` get places in a list in LDS, in no order that matters; the
-// others a place behind any list's end.
-__device__ __forceinline__ int place(bool yes, int* listed) {
-  const unsigned long long all = __ballot(yes);
-  if (!all) return 1 << 30;
+// Places in a list in LDS for `mine` entries of each thread, in no order that
+// matters: the first of the thread's.
+__device__ __forceinline__ int places(int mine, int* listed) {
+  int upto = mine;   // sums over the lanes so far, as in wave_reduce
+  const auto add = [&](int other) { upto += other; };
+  add(__builtin_amdgcn_update_dpp(0, upto, 0x111, 0xf, 0xf, false));
+  add(__builtin_amdgcn_update_dpp(0, upto, 0x112, 0xf, 0xf, false));
+  add(__builtin_amdgcn_update_dpp(0, upto, 0x114, 0xf, 0xf, false));
+  add(__builtin_amdgcn_update_dpp(0, upto, 0x118, 0xf, 0xf, false));
+  add(__builtin_amdgcn_update_dpp(0, upto, 0x142, 0xa, 0xf, false));
+  add(__builtin_amdgcn_update_dpp(0, upto, 0x143, 0xc, 0xf, false));
+  const int all = __builtin_amdgcn_readlane(upto, 63);
+  if (all == 0) return 0;
   int at = 0;
-  if ((threadIdx.x & 63) == 0) at = atomicAdd(listed, (int)__popcll(all));
-  at = __builtin_amdgcn_readfirstlane(at);
-  return yes ? at + (int)__popcll(all & ((1ull << (threadIdx.x & 63)) - 1)) : 1 << 30;
+  if ((threadIdx.x & 63) == 0) at = atomicAdd(listed, all);
+  return __builtin_amdgcn_readfirstlane(at) + upto - mine;
 }
 
-// The k largest of n <= K NT keys (key i of thread t has position i NT + t),
-// equal ones by their position: put(i, o) is called for each with its place o
-// in the order of positions.  The k-th largest key is found bit by bit, by
-// counting the keys that are at least as large.
-template <int NT, int K, int BITS, typename Key, typename Put>
-__device__ __forceinline__ void select(Key key, int n, int k, TopShared<NT>& sh, Put put) {
+// The k largest of the first `used` NT keys in sh.group, equal ones by their
+// position: put(position, o) is called for each with its place o in the order
+// of positions.  The k-th largest key is found bit by bit, by counting the
+// keys that are at least as large.  For rare rows, so with little code and few
+// registers.
+template <int NT, typename Put>
+__device__ __forceinline__ void select(int used, int k, TopShared<NT>& sh, Put put) {
   constexpr int W = NT / 64;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int used = (n + NT - 1) / NT;
+  const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
   uint32_t least = 0;
   int turn = 0;
-  for (int b = BITS - 1; b >= 0; --b) {
+#pragma unroll 1
+  for (int b = 31; b >= 0; --b) {
     const uint32_t cand = least | 1u << b;
-    const int total = count_keys<NT, K>(key, used, cand, sh, turn);
+    int c = 0;
+#pragma unroll 1
+    for (int i = 0; i < used; ++i) c += (int)__popcll(__ballot(sh.group[i * NT + t] >= cand));
+    const int total = block_count<NT>(c, sh, turn);
     if (total >= k) least = cand;
     if (total == k) break;
   }
   // what lies above it, and the first of those equal to it
-#pragma unroll
-  for (int i = 0; i < K; ++i) {
-    const uint32_t v = key(i);
-    const int e = __popcll(__ballot(v > least)) | __popcll(__ballot(v == least)) << 16;
+#pragma unroll 1
+  for (int i = 0; i < KEYS; ++i) {
+    const uint32_t v = i < used ? sh.group[i * NT + t] : 0;
+    const int e = (int)__popcll(__ballot(v > least)) | (int)__popcll(__ballot(i < used && v == least)) << 16;
     if (lane == 0) sh.entry[i * W + wave] = e;
   }
   lds_barrier();
   if (wave == 0) {   // exclusive sums in the order of positions
-    constexpr int E = K * W, PER = (E + 63) / 64;
+    constexpr int E = KEYS * W, PER = (E + 63) / 64;
     int v[PER], sum = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -207,13 +201,13 @@ __device__ __forceinline__ void select(Key key, int n, int k, TopShared<NT>& sh,
   lds_barrier();
   const int need = k - (sh.total & 0xffff);
   const unsigned long long below = (1ull << lane) - 1;
-#pragma unroll
-  for (int i = 0; i < K; ++i) {
-    const uint32_t v = key(i);
+#pragma unroll 1
+  for (int i = 0; i < used; ++i) {
+    const uint32_t v = sh.group[i * NT + t];
     const unsigned long long more = __ballot(v > least), same = __ballot(v == least);
     const int e = sh.entry[i * W + wave];
-    const int gt = (e & 0xffff) + __popcll(more & below), eq = (e >> 16) + __popcll(same & below);
-    if (v > least || (v == least && eq < need)) put(i, gt + min(eq, need));
+    const int gt = (e & 0xffff) + (int)__popcll(more & below), eq = (e >> 16) + (int)__popcll(same & below);
+    if (v > least || (v == least && eq < need)) put(i * NT + t, gt + min(eq, need));
   }
   lds_barrier();
 }
@@ -233,21 +227,32 @@ __device__ __forceinline__ void far_sums(const Z* z, int vocab, float temp, floa
   }
 }
 
-// One row to a block, read once, chunk i NT + t of 16 bytes by thread t, U of
-// them at once and the next U asked for before they are used.  With the
-// alternatives (TOP), the largest of each group of 2^lg neighbouring chunks is
-// kept in LDS, for the k largest logits lie in the k groups with the largest
-// maxima (equal ones by their order): k other groups' maxima come before
-// anything in the rest.  The same again for parts of those groups, which are
-// in the caches, down to single logits.
+// One row to a block, read once, chunk i NT + t of 16 bytes by thread t, AHEAD
+// of them asked for before they are used.  With the alternatives (TOP), the
+// largest of each group of 2^lg neighbouring chunks is kept in LDS: a bound
+// that k or a few more groups reach is reached by k logits at least, and by
+// none outside those groups, which are read again (from the caches) and their
+// logits above it ranked against one another.  Where no such bound is found
+// (many equal logits, or large ones side by side), the k groups with the
+// largest maxima are taken, equal ones by their order: k other groups' maxima
+// come before anything in the rest.  Then the same for parts of those groups,
+// down to single logits.
 template <typename Z, int NT, bool TOP>
 __global__ __launch_bounds__(NT, 4) void k_logprobs(LogprobArgs a, int lg) {
   typedef Chunk<Z> C;
-  constexpr int N = C::N, U = 4, STEP = NT * N;
+  constexpr int N = C::N, AHEAD = 8, STEP = NT * N;
   __shared__ float red[3][NT / 64];
   __shared__ TopShared<TOP ? NT : 64> sh;
   const float c = LOG2E / a.temp;
   const int t = threadIdx.x;
+  const int whole = a.vocab / STEP;   // steps in which every thread has a chunk
+  uintx4 none4;
+  {
+    float f[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = NEG;
+    none4 = C::pack(f);
+  }
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const Z* z = (const Z*)a.z + row * a.ldz;
     int64_t token = -1;
@@ -259,64 +264,57 @@ __global__ __launch_bounds__(NT, 4) void k_logprobs(LogprobArgs a, int lg) {
     }
     Sums<false> S;
     S.clear(a.temp, c);
-    auto absorb = [&](const uintx4 (&v)[U], int step) {
+    auto absorb = [&](const uintx4& v0, const uintx4& v1, int step) {   // two chunks at once
+      float f[2][N], top = S.m, low = __builtin_inff();
+      C::unpack(v0, f[0]);
+      C::unpack(v1, f[1]);
 #pragma unroll
-      for (int h = 0; h < U; h += 2) {   // two chunks: as many values as there are registers for
-        float f[2][N], top = S.m, low = __builtin_inff();
+      for (int u = 0; u < 2; ++u) {
+        float most = NEG;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          C::unpack(v[h + u], f[u]);
-          float most = NEG;
-#pragma unroll
-          for (int i = 0; i < N; i += 2) {
-            most = max3(most, f[u][i], f[u][i + 1]);
-            low = min3(low, f[u][i], f[u][i + 1]);
-          }
-          top = fmaxf(top, most);
-          if (TOP) {
-            if (lg >= 2) {
-              most = fmaxf(most, lane_move<0xb1, 0xf>(most, most));   // lane xor 1
-              most = fmaxf(most, lane_move<0x4e, 0xf>(most, most));   // lane xor 2
-            }
-            if (lg == 3) most = fmaxf(most, lane_move<0x141, 0xf>(most, most));   // the other half of 8
-            if ((t & ((1 << lg) - 1)) == 0) sh.group[((step + h + u) * NT + t) >> lg] = Key<Z>::of(most);
-          }
+        for (int i = 0; i < N; i += 2) {
+          most = max3(most, f[u][i], f[u][i + 1]);
+          low = min3(low, f[u][i], f[u][i + 1]);
         }
-        if (top > S.m) S.to(top, c);
-        if (!(fmaf(low, c, -S.r) > -200.f)) {
-          S.template add<true, N>(f[0], c);
-          S.template add<true, N>(f[1], c);
-        } else {
-          S.template add<false, N>(f[0], c);
-          S.template add<false, N>(f[1], c);
+        top = fmaxf(top, most);
+        if (TOP) {
+          if (lg >= 2) {
+            most = fmaxf(most, lane_move<0xb1, 0xf>(most, most));   // lane xor 1
+            most = fmaxf(most, lane_move<0x4e, 0xf>(most, most));   // lane xor 2
+          }
+          if (lg == 3) most = fmaxf(most, lane_move<0x141, 0xf>(most, most));   // the other half of 8
+          if ((t & ((1 << lg) - 1)) == 0) sh.group[((step + u) * NT + t) >> lg] = __float_as_uint(most);
         }
+      }
+      if (top > S.m) S.to(top, c);
+      if (!(fmaf(low, c, -S.r) > -200.f)) {
+        S.template add<true, N>(f[0], c);
+        S.template add<true, N>(f[1], c);
+      } else {
+        S.template add<false, N>(f[0], c);
+        S.template add<false, N>(f[1], c);
       }
     };
-    const int whole = a.vocab / STEP / U * U;   // steps in batches of whole chunks
-    if (whole > 0) {
-      uintx4 v[U], next[U];
-      const Z* p = z + t * N;
+    const int rest = a.vocab - whole * STEP;   // of the row, a chunk of some threads
+    const uintx4 last = rest ? C::load(z + (int64_t)whole * STEP, min(t * N, rest), rest, NEG) : none4;
+    const Z* p = z + t * N;
+    auto fetch = [&](int i) {
+      return i < whole ? *(const uintx4u*)(p + (int64_t)i * STEP) : i == whole ? (uintx4u)last : (uintx4u)none4;
+    };
+    const int steps = whole + (rest ? 1 : 0);
+    uintx4 v[AHEAD];
 #pragma unroll
-      for (int u = 0; u < U; ++u) v[u] = *(const uintx4u*)(p + (int64_t)u * STEP);
-      for (int i = 0; i < whole; i += U) {
-        if (i + U < whole) {
+    for (int u = 0; u < AHEAD; ++u) v[u] = fetch(u);
+    for (int i = 0; i < steps; i += AHEAD)
 #pragma unroll
-          for (int u = 0; u < U; ++u) next[u] = *(const uintx4u*)(p + (int64_t)(i + U + u) * STEP);
+      for (int u = 0; u < AHEAD; u += 2) {
+        if (i + u >= steps) break;
+        absorb(v[u], v[u + 1], i + u);
+        if (i + u + AHEAD < steps) {
+          v[u] = fetch(i + u + AHEAD);
+          v[u + 1] = fetch(i + u + 1 + AHEAD);
         }
-        absorb(v, i);
-#pragma unroll
-        for (int u = 0; u < U; ++u) v[u] = next[u];
       }
-    }
-    if ((int64_t)whole * STEP < a.vocab) {   // fewer than U steps and a part of one
-      uintx4 v[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t j = (int64_t)(whole + u) * STEP + t * N;
-        v[u] = C::load(z, (int)min(j, (int64_t)a.vocab), a.vocab, NEG);
-      }
-      absorb(v, whole);
-    }
     S.template join<NT>(c, red);
     float m = S.m, s = S.s, w = S.w;
     if (S.wide(c)) {   // rare: again, from the caches
@@ -335,56 +333,74 @@ __global__ __launch_bounds__(NT, 4) void k_logprobs(LogprobArgs a, int lg) {
       if (a.stats) a.stats[row] = make_float4(m, s, entropy, logs);
     }
     if constexpr (TOP) {
-      int size = N << lg, n = (a.vocab + size - 1) / size, k = min(a.k, n), turn = 0;
+      int size = N << lg, n = (a.vocab + size - 1) / size, k = min(a.k, n);
       auto output = [&](int i, unsigned long long v) {   // place i
         const uint32_t best = (uint32_t)(v >> 32);
-        a.top[row * a.k + i] = best ? logprob(Key<Z>::value(best)) : NEG;
-        a.index[row * a.k + i] = best ? (int64_t)(0xffffffffu - (uint32_t)v) : -1;
+        a.top[row * a.k + i] = best >= ABSENT ? logprob(value_of(best)) : NEG;
+        a.index[row * a.k + i] = best >= ABSENT ? (int64_t)(0xffffffffu - (uint32_t)v) : -1;
       };
       auto pair = [&](uint32_t key, int id) { return (unsigned long long)key << 32 | (0xffffffffu - (uint32_t)id); };
       bool done = false;
       {
-        const auto key = [&](int i) { return i * NT + t < n ? sh.group[i * NT + t] : 0u; };   // (written before the joins' barriers)
-        // A bound that few groups reach, k or more of them where there are as
-        // many: down from the largest in growing steps, then between the last two.
-        const int used = (n + NT - 1) / NT, few = min(2 * NT, 2 * a.k + 64);
-        const uint32_t top = Key<Z>::of(m);
-        uint32_t lo = top + 1, hi = top + 1, step = 1u << (Key<Z>::MANTISSA - 1);
+        float held[KEYS];   // (written before the joins' barriers)
+#pragma unroll
+        for (int i = 0; i < KEYS; ++i) {
+          const float v = __uint_as_float(sh.group[i * NT + t]);
+          held[i] = i * NT + t < n ? v : NEG;
+        }
+        int turn = 0;
+        auto reached = [&](uint32_t key) {
+          const float bound = value_of(key);
+          int c = 0;
+#pragma unroll
+          for (int i = 0; i < KEYS; ++i) c += (int)__popcll(__ballot(held[i] >= bound));
+          return block_count<NT>(c, sh, turn);
+        };
+        // The bound: down from the largest in growing steps (half an exponent's
+        // first), then between the last two.
+        const int few = min(2 * NT, 2 * a.k + 64);
+        const uint32_t top = max(key_of(m), ABSENT);
+        uint32_t lo = top + 1, hi = top + 1, step = 1u << 22;
         int reach = 0;
-        while (reach < a.k && lo > 1) {
+        while (reach < a.k && lo > ABSENT) {
           hi = lo;
-          lo = top > step ? top - step + 1 : 1;
+          lo = top - ABSENT > step ? top - step : ABSENT;
           step = step >> 31 ? ~0u : 2 * step;
-          reach = count_keys<NT, KEYS>(key, used, lo, sh, turn);
+          reach = reached(lo);
         }
         while (reach > few && hi - lo > 1) {
           const uint32_t mid = lo + (hi - lo) / 2;
-          const int c = count_keys<NT, KEYS>(key, used, mid, sh, turn);
+          const int c = reached(mid);
           if (c >= a.k) lo = mid, reach = c;
           else hi = mid;
         }
         if (reach <= few) {
-          // everything that reaches it lies in them; each is ranked against all others
+          const float bound = value_of(lo);
           if (t < 2) sh.listed[t] = 0;
           lds_barrier();
+          uint32_t hits = 0;
 #pragma unroll
-          for (int i = 0; i < KEYS; ++i)
-            if (i < used) {
-              const int at = place(key(i) >= lo, &sh.listed[0]);
-              if (at < few) sh.near[at] = i * NT + t;
-            }
+          for (int i = 0; i < KEYS; ++i) hits |= held[i] >= bound ? 1u << i : 0;
+          int at = places(__popc(hits), &sh.listed[0]);
+          for (; hits; hits &= hits - 1) sh.near[at++] = (__ffs(hits) - 1) * NT + t;
           lds_barrier();
           for (int q0 = 0; q0 < reach << lg; q0 += NT) {
             const int q = q0 + t;
             float f[N];
             int j = a.vocab;
             if (q < reach << lg) j = ((sh.near[q >> lg] << lg) + (q & ((1 << lg) - 1))) * N;
-            C::unpack(C::load(z, min(j, a.vocab), a.vocab, NEG), f);
+            const uintx4 v = C::load(z, min(j, a.vocab), a.vocab, NEG);
+            C::unpack(v, f);
 #pragma unroll
-            for (int e = 0; e < N; ++e) {
-              const uint32_t v = Key<Z>::of(f[e]);
-              const int at = place(v >= lo, &sh.listed[1]);
-              if (at < 2 * NT) sh.order[at] = pair(v, j + e);
+            for (int e = 0; e < N; ++e) hits |= f[e] >= bound ? 1u << e : 0;
+            at = places(__popc(hits), &sh.listed[1]);
+            for (; hits; hits &= hits - 1) {
+              const int e = __ffs(hits) - 1;
+              float x = f[0];
+#pragma unroll
+              for (int o = 1; o < N; ++o) x = e == o ? f[o] : x;
+              if (at < 2 * NT) sh.order[at] = pair(key_of(x), j + e);
+              ++at;
             }
           }
           lds_barrier();
@@ -396,6 +412,7 @@ __global__ __launch_bounds__(NT, 4) void k_logprobs(LogprobArgs a, int lg) {
             for (int i = t; i < found; i += NT) {
               const unsigned long long v = sh.order[i];
               int rank = 0;
+#pragma unroll 4
               for (int o = 0; o < found; o += 2) {
                 const ulonglong2 w = *(const ulonglong2*)(sh.order + o);
                 rank += (w.x > v) + (w.y > v);
@@ -405,47 +422,52 @@ __global__ __launch_bounds__(NT, 4) void k_logprobs(LogprobArgs a, int lg) {
             for (int i = found + t; i < a.k; i += NT) output(i, 0);
           }
         }
-        if (!done) {   // many equal ones, or large ones side by side: exactly the k groups
-          lds_barrier();   // the counts may be written
-          select<NT, KEYS, Key<Z>::BITS>(key, n, k, sh, [&](int i, int o) { sh.id[0][o] = i * NT + t; });
-        }
-        turn = 0;
       }
-      while (!done && size > 1) {
-        const int part = max(1, size / SUB), r = size / part;
-        uint32_t sub[SUB];
-        int id[SUB];
-#pragma unroll
-        for (int i = 0; i < SUB; ++i) {
-          const int q = i * NT + t;
-          sub[i] = 0;
-          id[i] = 0;
-          if (q < k * r) {
-            id[i] = sh.id[turn][q / r] * r + q % r;
-            const int j = id[i] * part;
+      if (!done) {
+        int turn = 0;
+        const int used = (n + NT - 1) / NT;
+        lds_barrier();   // counts and lists may be written
+#pragma unroll 1
+        for (int i = 0; i < used; ++i) {
+          const int g = i * NT + t;
+          sh.group[g] = g < n ? key_of(__uint_as_float(sh.group[g])) : 0;
+        }
+        select<NT>(used, k, sh, [&](int g, int o) { sh.id[0][o] = g; });
+#pragma unroll 1
+        while (size > 1) {
+          const int part = max(1, size / SUB), r = size / part;
+          // the parts that lie in the row at all: only its last group may hold others, behind them
+          const int parts = (a.vocab + part - 1) / part, last_id = sh.id[turn][k - 1], all = k * r;
+          n = all - max(0, (last_id + 1) * r - parts);
+          const int held = (all + NT - 1) / NT, from = turn;
+#pragma unroll 1
+          for (int i = 0; i < held; ++i) {
+            const int q = i * NT + t;
             float top = NEG;
-            for (int e = 0; e < part; ++e)
-              if (j + e < a.vocab) top = fmaxf(top, to_f(z[j + e]));
-            sub[i] = Key<Z>::of(top);
+            if (q < all) {
+              const int j = (sh.id[from][q / r] * r + q % r) * part;
+              for (int e = 0; e < part; ++e)
+                if (j + e < a.vocab) top = fmaxf(top, to_f(z[j + e]));
+            }
+            sh.group[q] = q < all ? key_of(top) : 0;
           }
+          k = min(a.k, n);
+          turn ^= 1;
+          select<NT>(held, k, sh, [&](int q, int o) {
+            sh.id[turn][o] = sh.id[from][q / r] * r + q % r;
+            if (part == 1) sh.order[o] = pair(sh.group[q], sh.id[turn][o]);
+          });
+          size = part;
         }
-        // the parts that lie in the row at all: only its last group may hold others, behind them
-        const int parts = (a.vocab + part - 1) / part, last = sh.id[turn][k - 1];
-        n = k * r - max(0, (last + 1) * r - parts);
-        k = min(a.k, n);
-        turn ^= 1;
-        select<NT, SUB, Key<Z>::BITS>([&](int i) { return sub[i]; }, n, k, sh, [&](int i, int o) {
-          sh.id[turn][o] = id[i];
-          sh.key[o] = sub[i];
-        });
-        size = part;
-      }
-      if (!done) {   // in order: a bitonic sort of as many places as a power of two
+        // in order: a bitonic sort of as many places as a power of two
         int places = 2;
         while (places < k) places *= 2;
-        for (int i = t; i < places; i += NT) sh.order[i] = i < k ? pair(sh.key[i], sh.id[turn][i]) : 0;
+        for (int i = t; i < places; i += NT)
+          if (i >= k) sh.order[i] = 0;
         lds_barrier();
+#pragma unroll 1
         for (int len = 2; len <= places; len *= 2)
+#pragma unroll 1
           for (int d = len / 2; d > 0; d /= 2) {
             for (int q = t; q < places / 2; q += NT) {
               const int lo = q / d * 2 * d + q % d, hi = lo + d;
