@@ -183,10 +183,12 @@ __device__ __forceinline__ float biased(const MxArgs& g, int64_t col, float v) {
 // One BM x BN tile of the output by WM x WN waves, as the 8-bit product's: S
 // stages of BK bytes of codes (256 k) in LDS, copied straight there S - 1
 // stages ahead, fragments of the next 32 bytes read while the present ones are
-// multiplied.  The scales come along in chunks of 16 bytes, those of two
-// stages for one row, into places of their own; a lane's four of a stage
-// (blocks l / 32, 2 + l / 32, ..) are picked into one register.  Codes and
-// scales lie in rows at multiples of 16 bytes, whole chunks of them.
+// multiplied.  The scales come along 32 bytes of a row at once, those of G =
+// 4 stages, into two places of their own in turn, and a stage ahead of the
+// codes, so that a stage's are read from LDS in the middle of the one before; a
+// lane's four (blocks l / 32, 2 + l / 32, ..) are picked into one register.
+// (8192 x 14336 x 4096: 297 us with 16 bytes at once, read at the turn.)  Codes
+// and scales lie in rows at multiples of 16 bytes, whole chunks of them.
 template <int BM, int BN, int WM, int WN, int S, typename O>
 __global__ __launch_bounds__(64 * WM * WN) void k_mxfp4_mma(MxArgs g, float* partial) {
   constexpr int W = WM * WN, NT = 64 * W;
@@ -194,15 +196,15 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mxfp4_mma(MxArgs g, float* par
   constexpr int STAGE = (BM + BN) * BK;
   constexpr int NP = STAGE / 1024 / W;            // 1 KB pieces of a stage per wave
   constexpr int PR = 1024 / BK, CR = BK / 16;     // rows of a piece, chunks of a row
-  constexpr int SCALES = (BM + BN) * 16, SP = SCALES / 1024, PAIRS = S <= 3 ? 2 : 4;   // pairs of stages in LDS
+  constexpr int G = 4, SCALES = (BM + BN) * 8 * G, SP = SCALES / 1024 / W;   // pieces of a group's scales per wave
   constexpr int OV = OutVec<O>::N, SROW = TN + OV;   // staged output row
   constexpr int STAGED = W * 32 * SROW * (int)sizeof(O);
-  constexpr int HELD = S * STAGE + PAIRS * SCALES, LDS = HELD > STAGED ? HELD : STAGED;
+  constexpr int HELD = S * STAGE + 2 * SCALES, LDS = HELD > STAGED ? HELD : STAGED;
   constexpr int KS = BK / 32;
   constexpr bool SPREAD = BM * BN >= 256 * 256;
   constexpr int PW = NP / 2, EVERY = SPREAD ? FM * FN / PW : 1;
   static_assert(!SPREAD || (PW * 2 == NP && EVERY * PW == FM * FN), "the copies divide the products");
-  static_assert(S <= 4 && NP * W * 1024 == STAGE && BM % PR == 0 && BM % 64 == 0 && SP <= W, "whole pieces");
+  static_assert(S <= 4 && NP * W * 1024 == STAGE && BM % PR == 0 && SP * W * 1024 == SCALES && S <= G, "whole pieces");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[LDS];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
@@ -227,10 +229,8 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mxfp4_mma(MxArgs g, float* par
   const intx4 rsb = raw_buffer(g.sb + n0 * g.ldsb, (uint32_t)((rn - 1) * g.ldsb + sb16));
   const int prow = wave * PR + lane / CR, vk = swz(prow, lane % CR) * 16;
   const uint32_t va = (uint32_t)(prow * (int)g.lda + vk), vb = (uint32_t)(prow * (int)g.ldb + vk);
-  // piece `wave` of a pair's scales: rows 64 wave .. of a, then of b, one to a lane
-  const bool sisa = wave < BM / 64;
-  const int sr = (sisa ? wave : wave - BM / 64) * 64 + lane;
-  const uint32_t soff = sr < (sisa ? rm : rn) ? (uint32_t)(sr * (sisa ? g.ldsa : g.ldsb)) : OUT_OF_RANGE;
+  // piece q = wave + i W of a group's scales: rows 32 q .. of a, then of b, two lanes to a row
+  const int schunk = (lane & 1) * 16;
   auto issue = [&](int kt, int i) {   // piece i of stage kt
     constexpr int A = BM / PR / W;   // pieces of a
     const int k0 = (kt0 + kt) * BK, q = wave + i * W;
@@ -238,16 +238,23 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mxfp4_mma(MxArgs g, float* par
     dma16(k0 + vk < g.kb ? v : OUT_OF_RANGE, i < A ? ra : rb, (uint32_t)k0,
           (uint32_t)__builtin_amdgcn_readfirstlane(lds0 + (kt % S) * STAGE + q * 1024));
   };
-  auto issue_scales = [&](int kt) {   // with the first of a pair's stages
-    const int pair = (kt0 + kt) / 2;
-    if (((kt0 + kt) & 1 && kt > 0) || wave >= SP) return;
-    dma16(soff, sisa ? rsa : rsb, (uint32_t)(pair * 16),
-          (uint32_t)__builtin_amdgcn_readfirstlane(lds0 + S * STAGE + pair % PAIRS * SCALES + wave * 1024));
+  auto issue_scales = [&](int kt) {   // with the first of a group's stages
+    const uint32_t group = (uint32_t)(kt0 + kt) / G;
+    if ((uint32_t)(kt0 + kt) % G != 0 && kt > 0) return;
+#pragma unroll
+    for (int i = 0; i < SP; ++i) {
+      const int q = wave + i * W, row = q * 32 + lane / 2;
+      const bool isa = q < BM / 32;
+      const uint32_t v = (uint32_t)(isa ? row * (int)g.ldsa : (row - BM) * (int)g.ldsb) + schunk;
+      dma16((int)(group * 8 * G) + schunk < sb16 ? v : OUT_OF_RANGE, isa ? rsa : rsb, group * 8 * G,
+            (uint32_t)__builtin_amdgcn_readfirstlane(lds0 + S * STAGE + group % 2 * SCALES + q * 1024));
+    }
   };
 
   floatx16 acc[FM][FN] = {};
   intx4 fa[2][FM], fb[2][FN];
-  int sa[FM], sb[FN], na[FM], nb_[FN];   // the scales of this stage and of the next
+  int sa[FM], sb[FN];       // the scales of this stage
+  uint2 na[FM], nb[FN];     // of the next, all eight of a row
   const int r = lane & 31;
   const uint32_t pick = lane < 32 ? 0x06040200u : 0x07050301u;
   auto fetch = [&](int kt, int ks, int set) {
@@ -258,23 +265,18 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mxfp4_mma(MxArgs g, float* par
     for (int f = 0; f < FN; ++f) fb[set][f] = *(const intx4*)(s + (BM + wn * TN + f * 32 + r) * BK);
   };
   auto fetch_scales = [&](int kt) {
-    const uint8_t* s = smem + S * STAGE + (kt0 + kt) / 2 % PAIRS * SCALES + ((kt0 + kt) & 1) * 8;
+    const uint32_t at = (uint32_t)(kt0 + kt);
+    const uint8_t* s = smem + S * STAGE + at / G % 2 * SCALES + at % G * 8;
 #pragma unroll
-    for (int f = 0; f < FM; ++f) {
-      const uint2 v = *(const uint2*)(s + (wm * TM + f * 32 + r) * 16);
-      na[f] = (int)__builtin_amdgcn_perm(v.y, v.x, pick);
-    }
+    for (int f = 0; f < FM; ++f) na[f] = *(const uint2*)(s + (wm * TM + f * 32 + r) * 8 * G);
 #pragma unroll
-    for (int f = 0; f < FN; ++f) {
-      const uint2 v = *(const uint2*)(s + (BM + wn * TN + f * 32 + r) * 16);
-      nb_[f] = (int)__builtin_amdgcn_perm(v.y, v.x, pick);
-    }
+    for (int f = 0; f < FN; ++f) nb[f] = *(const uint2*)(s + (BM + wn * TN + f * 32 + r) * 8 * G);
   };
   auto take_scales = [&]() {
 #pragma unroll
-    for (int f = 0; f < FM; ++f) sa[f] = na[f];
+    for (int f = 0; f < FM; ++f) sa[f] = (int)__builtin_amdgcn_perm(na[f].y, na[f].x, pick);
 #pragma unroll
-    for (int f = 0; f < FN; ++f) sb[f] = nb_[f];
+    for (int f = 0; f < FN; ++f) sb[f] = (int)__builtin_amdgcn_perm(nb[f].y, nb[f].x, pick);
   };
   // the stage that is needed next has landed, and every wave is done with the one before it
   auto turn = [&](int kt) {
@@ -283,19 +285,19 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mxfp4_mma(MxArgs g, float* par
     else if (S >= 3 && later >= 1) wait_vmcnt<NP>();
     else wait_vmcnt<0>();
     lds_barrier();
-    if (kt + S - 1 < nk) {
-      issue_scales(kt + S - 1);
-      if (!SPREAD) {
+    if (kt + S < nk) issue_scales(kt + S);
+    if (!SPREAD && kt + S - 1 < nk) {
 #pragma unroll
-        for (int i = 0; i < NP; ++i) issue(kt + S - 1, i);
-      }
+      for (int i = 0; i < NP; ++i) issue(kt + S - 1, i);
     }
   };
   if (nk > 0) {
 #pragma unroll
+    for (int t = 0; t < S; ++t)
+      if (t < nk) issue_scales(t);
+#pragma unroll
     for (int t = 0; t < S - 1; ++t)
       if (t < nk) {
-        issue_scales(t);
 #pragma unroll
         for (int i = 0; i < NP; ++i) issue(t, i);
       }
@@ -312,10 +314,10 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mxfp4_mma(MxArgs g, float* par
       for (int ks = 0; ks < KS; ++ks) {
         if (ks + 1 < KS) {
           fetch(kt, ks + 1, (ks + 1) & 1);
+          if (ks == 1 && kt + 1 < nk) fetch_scales(kt + 1);
         } else if (kt + 1 < nk) {
           turn(kt + 1);
           fetch(kt + 1, 0, 0);
-          fetch_scales(kt + 1);
         }
         __builtin_amdgcn_sched_barrier(0);   // the reads above go out before the products, not beside their use
         // spread copies, one after every EVERY products: half of a stage's
@@ -326,7 +328,9 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mxfp4_mma(MxArgs g, float* par
 #pragma unroll
           for (int j = 0; j < FN; ++j) {
             acc[i][j] = mma32(fb[ks & 1][j], fa[ks & 1][i], acc[i][j], sb[j], sa[i], ks);
-            asm volatile("" : "+v"(acc[i][j]));   // here: the compiler would move products behind later branches
+            // here: the compiler would move products behind later branches
+            if constexpr (SPREAD) asm volatile("" : "+v"(acc[i][j]));
+            else asm volatile("" : "+a"(acc[i][j]));
             const int t = i * FN + j;
             if (SPREAD && w < 2 && t % EVERY == EVERY - 1) {
               __builtin_amdgcn_sched_barrier(0);
