@@ -431,19 +431,17 @@ void launch_mma(const MxArgs& a, int splits, hipStream_t s) {
   if (part) launch_join(a, splits, s);
 }
 
-// Up to 16 tokens, as the 8-bit product's: the block takes 16 NW channels; its
-// waves take 16 of them and every KW-th 128-byte piece of the split's share of
-// k each, and the sums of the KW meet in LDS.  Codes and scales go from global
-// memory to registers, at any alignment.  Rows past the end repeat the last
-// one and are not written.
-template <int NW, int KW, typename O>
-__global__ __launch_bounds__(64 * NW * KW) void k_mxfp4_rows(MxArgs g, float* partial) {
-  __shared__ __attribute__((aligned(16))) float sum[KW * NW * 256];
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int nw = wave % NW, kw = wave / NW;
-  const int64_t n0 = (int64_t)blockIdx.x * (16 * NW);
+// Up to 16 tokens: the block takes 16 channels; each of its KW waves every
+// KW-th 128-byte piece of the split's share of k, and the sums of the KW meet
+// in LDS.  Codes and scales go from global memory to registers, at any
+// alignment.  Rows past the end repeat the last one and are not written.
+constexpr int KW = 16;
+template <typename O> __global__ __launch_bounds__(64 * KW) void k_mxfp4_rows(MxArgs g, float* partial) {
+  __shared__ __attribute__((aligned(16))) float sum[KW * 256];
+  const int tid = threadIdx.x, lane = tid & 63, kw = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
   const int r = lane & 15, kc = lane >> 4;   // row, block of 32 in its 128
-  const int64_t rb = min(n0 + nw * 16 + r, g.n - 1), ra = min((int64_t)r, g.m - 1);
+  const int64_t rb = min(n0 + r, g.n - 1), ra = min((int64_t)r, g.m - 1);
   const uint8_t *b = g.b + rb * g.ldb, *a = g.a + ra * g.lda, *sb = g.sb + rb * g.ldsb, *sa = g.sa + ra * g.ldsa;
   floatx4 acc = {0.f, 0.f, 0.f, 0.f};
   const int pieces = (g.kb + 127) / 128, nb = (g.kb + 15) / 16;
@@ -467,14 +465,13 @@ __global__ __launch_bounds__(64 * NW * KW) void k_mxfp4_rows(MxArgs g, float* pa
       acc = mma16(load_chunk((const int8_t*)b, k, kend), load_chunk((const int8_t*)a, k, kend), acc, xb, xa);
     }
   }
-  // [kw][token][channel of the block]
-  *(floatx4*)(sum + (kw * 16 + r) * (16 * NW) + nw * 16 + kc * 4) = acc;
+  *(floatx4*)(sum + (kw * 16 + r) * 16 + kc * 4) = acc;   // [kw][token][channel of the block]
   __syncthreads();
-  for (int i = tid; i < NW * 256; i += 64 * NW * KW) {
+  if (tid < 256) {
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < KW; ++w) v += sum[w * NW * 256 + i];
-    const int64_t row = i / (16 * NW), col = n0 + i % (16 * NW);
+    for (int w = 0; w < KW; ++w) v += sum[w * 256 + tid];
+    const int64_t row = tid / 16, col = n0 + tid % 16;
     if (row < g.m && col < g.n) {
       if (partial) partial[((int64_t)blockIdx.y * g.m + row) * g.n + col] = v;
       else ((O*)g.out)[row * g.ldo + col] = from_f<O>(biased(g, col, v));
@@ -482,13 +479,12 @@ __global__ __launch_bounds__(64 * NW * KW) void k_mxfp4_rows(MxArgs g, float* pa
   }
 }
 
-template <int NW, int KW>
 void launch_rows(const MxArgs& a, int splits, hipStream_t s) {
-  const dim3 grid((unsigned)((a.n + 16 * NW - 1) / (16 * NW)), splits), block(64 * NW * KW);
+  const dim3 grid((unsigned)((a.n + 15) / 16), splits), block(64 * KW);
   float* part = splits > 1 ? a.partial : nullptr;
-  if (a.out_fmt == 1) hipLaunchKernelGGL((k_mxfp4_rows<NW, KW, float>), grid, block, 0, s, a, part);
-  else if (a.out_fmt == 0) hipLaunchKernelGGL((k_mxfp4_rows<NW, KW, bf16_t>), grid, block, 0, s, a, part);
-  else hipLaunchKernelGGL((k_mxfp4_rows<NW, KW, fp16_t>), grid, block, 0, s, a, part);
+  if (a.out_fmt == 1) hipLaunchKernelGGL((k_mxfp4_rows<float>), grid, block, 0, s, a, part);
+  else if (a.out_fmt == 0) hipLaunchKernelGGL((k_mxfp4_rows<bf16_t>), grid, block, 0, s, a, part);
+  else hipLaunchKernelGGL((k_mxfp4_rows<fp16_t>), grid, block, 0, s, a, part);
   if (part) launch_join(a, splits, s);
 }
 
@@ -518,29 +514,48 @@ __global__ __launch_bounds__(256) void k_mxfp4_align(AlignJobs jobs) {
   }
 }
 
-// Which kernel takes a product, by its sizes alone: as the 8-bit product's,
-// whose stages have as many bytes.
+// Which kernel takes a product, by its sizes, and whether its operands lie as
+// the tiles need them (us on an MI355X, bf16 output).
+//  - Up to 16 tokens the rows kernel, which reads the weights once at any
+//    alignment (1 x 4096 x 4096: 5.0, 64 x 64 tiles 9.0; 16 x 4096 x 14336:
+//    10.8 against 13.8 with k in four splits), with k split over blocks where
+//    there are few channels (1 x 512 x 14336: 7.4 against 7.9).  Where the tiles
+//    of 64 channels fill the CUs and nothing has to be copied for them, they:
+//    their copies straight into LDS keep more of memory busy, and each of 16
+//    tokens costs the rows kernel reads of its own (1 x 14336 x 4096: 9.7
+//    against 10.6; 16 tokens: 9.7 against 13.5).
+//  - Otherwise the tile and the split of k with the least of the sum of the
+//    rounds over the 256 CUs at a stage's time (256 k), a tile's fixed time, and
+//    the time of writing and joining the splits' sums.  A stage takes 2.0 for
+//    256 x 256, one block per CU, and 1.3 while half of the CUs have none (1024 x
+//    14336 x 4096: 39, 128 x 128: 51); 1.3 for 128 x 128 two to a CU, 0.8 and
+//    0.58 alone (2048 x 4096 x 4096: 27; 512 x 14336 x 4096: 26, 256 x 256: 33);
+//    0.6, 0.36 and 0.31 for 64 x 64 (512 x 4096 x 4096: 13; 256 x 14336 x 4096:
+//    23.5, 128 x 128: 20.7).  24 x 4096 x 14336 on 64 x 64: 12.6 in four splits, 21
+//    in one.
 struct MxPlan {
-  enum { ROWS1, ROWS4, TILE64, TILE128, TILE256 } kind;
+  enum { ROWS, TILE64, TILE128, TILE256 } kind;
   int splits;
 };
 
-MxPlan mx_plan(int64_t m, int64_t n, int kb) {
+MxPlan mx_plan(int64_t m, int64_t n, int kb, bool aligned) {
   const int stages = (kb + 127) / 128;
   if (m <= 16) {
-    if (n >= 64 * 208) return {MxPlan::ROWS4, 1};
+    if (aligned && n >= 64 * 208) return {MxPlan::TILE64, 1};
     const int64_t blocks = (n + 15) / 16;
-    return {MxPlan::ROWS1, (int)std::max<int64_t>(1, std::min<int64_t>(256 / blocks, stages / 28))};
+    return {MxPlan::ROWS, (int)std::max<int64_t>(1, std::min<int64_t>(256 / blocks, stages / 28))};
   }
   const auto tiles = [&](int64_t t) { return (m + t - 1) / t * ((n + t - 1) / t); };
   MxPlan best{MxPlan::TILE64, 1};
   double least = 1e30;
-  const auto consider = [&](decltype(MxPlan::TILE64) kind, int64_t t, double alone, double two, double fixed) {
+  const auto consider = [&](decltype(MxPlan::TILE64) kind, int64_t t, double half, double alone, double two, double fixed) {
     for (int s = 1; s <= 16; ++s) {
       if (s > 1 && stages / s < 4) break;
       const int64_t blocks = tiles(t) * s;
-      const double round = two > 0 ? (blocks <= 256 ? alone : two * (double)((blocks + 511) / 512))
-                                   : alone * (double)((blocks + 255) / 256);
+      const double round = blocks <= 128          ? half
+                           : blocks <= 256        ? alone
+                           : two > 0              ? two * (double)((blocks + 511) / 512)
+                                                  : alone * (double)((blocks + 255) / 256);
       const double us = round * ((stages + s - 1) / s) + fixed + (s > 1 ? 3.0 + 8e-6 * s * (double)m * (double)n / 4.0 : 0.0);
       if (us < least) {
         least = us;
@@ -548,9 +563,9 @@ MxPlan mx_plan(int64_t m, int64_t n, int kb) {
       }
     }
   };
-  consider(MxPlan::TILE256, 256, 1.31, 0, 9);
-  consider(MxPlan::TILE128, 128, 0.70, 1.28, 5);
-  consider(MxPlan::TILE64, 64, 0.30, 0.55, 3);
+  consider(MxPlan::TILE256, 256, 1.3, 2.0, 0, 7);
+  consider(MxPlan::TILE128, 128, 0.58, 0.82, 1.3, 6.7);
+  consider(MxPlan::TILE64, 64, 0.31, 0.36, 0.6, 4);
   return best;
 }
 
@@ -565,17 +580,17 @@ struct MxLayout {
 
 MxLayout mx_layout(const MxArgs& g) {
   const int nb = (g.kb + 15) / 16;
-  MxLayout l{mx_plan(g.m, g.n, g.kb), 0, {}, {nb * 16, (nb + 15) / 16 * 16}};
-  const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  if (l.plan.splits > 1) l.partial = up((size_t)l.plan.splits * g.m * g.n * 4);
-  if (l.plan.kind == MxPlan::ROWS1 || l.plan.kind == MxPlan::ROWS4 || g.kb == 0) return l;
   const auto bad = [&](const uint8_t* p, int64_t ld, int bytes) {
     return ((uintptr_t)p | (uint64_t)ld | (uint64_t)bytes) % 16 != 0 || ld >= (1 << 22);
   };
-  if (bad(g.a, g.lda, g.kb)) l.copy[0] = up((size_t)g.m * l.pitch[0]);
-  if (bad(g.sa, g.ldsa, nb)) l.copy[1] = up((size_t)g.m * l.pitch[1]);
-  if (bad(g.b, g.ldb, g.kb)) l.copy[2] = up((size_t)g.n * l.pitch[0]);
-  if (bad(g.sb, g.ldsb, nb)) l.copy[3] = up((size_t)g.n * l.pitch[1]);
+  const bool copies[4] = {bad(g.a, g.lda, g.kb), bad(g.sa, g.ldsa, nb), bad(g.b, g.ldb, g.kb), bad(g.sb, g.ldsb, nb)};
+  const bool aligned = !(copies[0] || copies[1] || copies[2] || copies[3]);
+  MxLayout l{mx_plan(g.m, g.n, g.kb, aligned), 0, {}, {nb * 16, (nb + 15) / 16 * 16}};
+  const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  if (l.plan.splits > 1) l.partial = up((size_t)l.plan.splits * g.m * g.n * 4);
+  if (l.plan.kind == MxPlan::ROWS || g.kb == 0) return l;
+  for (int q = 0; q < 4; ++q)
+    if (copies[q]) l.copy[q] = up((size_t)(q < 2 ? g.m : g.n) * l.pitch[q % 2]);
   return l;
 }
 
@@ -609,8 +624,7 @@ void launch_mxfp4_linear(MxArgs g, hipStream_t s) {
     if (l.copy[0] || l.copy[2]) g.kb = l.pitch[0];   // the zeros of at least one of the two factors fill the rest
   }
   switch (l.plan.kind) {
-    case MxPlan::ROWS1: return launch_rows<1, 16>(g, l.plan.splits, s);
-    case MxPlan::ROWS4: return launch_rows<4, 4>(g, l.plan.splits, s);
+    case MxPlan::ROWS: return launch_rows(g, l.plan.splits, s);
     case MxPlan::TILE64: return launch_mma<64, 64, 2, 2, 4>(g, l.plan.splits, s);
     case MxPlan::TILE128: return launch_mma<128, 128, 2, 2, 2>(g, l.plan.splits, s);
     case MxPlan::TILE256: return launch_mma<256, 256, 2, 4, 2>(g, l.plan.splits, s);
