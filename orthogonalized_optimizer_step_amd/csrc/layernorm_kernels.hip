@@ -53,7 +53,7 @@ template <int N> __device__ __forceinline__ void centre(float* s, float mean, in
 }
 
 template <typename T, int NT, int CH>
-__global__ __launch_bounds__(block_of(NT)) void k_layernorm(LayerNormArgs a, bool w32) {
+__global__ __launch_bounds__(block_of(NT), NT >= 256 && CH == 1 ? 8 : 4) void k_layernorm(LayerNormArgs a, bool w32) {
   typedef Chunk<T> C;
   constexpr int N = C::N, RPB = block_of(NT) / NT;
   __shared__ __attribute__((aligned(8))) float red[2][32];
@@ -170,7 +170,7 @@ __global__ __launch_bounds__(1024) void k_layernorm_long(LayerNormArgs a, bool w
 // for each block, in the order of its rows, joined over blocks by
 // k_layernorm_join.
 template <typename T, int NT, int CH>
-__global__ __launch_bounds__(block_of(NT)) void k_layernorm_backward(LayerNormBackArgs a, bool w32) {
+__global__ __launch_bounds__(block_of(NT), NT == 64 && CH == 2 ? 1 : 4) void k_layernorm_backward(LayerNormBackArgs a, bool w32) {
   typedef Chunk<T> C;
   constexpr int N = C::N, RPB = block_of(NT) / NT;
   __shared__ __attribute__((aligned(8))) float red[2][32];
@@ -373,8 +373,11 @@ void launch_forward(const LayerNormArgs& a, bool w32, hipStream_t s) {
 
 constexpr int kHeldChunks = 2048;   // longest row that is held, in 16-byte chunks
 
-// Threads and chunks of a row, as for the RMS norm: many threads with little
-// each hide memory best.
+// Threads and chunks of a row: many threads with little each hide memory best,
+// and 64 registers (eight waves a SIMD) where a row is more than a wave's.  2^25
+// elements of bf16 with a residual (us): rows of 4096 46 to 49 on 512 threads; of
+// 8192 52 on 1024 threads and 64 registers, 61 with 62 to 71, 69 on 512 with two chunks;
+// of 16384 63 on 1024 with two.
 template <typename T> void launch_norm(const LayerNormArgs& a, bool w32, hipStream_t s) {
   const int chunks = (a.cols + Chunk<T>::N - 1) / Chunk<T>::N;
   if (chunks <= 16) launch_forward<T, 16, 1>(a, w32, s);
@@ -383,7 +386,7 @@ template <typename T> void launch_norm(const LayerNormArgs& a, bool w32, hipStre
   else if (chunks <= 128) launch_forward<T, 64, 2>(a, w32, s);
   else if (chunks <= 256) launch_forward<T, 256, 1>(a, w32, s);
   else if (chunks <= 512) launch_forward<T, 512, 1>(a, w32, s);
-  else if (chunks <= 1024) launch_forward<T, 512, 2>(a, w32, s);
+  else if (chunks <= 1024) launch_forward<T, 1024, 1>(a, w32, s);
   else if (chunks <= kHeldChunks) launch_forward<T, 1024, 2>(a, w32, s);
   else
     hipLaunchKernelGGL((k_layernorm_long<T>), dim3((unsigned)std::min<int64_t>(a.rows, 1 << 20)), dim3(1024), 0, s, a, w32);
@@ -394,7 +397,7 @@ void launch_backward(const LayerNormBackArgs& a, bool w32, hipStream_t s) {
   hipLaunchKernelGGL((k_layernorm_backward<T, NT, CH>), dim3((unsigned)a.parts), dim3(block_of(NT)), 0, s, a, w32);
 }
 
-constexpr int kHeldBackChunks = 1024;   // the same of the backward pass
+constexpr int kHeldBackChunks = 2048;   // the same of the backward pass
 
 template <typename T> void launch_back(const LayerNormBackArgs& a, bool w32, hipStream_t s) {
   const int chunks = (a.cols + Chunk<T>::N - 1) / Chunk<T>::N;
@@ -405,7 +408,8 @@ template <typename T> void launch_back(const LayerNormBackArgs& a, bool w32, hip
     else if (chunks <= 128) launch_backward<T, 64, 2>(a, w32, s);
     else if (chunks <= 256) launch_backward<T, 256, 1>(a, w32, s);
     else if (chunks <= 512) launch_backward<T, 512, 1>(a, w32, s);
-    else if (chunks <= kHeldBackChunks) launch_backward<T, 1024, 1>(a, w32, s);
+    else if (chunks <= 1024) launch_backward<T, 1024, 1>(a, w32, s);
+    else if (chunks <= kHeldBackChunks) launch_backward<T, 1024, 2>(a, w32, s);
     else {
       const unsigned gx = (unsigned)((a.cols + 255) / 256);
       // the sums first: dx may be written over dy or dh
@@ -421,10 +425,18 @@ template <typename T> void launch_back(const LayerNormBackArgs& a, bool w32, hip
 
 }  // namespace
 
+// As the RMS norm's, whose measurements hold for two sums as well: 16000 x 1066
+// bf16 84 -> 57 us, 262144 x 64 42 -> 31, 16384 x 768 27 -> 25 against 512 blocks
+// for every size.
 int layernorm_back_parts(int64_t rows, int cols, int fmt) {
   const int chunks = (cols + (fmt == 1 ? 3 : 7)) / (fmt == 1 ? 4 : 8);
   if (chunks > kHeldBackChunks) return (int)std::min<int64_t>(256, (rows + 31) / 32);
-  const int64_t most = 512;
+  const bool whole = cols % (fmt == 1 ? 4 : 8) == 0;
+  const int64_t most = cols <= (fmt == 1 ? 1536 : 512)               ? 1024
+                       : chunks <= 128                               ? 768
+                       : cols <= 1536                                ? 1024
+                       : cols <= 2048 || (cols <= 4096 && !whole)    ? 512
+                                                                     : 256;
   const int64_t per = chunks <= 16 ? 16 : chunks <= 32 ? 8 : chunks <= 128 ? 4 : 1;   // rows at once
   return (int)std::min(most, (rows + per - 1) / per);
 }
