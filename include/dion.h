@@ -560,10 +560,14 @@ int dion_mxfp4_linear(const uint8_t* a, int64_t lda, const uint8_t* a_scale, int
  *                beyond them hold -infinity and -1
  *   top          0 .. 1024, with vocab up to 2^19 where it is not 0
  * A row that holds a NaN or +infinity has NaN statistics; a row of -infinity
- * alone has entropy 0 and log probability -infinity. */
+ * alone has entropy 0 and log probability -infinity.  The workspace holds parts
+ * of a few rows that are shared out between blocks; sizes whose workspace size
+ * is 256 use none (it may be NULL), the others' is 512 at least. */
+size_t dion_token_logprobs_workspace_size(int64_t rows, int32_t vocab, int32_t top, int32_t dtype);
 int dion_token_logprobs(const void* logits, int64_t ldz, const void* tokens, float* logprob, float* entropy,
                         float* stats, float* top_logprob, int64_t* top_index, int64_t rows, int32_t vocab, int32_t top,
-                        int32_t dtype, int32_t token_bytes, float temperature, void* stream);
+                        int32_t dtype, int32_t token_bytes, float temperature, void* workspace, size_t workspace_bytes,
+                        void* stream);
 
 /* Gradient of the logits, from the gradients gl of each row's logprob and ge of
  * its entropy (rows floats; NULL: 0):

@@ -50,8 +50,8 @@ EXPORTS = (
     "dion_int8_linear", "dion_distill_topk_workspace_size", "dion_distill_topk", "dion_distill_topk_backward",
     "dion_distill_topk_step",
     "dion_layernorm", "dion_layernorm_backward_workspace_size", "dion_layernorm_backward", "dion_mxfp4_quantize",
-    "dion_mxfp4_dequantize", "dion_mxfp4_linear_workspace_size", "dion_mxfp4_linear", "dion_token_logprobs",
-    "dion_token_logprobs_backward",
+    "dion_mxfp4_dequantize", "dion_mxfp4_linear_workspace_size", "dion_mxfp4_linear", "dion_token_logprobs_workspace_size",
+    "dion_token_logprobs",    "dion_token_logprobs_backward",
 )
 
 
@@ -170,7 +170,9 @@ def _load():
     lib.dion_mxfp4_linear_workspace_size.restype = sz
     lib.dion_mxfp4_linear.argtypes = mat + mat + mat + mat + [vp, i32] + mat + [i64, i64, i32, i32, vp, sz, vp]
     lib.dion_mxfp4_linear.restype = ctypes.c_int
-    lib.dion_token_logprobs.argtypes = mat + [vp, vp, vp, vp, vp, vp, i64, i32, i32, i32, i32, f32, vp]
+    lib.dion_token_logprobs_workspace_size.argtypes = [i64, i32, i32, i32]
+    lib.dion_token_logprobs_workspace_size.restype = sz
+    lib.dion_token_logprobs.argtypes = mat + [vp, vp, vp, vp, vp, vp, i64, i32, i32, i32, i32, f32, vp, sz, vp]
     lib.dion_token_logprobs.restype = ctypes.c_int
     lib.dion_token_logprobs_backward.argtypes = [vp, vp] + mat + [vp, vp] + mat + [i64, i32, i32, i32, f32, vp]
     lib.dion_token_logprobs_backward.restype = ctypes.c_int

@@ -227,6 +227,15 @@ __device__ __forceinline__ void far_sums(const Z* z, int vocab, float temp, floa
   }
 }
 
+// The row's token and its logit; -1 where there is none inside the vocabulary.
+template <typename Z> __device__ __forceinline__ int64_t token_of(const LogprobArgs& a, int64_t row, float& z) {
+  if (!a.tok) return -1;
+  const int64_t t = a.tok64 ? ((const int64_t*)a.tok)[row] : (int64_t)((const int32_t*)a.tok)[row];
+  if (t < 0 || t >= a.vocab) return -1;
+  z = to_f(((const Z*)a.z)[row * a.ldz + t]);
+  return t;
+}
+
 // One row to a block, read once, chunk i NT + t of 16 bytes by thread t, AHEAD
 // of them asked for before they are used.  With the alternatives (TOP), the
 // largest of each group of 2^lg neighbouring chunks is kept in LDS: a bound
@@ -236,7 +245,8 @@ __device__ __forceinline__ void far_sums(const Z* z, int vocab, float temp, floa
 // (many equal logits, or large ones side by side), the k groups with the
 // largest maxima are taken, equal ones by their order: k other groups' maxima
 // come before anything in the rest.  Then the same for parts of those groups,
-// down to single logits.
+// down to single logits.  A few rows are shared between gridDim.y blocks each,
+// whose sums and alternatives k_logprobs_join puts together.
 template <typename Z, int NT, bool TOP>
 __global__ __launch_bounds__(NT, 4) void k_logprobs(LogprobArgs a, int lg) {
   typedef Chunk<Z> C;
@@ -245,7 +255,9 @@ __global__ __launch_bounds__(NT, 4) void k_logprobs(LogprobArgs a, int lg) {
   __shared__ TopShared<TOP ? NT : 64> sh;
   const float c = LOG2E / a.temp;
   const int t = threadIdx.x;
-  const int whole = a.vocab / STEP;   // steps in which every thread has a chunk
+  const int first = a.parts ? (int)blockIdx.y * a.per : 0;   // this block's logits: a share of the row, or all
+  const int vocab = a.parts ? min(a.per, a.vocab - first) : a.vocab;
+  const int whole = vocab / STEP;   // steps in which every thread has a chunk
   uintx4 none4;
   {
     float f[N];
@@ -254,14 +266,9 @@ __global__ __launch_bounds__(NT, 4) void k_logprobs(LogprobArgs a, int lg) {
     none4 = C::pack(f);
   }
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    const Z* z = (const Z*)a.z + row * a.ldz;
-    int64_t token = -1;
+    const Z* z = (const Z*)a.z + row * a.ldz + first;
     float zt = 0.f;
-    if (a.tok) {
-      token = a.tok64 ? ((const int64_t*)a.tok)[row] : (int64_t)((const int32_t*)a.tok)[row];
-      if (token >= 0 && token < a.vocab) zt = to_f(z[token]);
-      else token = -1;
-    }
+    const int64_t token = a.parts ? -1 : token_of<Z>(a, row, zt);
     Sums<false> S;
     S.clear(a.temp, c);
     auto absorb = [&](const uintx4& v0, const uintx4& v1, int step) {   // two chunks at once
@@ -295,7 +302,7 @@ __global__ __launch_bounds__(NT, 4) void k_logprobs(LogprobArgs a, int lg) {
         S.template add<false, N>(f[1], c);
       }
     };
-    const int rest = a.vocab - whole * STEP;   // of the row, a chunk of some threads
+    const int rest = vocab - whole * STEP;   // of the row, a chunk of some threads
     const uintx4 last = rest ? C::load(z + (int64_t)whole * STEP, min(t * N, rest), rest, NEG) : none4;
     const Z* p = z + t * N;
     auto fetch = [&](int i) {
@@ -319,7 +326,7 @@ __global__ __launch_bounds__(NT, 4) void k_logprobs(LogprobArgs a, int lg) {
     float m = S.m, s = S.s, w = S.w;
     if (S.wide(c)) {   // rare: again, from the caches
       Sums<true> F;
-      far_sums<Z, NT>(z, a.vocab, a.temp, c, F);
+      far_sums<Z, NT>(z, vocab, a.temp, c, F);
       F.template join<NT>(c, red);
       m = F.m, s = F.s, w = F.w;
     }
@@ -328,18 +335,28 @@ __global__ __launch_bounds__(NT, 4) void k_logprobs(LogprobArgs a, int lg) {
     const float logs = logf(s), entropy = none ? 0.f : logs - w / s * LN2;
     auto logprob = [&](float v) { return none ? NEG : (v - m) / a.temp - logs; };
     if (t == 0) {
-      if (a.tok) a.logprob[row] = token >= 0 ? logprob(zt) : 0.f;
-      a.entropy[row] = entropy;
-      if (a.stats) a.stats[row] = make_float4(m, s, entropy, logs);
+      if (a.parts) {
+        a.parts[row * a.shares + blockIdx.y] = make_float4(m, s, w, 0.f);
+      } else {
+        if (a.tok) a.logprob[row] = token >= 0 ? logprob(zt) : 0.f;
+        a.entropy[row] = entropy;
+        if (a.stats) a.stats[row] = make_float4(m, s, entropy, logs);
+      }
     }
     if constexpr (TOP) {
-      int size = N << lg, n = (a.vocab + size - 1) / size, k = min(a.k, n);
+      int size = N << lg, n = (vocab + size - 1) / size, k = min(a.k, n);
       auto output = [&](int i, unsigned long long v) {   // place i
         const uint32_t best = (uint32_t)(v >> 32);
-        a.top[row * a.k + i] = best >= ABSENT ? logprob(value_of(best)) : NEG;
-        a.index[row * a.k + i] = best >= ABSENT ? (int64_t)(0xffffffffu - (uint32_t)v) : -1;
+        if (a.parts) {
+          a.list[(row * a.shares + blockIdx.y) * a.k + i] = best >= ABSENT ? v : 0;
+        } else {
+          a.top[row * a.k + i] = best >= ABSENT ? logprob(value_of(best)) : NEG;
+          a.index[row * a.k + i] = best >= ABSENT ? (int64_t)(0xffffffffu - (uint32_t)v) : -1;
+        }
       };
-      auto pair = [&](uint32_t key, int id) { return (unsigned long long)key << 32 | (0xffffffffu - (uint32_t)id); };
+      auto pair = [&](uint32_t key, int id) {
+        return (unsigned long long)key << 32 | (0xffffffffu - (uint32_t)(first + id));
+      };
       bool done = false;
       {
         float held[KEYS];   // (written before the joins' barriers)
@@ -387,9 +404,9 @@ __global__ __launch_bounds__(NT, 4) void k_logprobs(LogprobArgs a, int lg) {
           for (int q0 = 0; q0 < reach << lg; q0 += NT) {
             const int q = q0 + t;
             float f[N];
-            int j = a.vocab;
+            int j = vocab;
             if (q < reach << lg) j = ((sh.near[q >> lg] << lg) + (q & ((1 << lg) - 1))) * N;
-            const uintx4 v = C::load(z, min(j, a.vocab), a.vocab, NEG);
+            const uintx4 v = C::load(z, min(j, vocab), vocab, NEG);
             C::unpack(v, f);
 #pragma unroll
             for (int e = 0; e < N; ++e) hits |= f[e] >= bound ? 1u << e : 0;
@@ -437,7 +454,7 @@ __global__ __launch_bounds__(NT, 4) void k_logprobs(LogprobArgs a, int lg) {
         while (size > 1) {
           const int part = max(1, size / SUB), r = size / part;
           // the parts that lie in the row at all: only its last group may hold others, behind them
-          const int parts = (a.vocab + part - 1) / part, last_id = sh.id[turn][k - 1], all = k * r;
+          const int parts = (vocab + part - 1) / part, last_id = sh.id[turn][k - 1], all = k * r;
           n = all - max(0, (last_id + 1) * r - parts);
           const int held = (all + NT - 1) / NT, from = turn;
 #pragma unroll 1
@@ -447,7 +464,7 @@ __global__ __launch_bounds__(NT, 4) void k_logprobs(LogprobArgs a, int lg) {
             if (q < all) {
               const int j = (sh.id[from][q / r] * r + q % r) * part;
               for (int e = 0; e < part; ++e)
-                if (j + e < a.vocab) top = fmaxf(top, to_f(z[j + e]));
+                if (j + e < vocab) top = fmaxf(top, to_f(z[j + e]));
             }
             sh.group[q] = q < all ? key_of(top) : 0;
           }
@@ -479,6 +496,63 @@ __global__ __launch_bounds__(NT, 4) void k_logprobs(LogprobArgs a, int lg) {
         for (int i = t; i < a.k; i += NT) output(i, i < k ? sh.order[i] : 0);
       }
       lds_barrier();   // the next row's groups may be written
+    }
+  }
+}
+
+// A few rows in shares: their sums relative to the row's largest logit, and the
+// k first of the shares' alternatives.  Wave w walks list w, four at a time,
+// until they are behind the k first: an alternative's place is the number of
+// those before it in every list, one lane to a list.
+constexpr int kShares = 16, kSharedTop = 32;
+template <typename Z> __global__ __launch_bounds__(64 * kShares) void k_logprobs_join(LogprobArgs a) {
+  __shared__ unsigned long long list[kShares * kSharedTop];
+  const float c = LOG2E / a.temp;
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6, other = lane & 15;
+  const int64_t row = blockIdx.x;
+  const int n = a.shares * a.k;
+  for (int i = t; i < n; i += 64 * kShares) list[i] = a.list[row * n + i];
+  float zt = 0.f;
+  const int64_t token = token_of<Z>(a, row, zt);
+  const float4 p = lane < a.shares ? a.parts[row * a.shares + lane] : make_float4(LOWEST, 0.f, 0.f, 0.f);
+  Sums<true> S;
+  S.m = p.x, S.r = p.x * c, S.s = p.y, S.w = p.z;
+  S.to(wave_max(S.m), c);
+  const float m = S.m, s = wave_sum(S.s), w = wave_sum(S.w);
+  const bool none = s == 0.f;
+  const float logs = logf(s), entropy = none ? 0.f : logs - w / s * LN2;
+  auto logprob = [&](float v) { return none ? NEG : (v - m) / a.temp - logs; };
+  if (t == 0) {
+    if (a.tok) a.logprob[row] = token >= 0 ? logprob(zt) : 0.f;
+    a.entropy[row] = entropy;
+    if (a.stats) a.stats[row] = make_float4(m, s, entropy, logs);
+  }
+  __syncthreads();
+  // how many of list `other` are above v (the lists descend, absent ones are 0)
+  auto above = [&](unsigned long long v) {
+    int lo = 0, hi = other < a.shares ? a.k : 0;
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (list[other * a.k + mid] > v) lo = mid + 1;
+      else hi = mid;
+    }
+    return row16_reduce((float)lo, Add());
+  };
+  if (wave < a.shares)
+    for (int i = lane >> 4;; i += 4) {
+      const unsigned long long v = i < a.k ? list[wave * a.k + i] : 0;
+      const int place = (int)above(v);
+      const bool here = v != 0 && place < a.k;
+      if (!__any(here)) break;
+      if (here && other == 0) {
+        a.top[row * a.k + place] = logprob(value_of((uint32_t)(v >> 32)));
+        a.index[row * a.k + place] = (int64_t)(0xffffffffu - (uint32_t)v);
+      }
+    }
+  if (a.k > 0 && wave == 0) {   // places without one
+    for (int i = (int)above(0) + lane; i < a.k; i += 64) {
+      a.top[row * a.k + i] = NEG;
+      a.index[row * a.k + i] = -1;
     }
   }
 }
@@ -530,23 +604,47 @@ __global__ __launch_bounds__(NT, 8) void k_logprobs_backward(LogprobArgs a) {
   }
 }
 
-template <typename Z, int NT, bool TOP>
-void launch_rows(const LogprobArgs& a, int lg, hipStream_t s) {
-  hipLaunchKernelGGL((k_logprobs<Z, NT, TOP>), dim3((unsigned)std::min<int64_t>(a.rows, 1 << 20)), dim3(NT), 0, s, a, lg);
+// Shares of a row, where a few rows are split (0: they are not), and the logits
+// of one.  A row on one CU waits for its exponentials, and a second launch costs
+// 2.5 to 5 (us, one CU a row and 16 shares: 1 x 128256 bf16 10.4 and 7.0, with 20
+// alternatives 16.0 and 12.3, with 64 16.5 and 16.9; 1 x 32001 8.0 and 6.6, with
+// 20 13.8 and 13.0; 64 x 128256 12.3 and 11.4, with 20 18.8 and 18.3).
+int logprob_shares(int64_t rows, int vocab, int k, int& per) {
+  if (rows == 0 || rows > 32 || k > kSharedTop || vocab < (k ? 49152 : 24576)) return 0;
+  const int most = (int)std::min<int64_t>(kShares, 256 / rows);
+  per = (int)(((int64_t)vocab + most - 1) / most + 4095) / 4096 * 4096;
+  return (vocab + per - 1) / per;
 }
 
-template <typename Z> void launch_forward(const LogprobArgs& a, hipStream_t s) {
+template <typename Z, int NT, bool TOP>
+void launch_rows(const LogprobArgs& a, int lg, hipStream_t s) {
+  const dim3 grid((unsigned)std::min<int64_t>(a.rows, 1 << 20), (unsigned)(a.parts ? a.shares : 1));
+  hipLaunchKernelGGL((k_logprobs<Z, NT, TOP>), grid, dim3(NT), 0, s, a, lg);
+}
+
+template <typename Z> void launch_forward(LogprobArgs a, hipStream_t s) {
   constexpr int N = Chunk<Z>::N;
+  // groups of one, four or eight chunks, as many as the keys that the threads hold
+  const auto groups = [&](int64_t nt, int64_t vocab) {
+    return vocab <= nt * KEYS * N ? 0 : vocab <= nt * KEYS * N * 4 ? 2 : 3;
+  };
+  a.shares = logprob_shares(a.rows, a.vocab, a.k, a.per);
+  if (a.shares && a.parts) {   // parts: checked scratch, wherever there are shares
+    a.list = (uint64_t*)(a.parts + a.rows * a.shares);
+    if (a.k) launch_rows<Z, 256, true>(a, groups(256, a.per), s);
+    else launch_rows<Z, 256, false>(a, 0, s);
+    hipLaunchKernelGGL((k_logprobs_join<Z>), dim3((unsigned)a.rows), dim3(64 * kShares), 0, s, a);
+    return;
+  }
+  a.parts = nullptr;
   if (a.k == 0) {
     if (a.rows > 256 || a.vocab <= 256 * 8 * N) launch_rows<Z, 256, false>(a, 0, s);
     else launch_rows<Z, 1024, false>(a, 0, s);
     return;
   }
-  // groups of one, four or eight chunks, as many as the keys that the threads hold
-  const auto groups = [&](int64_t nt) { return a.vocab <= nt * KEYS * N ? 0 : a.vocab <= nt * KEYS * N * 4 ? 2 : 3; };
   const bool small = a.k <= 256 && a.vocab <= 256 * KEYS * N * 8;
-  if (small && (a.rows > 256 || a.vocab <= 256 * 8 * N)) launch_rows<Z, 256, true>(a, groups(256), s);
-  else launch_rows<Z, 1024, true>(a, groups(1024), s);
+  if (small && (a.rows > 256 || a.vocab <= 256 * 8 * N)) launch_rows<Z, 256, true>(a, groups(256, a.vocab), s);
+  else launch_rows<Z, 1024, true>(a, groups(1024, a.vocab), s);
 }
 
 // 4096 x 50257 and 8192 x 128256 bf16 (us): 164 and 823 on 512 threads with two
@@ -562,6 +660,12 @@ template <typename Z> void launch_gradient(const LogprobArgs& a, hipStream_t s) 
 }
 
 }  // namespace
+
+size_t logprob_scratch(int64_t rows, int vocab, int k, int) {
+  int per = 0;
+  const int shares = logprob_shares(rows, vocab, k, per);
+  return (size_t)rows * shares * (16 + 8 * (size_t)k);
+}
 
 void launch_token_logprobs(int fmt, const LogprobArgs& a, hipStream_t s) {
   if (fmt == 1) launch_forward<float>(a, s);

@@ -244,9 +244,19 @@ struct LogprobCheck : Check {
 
 extern "C" {
 
+size_t dion_token_logprobs_workspace_size(int64_t rows, int32_t vocab, int32_t top, int32_t dtype) {
+  if (rows < 0 || rows > kMaxRows || vocab <= 0 || vocab > (1 << 30) || top < 0 || top > kLogprobMaxTop ||
+      (top > 0 && vocab > kLogprobMaxTopVocab) || !valid_dtype(dtype)) {
+    (void)guarded([&]() { return set_error(DION_E_INVAL, "rows, vocab, top or dtype out of range"); });
+    return 0;
+  }
+  return reported_size(logprob_scratch(rows, vocab, top, dtype));
+}
+
 int dion_token_logprobs(const void* logits, int64_t ldz, const void* tokens, float* logprob, float* entropy,
                         float* stats, float* top_logprob, int64_t* top_index, int64_t rows, int32_t vocab, int32_t top,
-                        int32_t dtype, int32_t token_bytes, float temperature, void* stream) {
+                        int32_t dtype, int32_t token_bytes, float temperature, void* workspace, size_t workspace_bytes,
+                        void* stream) {
   return guarded([&]() {
     LogprobArgs a{};
     a.z = logits;
@@ -279,6 +289,15 @@ int dion_token_logprobs(const void* logits, int64_t ldz, const void* tokens, flo
       check_apart(c, out[i], c.z);
       check_apart(c, out[i], c.tok);
       for (int j = 0; j < i; ++j) check_apart(c, out[i], out[j]);
+    }
+    const size_t need = c.code != DION_OK ? 0 : dion_token_logprobs_workspace_size(rows, vocab, top, dtype);
+    if (need > kNone) {
+      check_workspace(c, workspace, workspace_bytes, need);
+      const View vws{workspace, (int64_t)workspace_bytes, 1, (int64_t)workspace_bytes, 1, "workspace"};
+      for (const View& v : out) check_apart(c, vws, v);
+      check_apart(c, vws, c.z);
+      check_apart(c, vws, c.tok);
+      a.parts = (float4*)workspace;
     }
     if (c.code != DION_OK || rows == 0) return c.done();
     const hipStream_t st = (hipStream_t)stream;

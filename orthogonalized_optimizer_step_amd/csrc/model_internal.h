@@ -83,6 +83,9 @@ struct LogprobArgs {
   int vocab, k;
   int tok64;
   float temp;
+  float4* parts;          // scratch of a few rows in shares: rows x shares sums,
+  uint64_t* list;         // and rows x shares x k alternatives; NULL otherwise
+  int shares, per;        // shares of a row, logits in one
 };
 
 constexpr int kLayerNormMaxCols = 65536;
@@ -102,6 +105,8 @@ void launch_mxfp4_dequantize(int fmt, const MxCodesArgs& a, hipStream_t s);
 size_t mxfp4_linear_scratch(const MxArgs& a);
 void launch_mxfp4_linear(MxArgs a, hipStream_t s);
 
+// bytes of scratch (LogprobArgs::parts) that the log probabilities need
+size_t logprob_scratch(int64_t rows, int vocab, int k, int fmt);
 void launch_token_logprobs(int fmt, const LogprobArgs& a, hipStream_t s);
 void launch_token_logprobs_backward(int fmt, const LogprobArgs& a, hipStream_t s);
 

@@ -161,7 +161,7 @@ def _logprob_inputs(logits, tokens, stream):
     return dev, rows, vocab, ldz, code, _dense(tokens, stream), tokens.element_size()
 
 
-def token_logprobs(logits, tokens, temperature=1.0, stream=None):
+def token_logprobs(logits, tokens, temperature=1.0, workspace=None, stream=None):
     """Log probability of each row's token and the row's entropy: returns (logprob, entropy, stats).
 
     ``logits``: rows x vocab; ``tokens`` (int64 or int32): rows.  A token outside the vocabulary (padding) has
@@ -169,36 +169,37 @@ def token_logprobs(logits, tokens, temperature=1.0, stream=None):
     dev, rows, vocab, ldz, code, tok, tb = _logprob_inputs(logits, tokens, stream)
     if tok is None:
         _fail("tokens are needed")
+    keep, ws, have = _scratch(lib.dion_token_logprobs_workspace_size(rows, vocab, 0, code), logits, workspace, stream)
     shape = logits.shape[:-1]
     logprob, entropy = _new(shape, torch.float32, logits, stream), _new(shape, torch.float32, logits, stream)
     stats = _new((*shape, 4), torch.float32, logits, stream)
     rc = lib.dion_token_logprobs(logits.data_ptr(), ldz, tok.data_ptr(), logprob.data_ptr(), entropy.data_ptr(),
-                                 stats.data_ptr(), None, None, rows, vocab, 0, code, tb, temperature,
+                                 stats.data_ptr(), None, None, rows, vocab, 0, code, tb, temperature, ws, have,
                                  _handle(stream, dev))
     if rc:
         check(rc)
-    _used(stream, logits, tok)
+    _used(stream, logits, tok, keep)
     return logprob, entropy, stats
 
 
-def top_logprobs(logits, k, tokens=None, temperature=1.0, stream=None):
+def top_logprobs(logits, k, tokens=None, temperature=1.0, workspace=None, stream=None):
     """The k likeliest tokens of each row: returns (top, index, logprob, entropy).
 
     ``top`` (fp32, descending) and ``index`` (int64; equal logits in the order of their index) have k places a row;
     places beyond the logits above -inf hold -inf and -1, which ``distill_loss`` takes as absent entries.  ``logprob``
     is that of ``tokens`` as in ``token_logprobs``, None without them."""
     dev, rows, vocab, ldz, code, tok, tb = _logprob_inputs(logits, tokens, stream)
+    keep, ws, have = _scratch(lib.dion_token_logprobs_workspace_size(rows, vocab, k, code), logits, workspace, stream)
     shape = logits.shape[:-1]
     logprob = None if tok is None else _new(shape, torch.float32, logits, stream)
     entropy = _new(shape, torch.float32, logits, stream)
-    top = _new((*shape, max(0, k)), torch.float32, logits, stream)
-    index = _new((*shape, max(0, k)), torch.int64, logits, stream)
+    top, index = _new((*shape, k), torch.float32, logits, stream), _new((*shape, k), torch.int64, logits, stream)
     rc = lib.dion_token_logprobs(logits.data_ptr(), ldz, _ptr(tok), _ptr(logprob), entropy.data_ptr(), None,
-                                 top.data_ptr(), index.data_ptr(), rows, vocab, k, code, tb, temperature,
+                                 top.data_ptr(), index.data_ptr(), rows, vocab, k, code, tb, temperature, ws, have,
                                  _handle(stream, dev))
     if rc:
         check(rc)
-    _used(stream, logits, tok)
+    _used(stream, logits, tok, keep)
     return top, index, logprob, entropy
 
 

@@ -47,9 +47,10 @@ void launch_mxfp4_linear(MxArgs a, hipStream_t) {
   need(a.out && a.m > 0 && a.n > 0 && (scratch == 0) == (a.partial == nullptr) &&
        (a.kb == 0 || (a.lda >= a.kb && a.ldb >= a.kb)));
 }
+size_t logprob_scratch(int64_t, int, int, int) { return scratch; }
 void launch_token_logprobs(int, const LogprobArgs& a, hipStream_t) {
   need(a.z && a.entropy && (!a.tok || a.logprob) && (a.k == 0 || (a.top && a.index)) && a.k <= kLogprobMaxTop &&
-       (a.k == 0 || a.vocab <= kLogprobMaxTopVocab) && a.temp > 0);
+       (a.k == 0 || a.vocab <= kLogprobMaxTopVocab) && a.temp > 0 && (scratch == 0) == (a.parts == nullptr));
 }
 void launch_token_logprobs_backward(int, const LogprobArgs& a, hipStream_t) { need(a.z && a.dz && a.stats && a.temp > 0); }
 }  // namespace dion
@@ -98,7 +99,8 @@ int main() {
     count(dion_mxfp4_dequantize(u8(), ld, u8(), ld, ptr(), ld, rows, cols, dt, nullptr));
     (void)dion_mxfp4_linear_workspace_size(u8(), ld, u8(), ld, u8(), ld, u8(), ld, rows, cols, k);
     count(dion_mxfp4_linear(u8(), ld, u8(), ld, u8(), ld, u8(), ld, ptr(), wdt, ptr(), ld, rows, cols, k, dt, ptr(), have, nullptr));
-    count(dion_token_logprobs(ptr(), ld, ptr(), f32(), f32(), f32(), f32(), (int64_t*)ptr(), rows, cols, k, dt, (int)PICK(4, 8, 2), temp, nullptr));
+    (void)dion_token_logprobs_workspace_size(rows, cols, k, dt);
+    count(dion_token_logprobs(ptr(), ld, ptr(), f32(), f32(), f32(), f32(), (int64_t*)ptr(), rows, cols, k, dt, (int)PICK(4, 8, 2), temp, ptr(), have, nullptr));
     count(dion_token_logprobs_backward(f32(), f32(), ptr(), ld, f32(), ptr(), ptr(), ld, rows, cols, dt, (int)PICK(4, 8), temp, nullptr));
   }
   if (reached < 1000 || refused < 1000) std::abort();

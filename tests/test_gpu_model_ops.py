@@ -397,7 +397,8 @@ def logprob_check(dion, z, tokens, temp, k, gl, ge):
 
 LOGPROB = [(1, 1, 1), (3, 2, 2), (1, 17, 5), (5, 1000, 1), (3, 1023, 64), (16, 4096, 100), (2, 50257, 20),
            (1, 131072, 128), (7, 32001, 17), (300, 257, 8), (20, 8192, 1024), (33, 40000, 3), (4, 32768, 256),
-           (3, 32769, 257), (600, 2000, 40), (5, 131073, 1000), (3, 100, 1024), (2, 300000, 64), (260, 5000, 12)]
+           (3, 32769, 257), (600, 2000, 40), (5, 131073, 1000), (3, 100, 1024), (2, 300000, 64), (260, 5000, 12),
+           (1, 49152, 32), (32, 50000, 5), (33, 50000, 5), (3, 400001, 32), (17, 65537, 1), (1, 128256, 20)]
 
 
 @pytest.mark.parametrize("rows,vocab,k", LOGPROB)
@@ -446,11 +447,11 @@ def test_top_of_equal_ascending_and_masked_rows(dion, vocab, dtype):
     z[13] = torch.randint(-2, 1, (vocab,), generator=g, device="cuda").to(dt) * 1000
     tokens = torch.full((14,), 7, device="cuda")
     gl = torch.ones(14, device="cuda")
-    for k in (1, 64, 130):
+    for k in (1, 20, 64, 130):
         logprob_check(dion, z, tokens, 1.0, k, gl, -0.5 * gl)
 
 
-@pytest.mark.parametrize("vocab", [300, 70000])
+@pytest.mark.parametrize("vocab", [300, 40000, 70000])
 def test_logprobs_nan_and_infinite_rows(dion, vocab):
     """A NaN or +inf makes its row's statistics NaN, and no other's; a left-out row has gradient 0 whatever it holds."""
     z, _ = logits_case(5, vocab, torch.float32)

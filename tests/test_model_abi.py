@@ -112,8 +112,11 @@ def test_little_scratch_is_asked_for_and_checked(m, n, k, off):
 
 
 def test_logprobs_refusals():
-    def fwd(z=A, ldz=500, t=B, lp=C, ent=D, stats=E, top=F, index=G, rows=4, vocab=500, k=8, dt=BF16, tb=8, temp=1.0):
-        return lib.dion_token_logprobs(z, ldz, t, lp, ent, stats, top, index, rows, vocab, k, dt, tb, temp, None)
+    size = lib.dion_token_logprobs_workspace_size
+
+    def fwd(z=A, ldz=500, t=B, lp=C, ent=D, stats=E, top=F, index=G, rows=4, vocab=500, k=8, dt=BF16, tb=8, temp=1.0,
+            ws=None, have=0):
+        return lib.dion_token_logprobs(z, ldz, t, lp, ent, stats, top, index, rows, vocab, k, dt, tb, temp, ws, have, None)
 
     def back(z=A, ldz=500, t=B, gl=C, ge=D, stats=E, dz=F, ldd=500, rows=4, vocab=500, dt=BF16, tb=8, temp=1.0):
         return lib.dion_token_logprobs_backward(gl, ge, z, ldz, stats, t, dz, ldd, rows, vocab, dt, tb, temp, None)
@@ -131,6 +134,16 @@ def test_logprobs_refusals():
                       (dict(lp=A), INVAL), (dict(ent=B), INVAL), (dict(ent=C), INVAL), (dict(top=G), INVAL),
                       (dict(index=E), INVAL), (dict(stats=A), INVAL), (dict(index=G + 4), INVAL)):
         assert fwd(**bad) == code, bad
+    assert size(4, 500, 8, BF16) == 256 and size(4096, 128256, 64, BF16) == 256 and size(0, 128256, 64, BF16) == 256
+    for bad in ((-1, 5, 1, BF16), (1, 0, 1, BF16), (1, 5, 1025, BF16), (1, 5, -1, BF16), (1, (1 << 19) + 1, 1, BF16), (1, 5, 1, 3)):
+        assert size(*bad) == 0
+    for rows, vocab, k in ((1, 128256, 20), (1, 128256, 0), (4, 100000, 32), (1, 128256, 1)):
+        need, big = size(rows, vocab, k, BF16), dict(rows=rows, vocab=vocab, ldz=vocab, k=k)
+        assert need > 256
+        assert fwd(**big) == WORKSPACE and fwd(ws=H, have=need - 1, **big) == WORKSPACE
+        assert fwd(ws=H + 8, have=need, **big) == WORKSPACE
+        for on in (A, B, C, D, E) + ((F, G) if k else ()):
+            assert fwd(ws=on, have=need, **big) == INVAL
     for bad in (dict(stats=None), dict(stats=E + 8), dict(dz=None), dict(dz=A + 2), dict(dz=A, ldd=600), dict(dz=B),
                 dict(dz=C), dict(dz=D), dict(dz=E), dict(ldd=100), dict(gl=C + 2)):
         assert back(**bad) == INVAL, bad
@@ -141,5 +154,5 @@ def test_no_rows_is_no_work():
     assert lib.dion_mxfp4_quantize(None, 8, None, 4, None, 1, 0, 8, BF16, None) == 0
     assert lib.dion_mxfp4_dequantize(None, 4, None, 1, None, 8, 0, 8, BF16, None) == 0
     assert lib.dion_mxfp4_linear(None, 4, None, 1, A, 4, B, 1, None, 0, None, 8, 0, 8, 8, BF16, None, 0, None) == 0
-    assert lib.dion_token_logprobs(None, 8, None, None, None, None, None, None, 0, 8, 2, BF16, 8, 1.0, None) == 0
+    assert lib.dion_token_logprobs(None, 8, None, None, None, None, None, None, 0, 8, 2, BF16, 8, 1.0, None, 0, None) == 0
     assert lib.dion_token_logprobs_backward(None, None, None, 8, None, None, None, 8, 0, 8, BF16, 8, 1.0, None) == 0
