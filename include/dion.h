@@ -519,7 +519,8 @@ int dion_layernorm_backward(const void* dy, int64_t lddy, const void* h, int64_t
  * 2^(s - 127); 255 stands for NaN.
  *   q       rows of ceil(cols / 2) bytes (a missing last code is written as 0)
  *   scale   rows of ceil(cols / 32) bytes
- * both with a stride in bytes, at any alignment.  dion_mxfp4_quantize takes
+ * both with a stride in bytes, at any alignment; cols up to 2^30.
+ * dion_mxfp4_quantize takes
  * the least scale 2^e (e from -127 on) with max|x| < 7 2^e, and the nearest
  * code, ties to the even one; a block of 32 that holds an infinity or a NaN
  * gets the scale 255 and codes 0.  dion_mxfp4_dequantize writes the values,

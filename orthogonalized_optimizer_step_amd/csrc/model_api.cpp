@@ -110,7 +110,7 @@ struct MxViews {
       : q{q_, ldq, rows, (cols + 1) / 2, 1, codes}, s{s_, lds, rows, (cols + 31) / 32, 1, scales} {}
 };
 
-constexpr int32_t kMxMaxK = 1 << 22;
+constexpr int32_t kMxMaxK = 1 << 22, kMxMaxCols = 1 << 30;
 constexpr int64_t kMxMaxRows = 1 << 22;
 
 }  // namespace
@@ -123,6 +123,7 @@ int dion_mxfp4_quantize(const void* x, int64_t ldx, uint8_t* q, int64_t ldq, uin
     Check c;
     c.need(valid_dtype(dtype), "unknown dtype");
     check_rows(c, rows, cols, "cols must be positive");
+    if (cols > kMxMaxCols) c.fail(DION_E_UNSUPPORTED, "more than 2^30 columns");
     if (c.code != DION_OK) return c.done();
     const View vx{x, ldx, rows, cols, esize(dtype), "x"};
     const MxViews v(q, ldq, scale, lds, rows, cols, "q", "scale");
@@ -145,6 +146,7 @@ int dion_mxfp4_dequantize(const uint8_t* q, int64_t ldq, const uint8_t* scale, i
     Check c;
     c.need(valid_dtype(dtype), "unknown dtype");
     check_rows(c, rows, cols, "cols must be positive");
+    if (cols > kMxMaxCols) c.fail(DION_E_UNSUPPORTED, "more than 2^30 columns");
     if (c.code != DION_OK) return c.done();
     const View vy{y, ldy, rows, cols, esize(dtype), "y"};
     const MxViews v(q, ldq, scale, lds, rows, cols, "q", "scale");

@@ -69,23 +69,20 @@ def layernorm_backward(dy, h, weight, mean, rstd, dh=None, bias=True, workspace=
 
 
 # ------------------------------------------- microscaled 4-bit floating point
-def _bytes(t, what):
-    if t.dtype != torch.uint8:
-        _fail(f"{what}: expected torch.uint8, got {t.dtype}")
-
-
 def _codes(q, scale, what, cols, dev):
     """rows, row strides of codes and scales, and columns of a 4-bit matrix"""
-    _beside(scale, f"{what}'s scales", dev)
-    _bytes(q, what)
-    _bytes(scale, f"{what}'s scales")
+    _beside(scale, "the scales", dev)
+    if q.dtype != torch.uint8 or scale.dtype != torch.uint8:
+        _fail(f"{what} and its scales must be torch.uint8, got {q.dtype} and {scale.dtype}")
     rows, held, ldq = _matrix(q, what)
-    cols = 2 * held if cols is None else cols
-    if (cols + 1) // 2 != held:
+    if cols is None:
+        cols = 2 * held
+    elif (cols + 1) // 2 != held:
         _fail(f"{what}: {held} bytes a row hold {2 * held} or {max(0, 2 * held - 1)} columns, not {cols}")
-    if scale.shape != (*q.shape[:-1], (cols + 31) // 32):
+    srows, blocks, lds = _matrix(scale, "the scales")
+    if blocks != (cols + 31) // 32 or srows != rows or q.shape[:-1] != scale.shape[:-1]:
         _fail(f"{what}'s scales: shape {tuple(scale.shape)}, expected {(*q.shape[:-1], (cols + 31) // 32)}")
-    return rows, ldq, _matrix(scale, f"{what}'s scales")[2], cols
+    return rows, ldq, lds, cols
 
 
 def mxfp4_quantize(x, stream=None):

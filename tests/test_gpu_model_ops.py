@@ -259,7 +259,7 @@ LINEAR = [(1, 1, 2), (1, 5, 0), (2, 3, 18), (1, 64, 64), (1, 1000, 334), (3, 257
           (17, 100, 300), (24, 520, 1024), (33, 129, 66), (64, 256, 2048), (65, 300, 510), (100, 64, 14336),
           (128, 128, 256), (129, 257, 200), (200, 1000, 778), (256, 512, 1024), (300, 270, 130), (515, 777, 640),
           (1030, 260, 384), (70, 90, 48), (300, 140, 208), (1500, 1300, 1040), (4100, 4200, 400), (1, 14000, 512),
-          (7, 14001, 1000), (3000, 3001, 1536), (2, 100, 14336), (40, 40, 32), (2049, 1793, 2560), (130, 130, 512)]
+          (7, 14001, 1000), (3000, 3001, 1536), (2, 100, 14336), (40, 40, 32), (2049, 1793, 2560), (130, 130, 512), (40, 70, 0), (9, 14336, 768)]
 
 
 @pytest.mark.parametrize("m,n,k", LINEAR)
@@ -488,6 +488,47 @@ def test_logprobs_of_nearly_certain_rows_keep_a_small_entropy(dion):
     _, ent, _ = dion.token_logprobs(z, torch.zeros(3, dtype=torch.int64, device="cuda"))
     _, ref, _, _ = O.logprobs(n64(z), np.zeros(3, np.int64), 1.0)
     within(ent, ref, 12 * 2.0 ** -24 + ref * 2.0 ** -14, "entropy")
+
+
+# ------------------------------------------------------ beyond 2^31 elements
+def test_offsets_beyond_32_bits(dion):
+    """Rows behind 2^31 elements (and 2^32 bytes) come out as they do alone."""
+    rows, cols = 300000, 8192
+    x = torch.zeros(rows, cols, device="cuda", dtype=torch.bfloat16)
+    x[-3:] = randn(1, (3, cols), torch.bfloat16)
+    tail = x[-3:].clone()
+    w, b = randn(2, (cols,), torch.bfloat16), randn(3, (cols,), torch.bfloat16)
+    y, _, mean, rstd = dion.layernorm(x, w, b)
+    ty, _, tmean, trstd = dion.layernorm(tail, w, b)
+    assert torch.equal(y[-3:], ty) and torch.equal(mean[-3:], tmean) and torch.equal(rstd[-3:], trstd)
+    dx, _, _ = dion.layernorm_backward(y, x, w, mean, rstd)
+    assert torch.equal(dx[-3:], dion.layernorm_backward(ty, tail, w, tmean, trstd)[0])
+    del y, dx
+    q, s = dion.mxfp4_quantize(x)
+    tq, ts = dion.mxfp4_quantize(tail)
+    assert torch.equal(q[-3:], tq) and torch.equal(s[-3:], ts)
+    back = dion.mxfp4_dequantize(q, s)
+    assert torch.equal(back[-3:], dion.mxfp4_dequantize(tq, ts))
+    del back
+    # a product whose output and first operand are as large
+    head, hs = dion.mxfp4_quantize(randn(4, (8000, cols), torch.bfloat16))
+    out = dion.mxfp4_linear(q, s, head, hs)
+    want = dion.mxfp4_linear(q[-256:].contiguous(), s[-256:].contiguous(), head, hs, out_dtype=torch.float32)
+    assert not out[:5].any()
+    ref = n64(want[-3:])
+    within(out[-3:], ref, 2.0 ** -8 * np.abs(ref) + (cols / 64 + 80) * 2.0 ** -22 * np.abs(ref).max(), "out")
+    del out, q, s, want
+    t = torch.arange(rows, device="cuda") % cols
+    lp, ent, stats = dion.token_logprobs(x, t)
+    top, index, lp2, _ = dion.top_logprobs(x, 4, t)
+    a = dion.token_logprobs(tail, t[-3:])
+    c = dion.top_logprobs(tail, 4, t[-3:])
+    assert torch.equal(lp, lp2) and torch.equal(index[-3:], c[1])
+    within(lp[-3:], n64(a[0]), 2.0 ** -18, "logprob")   # 256 threads against 1024: the same to a few roundings of 10
+    one = torch.ones(rows, device="cuda")
+    d = dion.token_logprobs_backward(one, None, x, stats, t)
+    e = dion.token_logprobs_backward(one[-3:], None, tail, stats[-3:].contiguous(), t[-3:])
+    assert torch.equal(d[-3:], e)
 
 
 # ------------------------------------------------- streams, graphs, autograd

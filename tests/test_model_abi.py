@@ -62,7 +62,8 @@ def test_mxfp4_codes_refusals(read):
     for bad, code in ((dict(x=None), INVAL), (dict(q=None), INVAL), (dict(s=None), INVAL), (dict(ldx=99), INVAL),
                       (dict(ldq=49), INVAL), (dict(lds=3), INVAL), (dict(rows=-1), INVAL), (dict(cols=0), INVAL),
                       (dict(dt=4), INVAL), (dict(x=A + 1), INVAL), (dict(q=A), INVAL), (dict(s=A), INVAL),
-                      (dict(rows=(1 << 40) + 1), UNSUPPORTED), (dict(cols=-5), INVAL)):
+                      (dict(rows=(1 << 40) + 1), UNSUPPORTED), (dict(cols=-5), INVAL),
+                      (dict(cols=(1 << 30) + 1, ldx=1 << 31, ldq=1 << 30, lds=1 << 26), UNSUPPORTED)):
         assert codes(read, **bad) == code, bad
     assert read or codes(read, q=C) == INVAL
 
