@@ -374,8 +374,10 @@ __global__ __launch_bounds__(NT, 4) void k_logprobs(LogprobArgs a, int lg) {
           return block_count<NT>(c, sh, turn);
         };
         // The bound: down from the largest in growing steps (half an exponent's
-        // first), then between the last two.
-        const int few = min(2 * NT, 2 * a.k + 64);
+        // first), then between the last two.  Groups hold more than one logit above
+        // it now and then: few enough that their lists hold those as well (k = 256
+        // of 50257, 4096 rows: 165 us, 260 with as many groups as the lists have).
+        const int few = min(NT + NT / 2, 2 * a.k + 64);
         const uint32_t top = max(key_of(m), ABSENT);
         uint32_t lo = top + 1, hi = top + 1, step = 1u << 22;
         int reach = 0;
@@ -622,6 +624,12 @@ void launch_rows(const LogprobArgs& a, int lg, hipStream_t s) {
   hipLaunchKernelGGL((k_logprobs<Z, NT, TOP>), grid, dim3(NT), 0, s, a, lg);
 }
 
+// Threads of a row: 256, of which a CU holds eight rows, or 1024 where there is a
+// row to a CU at most and it is long, or the lists of 256 do not hold k (us,
+// bf16, 256 and 1024 threads: 4096 x 50257 90 and 149, with 64 alternatives 116
+// and 254; 300 x 128256 22 and 26, 33 and 38; 64 x 128256 16.5 and 12.0, 26.1 and
+// 19.8; 64 x 65536 10.5 and 8.2, 18.4 and 15.6; 64 x 32001 7.1 and 7.1, 13.7 and
+// 15.4; 64 x 8000 4.9 and 5.8, 11.4 and 14.1).
 template <typename Z> void launch_forward(LogprobArgs a, hipStream_t s) {
   constexpr int N = Chunk<Z>::N;
   // groups of one, four or eight chunks, as many as the keys that the threads hold
@@ -638,12 +646,12 @@ template <typename Z> void launch_forward(LogprobArgs a, hipStream_t s) {
   }
   a.parts = nullptr;
   if (a.k == 0) {
-    if (a.rows > 256 || a.vocab <= 256 * 8 * N) launch_rows<Z, 256, false>(a, 0, s);
+    if (a.rows > 256 || a.vocab <= 256 * KEYS * N) launch_rows<Z, 256, false>(a, 0, s);
     else launch_rows<Z, 1024, false>(a, 0, s);
     return;
   }
   const bool small = a.k <= 256 && a.vocab <= 256 * KEYS * N * 8;
-  if (small && (a.rows > 256 || a.vocab <= 256 * 8 * N)) launch_rows<Z, 256, true>(a, groups(256, a.vocab), s);
+  if (small && (a.rows > 256 || a.vocab <= 256 * KEYS * N)) launch_rows<Z, 256, true>(a, groups(256, a.vocab), s);
   else launch_rows<Z, 1024, true>(a, groups(1024, a.vocab), s);
 }
 
