@@ -534,8 +534,8 @@ int dion_mxfp4_dequantize(const uint8_t* q, int64_t ldq, const uint8_t* scale, i
  *   out[i][j] = sum_l a[i][l] b[j][l] + bias[j]
  * a: m x k activations, b: n x k weights (output channels as rows), any codes
  * and scales; k even, up to 2^22 (codes of an odd number of columns count one
- * more).  The products are exact and summed in fp32, in an order fixed by m, n
- * and k.  bias, out and the workspace as of dion_int8_linear; the workspace
+ * more).  The products are exact and summed in fp32, in an order fixed by m, n,
+ * k and whether all rows lie at multiples of 16 bytes.  bias, out and the workspace as of dion_int8_linear; the workspace
  * also holds copies of rows that are not whole multiples of 16 bytes, the
  * scales' among them (k not a multiple of 512), when m > 16. */
 size_t dion_mxfp4_linear_workspace_size(const uint8_t* a, int64_t lda, const uint8_t* a_scale, int64_t ldsa,
@@ -548,7 +548,7 @@ int dion_mxfp4_linear(const uint8_t* a, int64_t lda, const uint8_t* a_scale, int
 
 /* Log probabilities of given tokens, with the entropy and the top
  * alternatives.  For each row, with logits z (vocab values of `dtype`), a
- * token t and temperature T > 0:
+ * token t and temperature T (2^-126 at least):
  *   q = softmax(z / T)     logprob = log q_t     entropy = -sum_j q_j log q_j
  *   tokens       rows of token_bytes 4 or 8, or NULL (logprob is not written).
  *                A token outside [0, vocab) is left out: logprob 0

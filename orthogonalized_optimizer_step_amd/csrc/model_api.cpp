@@ -3,6 +3,7 @@
 // and the launches as profiled phases.
 #include <hip/hip_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 #include <string>
 
@@ -230,7 +231,7 @@ struct LogprobCheck : Check {
   LogprobCheck(const LogprobArgs& a, int dtype, int tok_bytes) {
     need(valid_dtype(dtype), "unknown logits dtype");
     need(!a.tok || tok_bytes == 4 || tok_bytes == 8, "tokens have 4 or 8 bytes");
-    need(std::isfinite(a.temp) && a.temp > 0.f, "temperature must be finite and positive");
+    need(std::isfinite(a.temp) && a.temp >= FLT_MIN, "temperature must be finite and 2^-126 at least");   // 1 / T is finite
     check_rows(*this, a.rows, a.vocab, "vocab must be positive");
     if (a.vocab > (1 << 30)) fail(DION_E_UNSUPPORTED, "more than 2^30 logits a row");
     if (code != DION_OK) return;

@@ -18,7 +18,8 @@
 // row 8 (e / 4) + 4 (l / 32) + e % 4 of the first operand and row l % 32 of
 // the second, of the other row 4 (l / 16) + e and row l % 16.  b goes first,
 // so that a lane holds four consecutive channels of one token.  Products are
-// exact, sums are fp32; their order depends on the sizes alone.
+// exact, sums are fp32; their order depends on the sizes and on whether rows
+// lie at multiples of 16 bytes.
 #include <algorithm>
 
 #include "mma_device.h"
@@ -48,7 +49,6 @@ template <int LANES> __device__ __forceinline__ uint32_t block_max(uint32_t v) {
 // rows along x, the rest of long rows along y.  8192 x 4096 bf16 (us): codes in
 // ROWS = 2 19.8, in 4 21.6, in 1 20.0; values in 4 16.7 past the caches, 21.5
 // through them.
-
 template <typename T>
 __global__ __launch_bounds__(256) void k_mxfp4_quantize(MxCodesArgs a, int tx) {
   typedef Chunk<T> C;

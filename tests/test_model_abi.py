@@ -124,7 +124,7 @@ def test_logprobs_refusals():
 
     common = ((dict(z=None), INVAL), (dict(rows=-1), INVAL), (dict(vocab=0), INVAL), (dict(dt=3), INVAL),
               (dict(tb=2), INVAL), (dict(temp=0.0), INVAL), (dict(temp=-1.0), INVAL), (dict(temp=float("nan")), INVAL),
-              (dict(temp=float("inf")), INVAL), (dict(ldz=499), INVAL), (dict(z=A + 1), INVAL), (dict(t=B + 4), INVAL),
+              (dict(temp=float("inf")), INVAL), (dict(temp=1e-39), INVAL), (dict(ldz=499), INVAL), (dict(z=A + 1), INVAL), (dict(t=B + 4), INVAL),
               (dict(vocab=(1 << 30) + 1, ldz=1 << 31), UNSUPPORTED), (dict(rows=(1 << 40) + 1), UNSUPPORTED))
     for f in (fwd, back):
         for bad, code in common:
