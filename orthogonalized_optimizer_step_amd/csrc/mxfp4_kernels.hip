@@ -375,7 +375,12 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mxfp4_mma(MxArgs g, float* par
     }
     return;
   }
-  __syncthreads();   // the stages are free: each wave stages 32 rows of its output at a time
+  // The stages are free: each wave stages 32 rows of its output at a time, and
+  // writes them past the caches, which the operands and the next call's inputs
+  // have more use for (8192 x 14336 x 4096 with a's codes before it: 308 us
+  // through them, 288 past them; 2048 x 4096 x 4096 with a norm of it behind 38.6
+  // and 37.9).
+  __syncthreads();
 
   O* st = (O*)smem + wave * 32 * SROW;
   const int64_t cbase = n0 + wn * TN;
@@ -403,7 +408,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mxfp4_mma(MxArgs g, float* par
       if (orow < g.m && col < g.n) {
         const O* s = st + rr * SROW + c;
         O* o = (O*)g.out + orow * g.ldo + col;
-        if (col + OV <= g.n) *(intx4u*)o = *(const intx4*)s;
+        if (col + OV <= g.n) __builtin_nontemporal_store(*(const intx4*)s, (intx4u*)o);
         else
           for (int e = 0; col + e < g.n; ++e) o[e] = s[e];
       }
