@@ -381,7 +381,8 @@ int dion_apply_batched(const float* const* Q, const void* const* X, void* const*
 /* ---- Operators of a training step around the optimizer ------------------
  * What a distillation step needs beside it: a teacher that runs in 8 bits
  * (norm with 8-bit output, 8-bit product), the student's norm with its
- * gradient, and the loss on the teacher's top logits with its gradient.
+ * gradient, and the loss on the teacher's top logits with its gradient; then
+ * layer norms, a teacher in 4-bit floating point, and log probabilities.
  *
  * Conventions (beside those above): matrices are row-major single device
  * pointers with a row stride in elements (ld >= the row length; any
@@ -520,11 +521,10 @@ int dion_layernorm_backward(const void* dy, int64_t lddy, const void* h, int64_t
  *   q       rows of ceil(cols / 2) bytes (a missing last code is written as 0)
  *   scale   rows of ceil(cols / 32) bytes
  * both with a stride in bytes, at any alignment; cols up to 2^30.
- * dion_mxfp4_quantize takes
- * the least scale 2^e (e from -127 on) with max|x| < 7 2^e, and the nearest
- * code, ties to the even one; a block of 32 that holds an infinity or a NaN
- * gets the scale 255 and codes 0.  dion_mxfp4_dequantize writes the values,
- * rounded to `dtype`. */
+ * dion_mxfp4_quantize takes the least scale 2^e (e from -127 on) with max|x| <
+ * 7 2^e, and the nearest code, ties to the even one; a block of 32 that holds
+ * an infinity or a NaN gets the scale 255 and codes 0.  dion_mxfp4_dequantize
+ * writes the values, rounded to `dtype`. */
 int dion_mxfp4_quantize(const void* x, int64_t ldx, uint8_t* q, int64_t ldq, uint8_t* scale, int64_t lds, int64_t rows,
                         int32_t cols, int32_t dtype, void* stream);
 int dion_mxfp4_dequantize(const uint8_t* q, int64_t ldq, const uint8_t* scale, int64_t lds, void* y, int64_t ldy,
@@ -574,8 +574,8 @@ int dion_token_logprobs(const void* logits, int64_t ldz, const void* tokens, flo
  * its entropy (rows floats; NULL: 0):
  *   d z_j = (gl ([j = t] - q_j) - ge q_j (log q_j + entropy)) / T
  * without the first term where the token is left out.  A row in which neither
- * term is left (gl and ge 0) has gradient 0 whatever its logits hold, and so has a row of
- * -infinity alone.  dlogits may be the logits in place. */
+ * term is left (gl and ge 0) has gradient 0 whatever its logits hold, and so
+ * has a row of -infinity alone.  dlogits may be the logits in place. */
 int dion_token_logprobs_backward(const float* grad_logprob, const float* grad_entropy, const void* logits, int64_t ldz,
                                  const float* stats, const void* tokens, void* dlogits, int64_t ldd, int64_t rows,
                                  int32_t vocab, int32_t dtype, int32_t token_bytes, float temperature, void* stream);

@@ -51,7 +51,7 @@ EXPORTS = (
     "dion_distill_topk_step",
     "dion_layernorm", "dion_layernorm_backward_workspace_size", "dion_layernorm_backward", "dion_mxfp4_quantize",
     "dion_mxfp4_dequantize", "dion_mxfp4_linear_workspace_size", "dion_mxfp4_linear", "dion_token_logprobs_workspace_size",
-    "dion_token_logprobs",    "dion_token_logprobs_backward",
+    "dion_token_logprobs", "dion_token_logprobs_backward",
 )
 
 

@@ -13,7 +13,9 @@
 //
 // A row is read once into registers, CH 16-byte chunks by each of its NT (16
 // to 1024) threads (chunk i of thread t at element (i NT + t) N), as the RMS
-// norm's are.  All of it is bound by memory.
+// norm's are.  All of it is bound by memory: 16384 x 768 bf16 with the residual
+// takes 23 us (4.4 TB/s; a copy on the card reaches 6.2), back 19 (4.0) and 3.9
+// for the join of the columns' sums; 8192 x 4096 46 to 49 (5.6) and 57.
 #include <algorithm>
 
 #include "model_internal.h"
@@ -168,7 +170,8 @@ __global__ __launch_bounds__(1024) void k_layernorm_long(LayerNormArgs a, bool w
 // chunks are asked for before this row's dx is written, and the terms of
 // dweight and dbias stay in registers until the end: one partial sum of each
 // for each block, in the order of its rows, joined over blocks by
-// k_layernorm_join.
+// k_layernorm_join.  64 threads with two chunks each hold more than 128
+// registers, and spill at the bound of the others.
 template <typename T, int NT, int CH>
 __global__ __launch_bounds__(block_of(NT), NT == 64 && CH == 2 ? 1 : 4) void k_layernorm_backward(LayerNormBackArgs a, bool w32) {
   typedef Chunk<T> C;

@@ -10,6 +10,11 @@
 // of it there is.  Where a factor is u itself it is -200 (in powers of two) at
 // least: below that exp(u) is 0 in fp32, and so is the product (u = -inf of a
 // masked entry among them).
+//
+// Reading bounds long batches: 8192 x 128256 bf16 take 355 us without
+// alternatives (5.9 TB/s; 5.8 is what a pass that only reads reaches in order),
+// 381 to 396 with 64 of them; the gradient of 4096 x 50257 164 to 174 (4.7 to
+// 5.0 TB/s read and written).
 #include <algorithm>
 
 #include "model_internal.h"
