@@ -60,14 +60,20 @@ template <bool FAR> struct Sums {
     m = other;
     r = o;
   }
+  // N elements, summed by themselves before they join the others: a thread that
+  // holds a likely token has an s near 1, and one exponential after another
+  // would lose what it has below half a unit of that, always downwards.
   // CLAMP: for chunks with elements so far below m that v would be -inf
   template <bool CLAMP, int N> __device__ __forceinline__ void add(const float* z, float c) {
+    float ps, pw;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float v = FAR ? (z[i] - m) * c : fmaf(z[i], c, -r), e = exp2_fast(v);
-      s += e;
-      w += e * (FAR || CLAMP ? factor(v) : v);
+      const float v = FAR ? (z[i] - m) * c : fmaf(z[i], c, -r), e = exp2_fast(v), ev = e * (FAR || CLAMP ? factor(v) : v);
+      ps = i ? ps + e : e;
+      pw = i ? pw + ev : ev;
     }
+    s += ps;
+    w += pw;
   }
   // over the block, the same in every thread
   template <int NT> __device__ __forceinline__ void join(float c, float (*red)[NT / 64]) {
@@ -252,10 +258,14 @@ template <typename Z> __device__ __forceinline__ int64_t token_of(const LogprobA
 // come before anything in the rest.  Then the same for parts of those groups,
 // down to single logits.  A few rows are shared between gridDim.y blocks each,
 // whose sums and alternatives k_logprobs_join puts together.
+// Eight chunks ahead; six where 1024 threads look for alternatives, whose 128
+// registers hold no more (bf16, six and eight with ten of them spilled, us: 256 x
+// 50257 with 20 17.3 and 19.6, 64 x 128256 with 20 18.3 and 19.2, 600 x 50257 with
+// 500 110 and 115; fp32 20.6 either way).
 template <typename Z, int NT, bool TOP>
 __global__ __launch_bounds__(NT, 4) void k_logprobs(LogprobArgs a, int lg) {
   typedef Chunk<Z> C;
-  constexpr int N = C::N, AHEAD = 8, STEP = NT * N;
+  constexpr int N = C::N, AHEAD = NT == 1024 && TOP ? 6 : 8, STEP = NT * N;
   __shared__ float red[3][NT / 64];
   __shared__ TopShared<TOP ? NT : 64> sh;
   const float c = LOG2E / a.temp;
@@ -299,13 +309,8 @@ __global__ __launch_bounds__(NT, 4) void k_logprobs(LogprobArgs a, int lg) {
         }
       }
       if (top > S.m) S.to(top, c);
-      if (!(fmaf(low, c, -S.r) > -200.f)) {
-        S.template add<true, N>(f[0], c);
-        S.template add<true, N>(f[1], c);
-      } else {
-        S.template add<false, N>(f[0], c);
-        S.template add<false, N>(f[1], c);
-      }
+      if (!(fmaf(low, c, -S.r) > -200.f)) S.template add<true, 2 * N>(f[0], c);
+      else S.template add<false, 2 * N>(f[0], c);
     };
     const int rest = vocab - whole * STEP;   // of the row, a chunk of some threads
     const uintx4 last = rest ? C::load(z + (int64_t)whole * STEP, min(t * N, rest), rest, NEG) : none4;
