@@ -6,8 +6,12 @@
 //   logprob = u_t - log s      entropy = -sum q_j log q_j = log s - sum exp(u_j) u_j / s
 //   top alternatives: the k largest logits, equal ones by their index
 //   dz_j = (gl ([j = t] - q_j) - ge q_j (log q_j + entropy)) / T
-// Both terms of the entropy are at least 0, so nothing cancels however little
-// of it there is.  Where a factor is u itself it is -200 (in powers of two) at
+// Both terms of the entropy are at least 0 as they are computed too (s at least
+// 1, its second sum at most 0), so nothing cancels between them, no entropy is
+// negative and no log probability above 0.  s holds what lies beside the largest
+// logit to half a unit of 1 for each addition that its 1 takes part in: a few
+// 2^-24, absolute, is what log s and the entropy of a nearly certain row are off
+// by.  Where a factor is u itself it is -200 (in powers of two) at
 // least: below that exp(u) is 0 in fp32, and so is the product (u = -inf of a
 // masked entry among them).
 //
@@ -92,11 +96,13 @@ template <bool FAR> struct Sums {
     s = row_reduce<W>(s, 0.f, Add());
     w = row_reduce<W>(w, 0.f, Add());
     lds_barrier();   // red may be written again
-    if (!FAR) {   // every v is larger by what R was rounded by
-      const float off = fmaf(m, c, -r), f = exp2_fast(-off);
-      w = (w - off * s) * f;
-      s *= f;
+    if (!FAR) {   // every v is larger by what R was rounded by, the largest one's 0 too
+#pragma clang fp contract(off)   // off s rounds as the largest one's part of w did
+      const float off = fmaf(m, c, -r), f = exp2_fast(off);
+      w = (w - off * s) / f;
+      s /= f;   // f is a term of s and no term is negative: 1 at least, exactly 1 of one logit alone
     }
+    w = w > 0.f ? 0.f : w;   // of terms that are 0 at most (NaN stays)
   }
   __device__ __forceinline__ bool wide(float c) const { return !(fabsf(m * c) < WIDE); }
 };

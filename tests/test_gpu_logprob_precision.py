@@ -59,3 +59,27 @@ def test_sums_are_as_exact_as_elementary_operations_in_fp32(dion, rows, vocab, t
     for what, a, p, w in zip(("log of the sum", "logprob", "entropy"), got, plain, want):
         far, limit = rms(torch.cat(a), w), rms(p, w)
         assert far <= 1.25 * limit, what
+
+
+@pytest.mark.parametrize("temp", [0.3, 0.5, 0.7, 1.0, 2.0])
+@pytest.mark.parametrize("rows,vocab", [(40, 1000), (300, 1000), (300, 50257), (40, 128256), (8, 128256)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_signs_of_certain_and_nearly_certain_rows(dion, rows, vocab, temp, dtype):
+    """No log probability is above 0 and no entropy below it.  A row with one finite logit (or equal ones alone) has them
+    exactly: 0 and 0, whatever the logit."""
+    g = gen(rows + vocab)
+    z = torch.randn((rows, vocab), generator=g, device="cuda") * 2
+    at = torch.randint(vocab, (rows,), generator=g, device="cuda")
+    peak = torch.randn((rows,), generator=g, device="cuda") * 12 + 3
+    kind = torch.arange(rows, device="cuda") % 4
+    z[kind == 0] = -float("inf")               # one finite logit
+    z[kind == 1] = torch.finfo(dtype).min      # one above the type's lowest value
+    z[kind == 2] -= 60                         # nearly certain
+    z[torch.arange(rows, device="cuda"), at] = torch.where(kind == 3, z[torch.arange(rows, device="cuda"), at], peak)
+    z = z.to(dtype)
+    lp, ent, _ = dion.token_logprobs(z, at, temperature=temp)
+    top, index, lp2, ent2 = dion.top_logprobs(z, 5, at, temperature=temp)
+    for l, e in ((lp, ent), (lp2, ent2)):
+        assert (l <= 0).all() and (e >= 0).all()
+        assert not l[kind < 2].any() and not e[kind < 2].any()
+    assert (top <= 0).all() and not top[kind < 2, 0].any() and torch.equal(index[kind < 2, 0], at[kind < 2])
