@@ -3,8 +3,10 @@ gradient, microscaled 4-bit floating point (codes, values, product), and the log
 entropy, top alternatives and gradient.
 
 Thin binding over the C ABI (include/dion.h), with the conventions of train_ops: tensors on the current GPU, leading
-dimensions that flatten into rows, ``stream``.  ``layer_norm`` and ``log_probs`` are the same operators as torch
-autograd functions.
+dimensions that flatten into rows, ``stream``.  A ``stream`` that is given first waits for what the current one holds
+(unless it is being captured, when its caller joins the two), so that tensors made there are whole when it reads them;
+whoever wants the two to overlap makes it the current one, with ``torch.cuda.stream``, and orders them as needed.
+``layer_norm`` and ``log_probs`` are the same operators as torch autograd functions.
 """
 from __future__ import annotations
 
@@ -15,6 +17,19 @@ from .train_ops import (_CODE, _F32, _beside, _code, _device, _dense, _fail, _gr
                         _new_like, _once, _ptr, _rows, _same, _scratch, _used, _vector, _workspace)
 
 
+def _behind(stream):
+    """a given stream, behind the current one"""
+    if stream is None:
+        return
+    current = torch.cuda.current_stream()
+    if stream == current:
+        return
+    with torch.cuda.stream(stream):
+        captured = torch.cuda.is_current_stream_capturing()
+    if not captured:
+        stream.wait_stream(current)
+
+
 # ---------------------------------------------------------------- layer norm
 def layernorm(x, weight, bias=None, residual=None, eps=1e-5, stream=None):
     """Layer norm of the rows of ``x + residual``: returns (y, h, mean, rstd).
@@ -23,6 +38,7 @@ def layernorm(x, weight, bias=None, residual=None, eps=1e-5, stream=None):
     (fp32, one for each row) and ``h`` are what ``layernorm_backward`` needs.  ``weight`` and ``bias``: x's type or
     fp32, both the same."""
     dev = _device(x, "x")
+    _behind(stream)
     rows, cols, ldx = _matrix(x, "x")
     code = _code(x.dtype, "x")
     ldr = 0 if residual is None else _same(residual, "residual", x, dev)
@@ -48,6 +64,7 @@ def layernorm_backward(dy, h, weight, mean, rstd, dh=None, bias=True, workspace=
     ``dh`` is the gradient that reaches h itself along the residual stream; dx is the gradient of x and of the residual
     alike."""
     dev = _device(h, "h")
+    _behind(stream)
     rows, cols, ldh = _matrix(h, "h")
     code = _code(h.dtype, "h")
     lddy = _same(dy, "dy", h, dev)
@@ -91,6 +108,7 @@ def mxfp4_quantize(x, stream=None):
     Both uint8: two codes a byte, the even element in the low half, and biased exponents (255 where a block holds an
     infinity or a NaN).  The weights of a product, once; the activations before each."""
     dev = _device(x, "x")
+    _behind(stream)
     rows, cols, ldx = _matrix(x, "x")
     code = _code(x.dtype, "x")
     held, blocks = (cols + 1) // 2, (cols + 31) // 32
@@ -107,6 +125,7 @@ def mxfp4_quantize(x, stream=None):
 def mxfp4_dequantize(q, scale, dtype=torch.bfloat16, cols=None, stream=None):
     """The values that 4-bit codes stand for.  ``cols``: the number of columns where it is odd."""
     dev = _device(q, "q")
+    _behind(stream)
     rows, ldq, lds, cols = _codes(q, scale, "q", cols, dev)
     code = _code(dtype, "dtype")
     y = _new((*q.shape[:-1], cols), dtype, q, stream)
@@ -122,6 +141,7 @@ def mxfp4_linear(a, a_scale, b, b_scale, bias=None, out_dtype=torch.bfloat16, wo
     """a (tokens x k) times b (channels x k) transposed, both 4-bit codes with their scales, and an optional bias; the
     products are exact, the sums fp32."""
     dev = _device(a, "a")
+    _behind(stream)
     _beside(b, "b", dev)
     m, lda, ldsa, k = _codes(a, a_scale, "a", None, dev)
     n, ldb, ldsb, kb = _codes(b, b_scale, "b", None, dev)
@@ -146,6 +166,7 @@ def mxfp4_linear(a, a_scale, b, b_scale, bias=None, out_dtype=torch.bfloat16, wo
 # ----------------------------------------------------------- log probabilities
 def _logprob_inputs(logits, tokens, stream):
     dev = _device(logits, "logits")
+    _behind(stream)
     rows, vocab, ldz = _matrix(logits, "logits")
     code = _code(logits.dtype, "logits")
     if tokens is None:
