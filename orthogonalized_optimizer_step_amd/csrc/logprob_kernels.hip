@@ -79,6 +79,13 @@ template <bool FAR> struct Sums {
     s += ps;
     w += pw;
   }
+  // all of it into other sums, which go on
+  __device__ __forceinline__ void into(Sums& other, float c) {
+    other.to(m, c);   // (m is the largest so far)
+    other.s += s;
+    other.w += w;
+    s = w = 0.f;
+  }
   // over the block, the same in every thread
   template <int NT> __device__ __forceinline__ void join(float c, float (*red)[NT / 64]) {
     constexpr int W = NT / 64;
@@ -98,9 +105,11 @@ template <bool FAR> struct Sums {
     lds_barrier();   // red may be written again
     if (!FAR) {   // every v is larger by what R was rounded by, the largest one's 0 too
 #pragma clang fp contract(off)   // off s rounds as the largest one's part of w did
-      const float off = fmaf(m, c, -r), f = exp2_fast(off);
-      w = (w - off * s) / f;
-      s /= f;   // f is a term of s and no term is negative: 1 at least, exactly 1 of one logit alone
+      const float off = fmaf(m, c, -r), f = exp2_fast(off), inv = __builtin_amdgcn_rcpf(f);   // f is near 1
+      w = (w - off * s) * inv;
+      // s / f: f is a term of s and no term is negative, so 1 at least, exactly 1 of one logit alone
+      const float q = s * inv;
+      s = fmaf(fmaf(-q, f, s), inv, q);
     }
     w = w > 0.f ? 0.f : w;   // of terms that are 0 at most (NaN stays)
   }
@@ -115,6 +124,11 @@ __device__ __forceinline__ uint32_t key_of(float z) {
   return (uint32_t)(u ^ (u >> 31 | (int)0x80000000));
 }
 __device__ __forceinline__ float value_of(uint32_t k) { return __uint_as_float(k ^ (k >> 31 ? 0x80000000u : ~0u)); }
+
+// Additions to one sum: those of rows with more (LONG below) go on in another
+// one, so that of 2^30 logits no sum has more than 1024 terms.  (Rows of 2^19
+// logits, the longest with alternatives, have 128 at most.)
+constexpr int RUN = 512;
 
 constexpr int KEYS = 16, SUB = 8;   // keys a thread holds: of a row's groups, of a level below
 
@@ -229,18 +243,24 @@ __device__ __forceinline__ void select(int used, int k, TopShared<NT>& sh, Put p
   lds_barrier();
 }
 
-// The rest of a row's chunks one by one, for sums by differences.
+// A row's chunks one by one, for sums by differences.
 template <typename Z, int NT>
 __device__ __forceinline__ void far_sums(const Z* z, int vocab, float temp, float c, Sums<true>& S) {
   typedef Chunk<Z> C;
   S.clear(temp, c);
-  for (int64_t j = threadIdx.x * C::N; j < vocab; j += NT * C::N) {
-    const uintx4 v = C::load(z, (int)j, vocab, NEG);
-    const float top = C::largest(S.m, v);
-    if (top > S.m) S.to(top, c);
-    float f[C::N];
-    C::unpack(v, f);
-    S.template add<true, C::N>(f, c);
+  Sums<true> part;
+  part.clear(temp, c);
+  int64_t j = threadIdx.x * C::N;
+  while (j < vocab) {
+    for (int i = 0; i < RUN && j < vocab; ++i, j += NT * C::N) {
+      const uintx4 v = C::load(z, (int)j, vocab, NEG);
+      const float top = C::largest(part.m, v);
+      if (top > part.m) part.to(top, c);
+      float f[C::N];
+      C::unpack(v, f);
+      part.template add<true, C::N>(f, c);
+    }
+    part.into(S, c);
   }
 }
 
@@ -268,7 +288,7 @@ template <typename Z> __device__ __forceinline__ int64_t token_of(const LogprobA
 // registers hold no more (bf16, six and eight with ten of them spilled, us: 256 x
 // 50257 with 20 17.3 and 19.6, 64 x 128256 with 20 18.3 and 19.2, 600 x 50257 with
 // 500 110 and 115; fp32 20.6 either way).
-template <typename Z, int NT, bool TOP>
+template <typename Z, int NT, bool TOP, bool LONG>
 __global__ __launch_bounds__(NT, 4) void k_logprobs(LogprobArgs a, int lg) {
   typedef Chunk<Z> C;
   constexpr int N = C::N, AHEAD = NT == 1024 && TOP ? 6 : 8, STEP = NT * N;
@@ -328,7 +348,9 @@ __global__ __launch_bounds__(NT, 4) void k_logprobs(LogprobArgs a, int lg) {
     uintx4 v[AHEAD];
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u) v[u] = fetch(u);
-    for (int i = 0; i < steps; i += AHEAD)
+    Sums<false> R;
+    if (LONG) R.clear(a.temp, c);
+    for (int i = 0; i < steps; i += AHEAD) {
 #pragma unroll
       for (int u = 0; u < AHEAD; u += 2) {
         if (i + u >= steps) break;
@@ -338,6 +360,12 @@ __global__ __launch_bounds__(NT, 4) void k_logprobs(LogprobArgs a, int lg) {
           v[u + 1] = fetch(i + u + 1 + AHEAD);
         }
       }
+      if (LONG && (i & (2 * RUN - 1)) == 2 * RUN - AHEAD) S.into(R, c);
+    }
+    if (LONG) {
+      S.into(R, c);
+      S = R;
+    }
     S.template join<NT>(c, red);
     float m = S.m, s = S.s, w = S.w;
     if (S.wide(c)) {   // rare: again, from the caches
@@ -637,7 +665,9 @@ int logprob_shares(int64_t rows, int vocab, int k, int& per) {
 template <typename Z, int NT, bool TOP>
 void launch_rows(const LogprobArgs& a, int lg, hipStream_t s) {
   const dim3 grid((unsigned)std::min<int64_t>(a.rows, 1 << 20), (unsigned)(a.parts ? a.shares : 1));
-  hipLaunchKernelGGL((k_logprobs<Z, NT, TOP>), grid, dim3(NT), 0, s, a, lg);
+  const bool runs = (a.parts ? a.per : a.vocab) > 2 * RUN * NT * Chunk<Z>::N;   // (TOP: never)
+  if (!TOP && runs) hipLaunchKernelGGL((k_logprobs<Z, NT, false, true>), grid, dim3(NT), 0, s, a, lg);
+  else hipLaunchKernelGGL((k_logprobs<Z, NT, TOP, false>), grid, dim3(NT), 0, s, a, lg);
 }
 
 // Threads of a row: 256, of which a CU holds eight rows, or 1024 where there is a

@@ -1,5 +1,7 @@
 """What the sums of the log probabilities keep: errors against 64 bits beside those of elementary fp32 operations, signs of
 log probabilities and entropies, and rows of very many logits."""
+import math
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -83,3 +85,36 @@ def test_signs_of_certain_and_nearly_certain_rows(dion, rows, vocab, temp, dtype
         assert (l <= 0).all() and (e >= 0).all()
         assert not l[kind < 2].any() and not e[kind < 2].any()
     assert (top <= 0).all() and not top[kind < 2, 0].any() and torch.equal(index[kind < 2, 0], at[kind < 2])
+
+
+@pytest.mark.parametrize("rows,vocab,dtype", [(257, 1 << 20, torch.bfloat16), (257, (1 << 21) + 5, torch.float32),
+                                              (40, 1 << 24, torch.bfloat16), (2, 1 << 28, torch.bfloat16),
+                                              (1, (1 << 28) + 4097, torch.float32), (1, 1 << 30, torch.bfloat16),
+                                              (257, (1 << 26) + 9, torch.bfloat16), (40, 1 << 28, torch.bfloat16)])
+@pytest.mark.parametrize("far", [0.0, 3e5])
+def test_sums_of_very_many_equal_terms(dion, rows, vocab, dtype, far):
+    """One logit above all others, which are equal: each of their terms rounds the same way wherever sums have the same
+    size.  s = 1 + (vocab - 1) exp(-d), entropy log s + (vocab - 1) exp(-d) d / s.  An fp32 sum in which no partial sum runs
+    over more than 1024 terms, and a term goes through 1024 additions of at most 2^-24 each, is off by at most 2^-14 of
+    itself, and its logarithm by as much; the second sum is off by as much of itself.  (Exponentials: 2^-22 of their own.)"""
+    if far and dtype != torch.float32:
+        pytest.skip("such logits are fp32 numbers only")   # 3e5 + d is one: a multiple of 2^-5
+    z = torch.full((rows, vocab), far, device="cuda", dtype=dtype)
+    t = torch.full((rows,), 3, device="cuda")
+    one = torch.ones(rows, device="cuda")
+    for d in (i / 16 for i in range(80, 257)):   # numbers of bf16, 16 at most
+        z[:, 3] = far + d
+        lp, ent, stats = dion.token_logprobs(z, t)
+        rest = (vocab - 1) * math.exp(-d)
+        s = 1 + rest
+        assert float((stats[:, 3].double() - math.log(s)).abs().max()) <= 2.0 ** -14 + 2.0 ** -21 * math.log(s), d
+        assert float((lp.double() + math.log(s)).abs().max()) <= 2.0 ** -14 + 2.0 ** -21 * math.log(s), d
+        want = math.log(s) + rest * d / s
+        assert float((ent.double() - want).abs().max()) <= 2.0 ** -14 * (1 + rest * d / s) + 2.0 ** -20 * want, d
+    # their gradient: of the token's logit 1 - 1 / s, which an error of 2^-14 s in s moves by 2^-14 / s; of the others -q
+    del lp, ent
+    grad = dion.token_logprobs_backward(one, None, z, stats, t)
+    u = torch.finfo(dtype).eps / 2
+    q = math.exp(-d) / s
+    assert float((grad[:, 3].double() - (1 - 1 / s)).abs().max()) <= u * (1 - 1 / s) + 2.0 ** -14 / s + 2.0 ** -23
+    assert float((grad[:, 4].double() + q).abs().max()) <= (u + 2.0 ** -13) * q
