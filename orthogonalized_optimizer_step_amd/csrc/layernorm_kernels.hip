@@ -54,6 +54,13 @@ template <int N> __device__ __forceinline__ void centre(float* s, float mean, in
   }
 }
 
+// sq: the mean of the squares about a mean that was off by `off`.  Squares
+// beyond fp32 leave 0: infinity less off's own, which is not rounded and so not
+// infinite with them.
+__device__ __forceinline__ float rstd_of(float sq, float off, float eps) {
+  return 1.f / sqrtf(fmaxf(fmaf(-off, off, sq), 0.f) + eps);
+}
+
 template <typename T, int NT, int CH>
 __global__ __launch_bounds__(block_of(NT), NT >= 256 && CH == 1 ? 8 : 4) void k_layernorm(LayerNormArgs a, bool w32) {
   typedef Chunk<T> C;
@@ -99,7 +106,7 @@ __global__ __launch_bounds__(block_of(NT), NT >= 256 && CH == 1 ? 8 : 4) void k_
     }
     row_sum2<NT>(off, sq, red[1]);
     off *= inv;
-    const float rstd = 1.f / sqrtf(fmaxf(sq * inv - off * off, 0.f) + a.eps);
+    const float rstd = rstd_of(sq * inv, off, a.eps);
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int j = (i * NT + t) * N;
@@ -148,7 +155,7 @@ __global__ __launch_bounds__(1024) void k_layernorm_long(LayerNormArgs a, bool w
     }
     row_sum2<1024>(off, sq, red[1]);
     off *= inv;
-    const float rstd = 1.f / sqrtf(fmaxf(sq * inv - off * off, 0.f) + a.eps);
+    const float rstd = rstd_of(sq * inv, off, a.eps);
     for (int j = threadIdx.x * N; j < a.cols; j += 1024 * N) {
       float s[N], w[N], b[N] = {};
       load(j, s);
