@@ -56,9 +56,10 @@ template <int N> __device__ __forceinline__ void centre(float* s, float mean, in
 
 // sq: the mean of the squares about a mean that was off by `off`.  Squares
 // beyond fp32 leave 0: infinity less off's own, which is not rounded and so not
-// infinite with them.
+// infinite with them.  NaN stays.
 __device__ __forceinline__ float rstd_of(float sq, float off, float eps) {
-  return 1.f / sqrtf(fmaxf(fmaf(-off, off, sq), 0.f) + eps);
+  const float var = fmaf(-off, off, sq);
+  return 1.f / sqrtf((var < 0.f ? 0.f : var) + eps);
 }
 
 template <typename T, int NT, int CH>

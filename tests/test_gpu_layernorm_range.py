@@ -45,3 +45,21 @@ def test_rows_whose_squares_overflow(dion, cols, dtype, size):
     dy, dh = randn(4, (6, cols), dtype), randn(5, (6, cols), dtype)
     dx, dw, db = dion.layernorm_backward(dy, h, w, mean, rstd, dh=dh)
     assert torch.equal(dx[[1, 4]], dh[[1, 4]]) and torch.isfinite(dw).all() and torch.isfinite(db).all()
+
+
+@pytest.mark.parametrize("cols", COLS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_statistics_of_rows_that_hold_no_number(dion, cols, dtype, bad):
+    """mean, rstd, y and dx of such a row are NaN, the others' are what they are without it."""
+    x = randn(1, (5, cols), dtype)
+    x[3, cols // 2] = bad
+    w, b, dy = randn(2, (cols,), dtype), randn(3, (cols,), dtype), randn(4, (5, cols), dtype)
+    y, h, mean, rstd = dion.layernorm(x, w, b)
+    assert torch.isnan(y[3]).all() and torch.isnan(rstd[3]) and not torch.isfinite(mean[3])
+    dx, _, _ = dion.layernorm_backward(dy, h, w, mean, rstd)
+    assert torch.isnan(dx[3]).all()
+    some = [0, 1, 2, 4]
+    cy, ch, cmean, crstd = dion.layernorm(x[some], w, b)
+    assert torch.equal(y[some], cy) and torch.equal(mean[some], cmean) and torch.equal(rstd[some], crstd)
+    assert torch.equal(dx[some], dion.layernorm_backward(dy[some], ch, w, cmean, crstd)[0])
