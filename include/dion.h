@@ -507,12 +507,18 @@ int dion_layernorm(const void* x, int64_t ldx, const void* residual, int64_t ldr
  *   dweight_j = sum over rows of dy_j u_j     dbias_j = sum over rows of dy_j
  * h, mean and rstd are the forward's (h = x without a residual); dh and dx as
  * of dion_rmsnorm_backward.  dweight and dbias (cols values of weight_dtype;
- * dbias may be NULL) are summed in a fixed order. */
+ * dbias may be NULL) are summed in a fixed order.  dion_layernorm_backward_dx
+ * writes dx alone, as for a norm whose weights are not trained: no sums, no
+ * workspace. */
 size_t dion_layernorm_backward_workspace_size(int64_t rows, int32_t cols, int32_t dtype);
 int dion_layernorm_backward(const void* dy, int64_t lddy, const void* h, int64_t ldh, const void* weight,
                             const float* mean, const float* rstd, const void* dh, int64_t lddh, void* dx, int64_t lddx,
                             void* dweight, void* dbias, int64_t rows, int32_t cols, int32_t dtype, int32_t weight_dtype,
                             void* workspace, size_t workspace_bytes, void* stream);
+int dion_layernorm_backward_dx(const void* dy, int64_t lddy, const void* h, int64_t ldh, const void* weight,
+                               const float* mean, const float* rstd, const void* dh, int64_t lddh, void* dx,
+                               int64_t lddx, int64_t rows, int32_t cols, int32_t dtype, int32_t weight_dtype,
+                               void* stream);
 
 /* Microscaled 4-bit floating point.  A code is a sign, two bits of exponent
  * and one of mantissa (0, 0.5, 1, 1.5, 2, 3, 4, 6 in the order of the codes 0

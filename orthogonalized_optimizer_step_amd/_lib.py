@@ -49,7 +49,8 @@ EXPORTS = (
     "dion_rmsnorm_backward_workspace_size", "dion_rmsnorm_backward", "dion_int8_linear_workspace_size",
     "dion_int8_linear", "dion_distill_topk_workspace_size", "dion_distill_topk", "dion_distill_topk_backward",
     "dion_distill_topk_step",
-    "dion_layernorm", "dion_layernorm_backward_workspace_size", "dion_layernorm_backward", "dion_mxfp4_quantize",
+    "dion_layernorm", "dion_layernorm_backward_workspace_size", "dion_layernorm_backward", "dion_layernorm_backward_dx",
+    "dion_mxfp4_quantize",
     "dion_mxfp4_dequantize", "dion_mxfp4_linear_workspace_size", "dion_mxfp4_linear", "dion_token_logprobs_workspace_size",
     "dion_token_logprobs", "dion_token_logprobs_backward",
 )
@@ -162,6 +163,8 @@ def _load():
     lib.dion_layernorm_backward.argtypes = (mat + mat + [vp, vp, vp] + mat + mat +
                                             [vp, vp, i64, i32, i32, i32, vp, sz, vp])
     lib.dion_layernorm_backward.restype = ctypes.c_int
+    lib.dion_layernorm_backward_dx.argtypes = mat + mat + [vp, vp, vp] + mat + mat + [i64, i32, i32, i32, vp]
+    lib.dion_layernorm_backward_dx.restype = ctypes.c_int
     lib.dion_mxfp4_quantize.argtypes = mat + mat + mat + [i64, i32, i32, vp]
     lib.dion_mxfp4_quantize.restype = ctypes.c_int
     lib.dion_mxfp4_dequantize.argtypes = lib.dion_mxfp4_quantize.argtypes

@@ -178,7 +178,7 @@ __global__ __launch_bounds__(1024) void k_layernorm_long(LayerNormArgs a, bool w
 // chunks are asked for before this row's dx is written, and the terms of
 // dweight and dbias stay in registers until the end: one partial sum of each
 // for each block, in the order of its rows, joined over blocks by
-// k_layernorm_join.  64 threads with two chunks each hold more than 128
+// k_layernorm_join (neither is written where no dweight is asked for).  64 threads with two chunks each hold more than 128
 // registers, and spill at the bound of the others.
 template <typename T, int NT, int CH>
 __global__ __launch_bounds__(block_of(NT), NT == 64 && CH == 2 ? 1 : 4) void k_layernorm_backward(LayerNormBackArgs a, bool w32) {
@@ -286,7 +286,7 @@ __global__ __launch_bounds__(block_of(NT), NT == 64 && CH == 2 ? 1 : 4) void k_l
         }
     }
   };
-  write(dw, a.partial + (int64_t)blockIdx.x * a.cols);
+  if (a.dweight) write(dw, a.partial + (int64_t)blockIdx.x * a.cols);
   if (a.dbias) write(db, a.partial + (int64_t)(a.parts + blockIdx.x) * a.cols);
 }
 
@@ -424,11 +424,12 @@ template <typename T> void launch_back(const LayerNormBackArgs& a, bool w32, hip
     else {
       const unsigned gx = (unsigned)((a.cols + 255) / 256);
       // the sums first: dx may be written over dy or dh
-      hipLaunchKernelGGL((k_layernorm_dw_long<T>), dim3(gx, (unsigned)a.parts), dim3(256), 0, s, a);
+      if (a.dweight) hipLaunchKernelGGL((k_layernorm_dw_long<T>), dim3(gx, (unsigned)a.parts), dim3(256), 0, s, a);
       hipLaunchKernelGGL((k_layernorm_dx_long<T>), dim3((unsigned)std::min<int64_t>(a.rows, 1 << 20)), dim3(1024), 0, s, a,
                          w32);
     }
   }
+  if (!a.dweight) return;
   const dim3 grid((unsigned)((a.cols + 31) / 32), a.dbias ? 2 : 1);
   if (w32) hipLaunchKernelGGL((k_layernorm_join<float>), grid, dim3(1024), 0, s, a);
   else hipLaunchKernelGGL((k_layernorm_join<T>), grid, dim3(1024), 0, s, a);

@@ -12,6 +12,49 @@
 
 using namespace dion;
 
+namespace {
+
+// The gradient with (sums) and without those of the weight and the bias.
+int layernorm_backward_call(LayerNormBackArgs a, bool sums, int32_t dtype, int32_t weight_dtype, size_t workspace_bytes,
+                            hipStream_t st) {
+  Check c;
+  const int64_t rows = a.rows;
+  const int32_t cols = a.cols;
+  c.need(valid_dtype(dtype), "unknown dtype");
+  c.need(weight_dtype == dtype || weight_dtype == DION_FP32, "the weight must be of x's type or fp32");
+  check_rows(c, rows, cols, "cols must be positive");
+  if (cols > kLayerNormMaxCols) c.fail(DION_E_UNSUPPORTED, "more than 65536 columns");
+  if (c.code != DION_OK) return c.done();
+  const int64_t es = esize(dtype), ws = esize(weight_dtype);
+  const View vdy{a.dy, a.lddy, rows, cols, es, "dy"}, vh{a.h, a.ldh, rows, cols, es, "h"},
+      vw{a.weight, cols, 1, cols, ws, "weight"}, vm{a.mean, 1, rows, 1, 4, "mean"}, vr{a.rstd, 1, rows, 1, 4, "rstd"},
+      vdh{a.dh, a.lddh, rows, cols, es, "dh"}, vdx{a.dx, a.lddx, rows, cols, es, "dx"},
+      vdw{a.dweight, cols, 1, cols, ws, "dweight"}, vdb{a.dbias, cols, 1, cols, ws, "dbias"};
+  for (const View& v : {vdy, vh, vw, vm, vr, vdx}) check_view(c, v);
+  if (sums) check_view(c, vdw);
+  if (a.dh) check_view(c, vdh);
+  if (a.dbias) check_view(c, vdb);
+  for (const View& in : {vdy, vdh}) check_apart(c, vdx, in, true);
+  for (const View& in : {vh, vw, vm, vr, vdw, vdb}) check_apart(c, vdx, in);
+  for (const View& out : {vdw, vdb})
+    for (const View& in : {vdy, vdh, vh, vw, vm, vr}) check_apart(c, out, in);
+  check_apart(c, vdw, vdb);
+  if (sums) {
+    check_workspace(c, a.partial, workspace_bytes, dion_layernorm_backward_workspace_size(rows, cols, dtype));
+    if (c.code == DION_OK) {
+      const View vws{a.partial, (int64_t)workspace_bytes, 1, (int64_t)workspace_bytes, 1, "workspace"};
+      for (const View& in : {vdy, vdh, vh, vw, vm, vr, vdx, vdw, vdb}) check_apart(c, vws, in);
+    }
+  }
+  if (c.code != DION_OK || (rows == 0 && !sums)) return c.done();
+  a.parts = layernorm_back_parts(rows, cols, dtype);
+  const double n = (double)rows * cols;
+  return run_phase("layernorm_backward", "dion::k_layernorm_backward", 14.0 * n, n * es * (3 + (a.dh ? 1 : 0)), st,
+                   [&]() { launch_layernorm_backward(dtype, weight_dtype, a, st); });
+}
+
+}  // namespace
+
 extern "C" {
 
 int dion_layernorm(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight, const void* bias,
@@ -65,37 +108,20 @@ int dion_layernorm_backward(const void* dy, int64_t lddy, const void* h, int64_t
                             void* dweight, void* dbias, int64_t rows, int32_t cols, int32_t dtype, int32_t weight_dtype,
                             void* workspace, size_t workspace_bytes, void* stream) {
   return guarded([&]() {
-    Check c;
-    c.need(valid_dtype(dtype), "unknown dtype");
-    c.need(weight_dtype == dtype || weight_dtype == DION_FP32, "the weight must be of x's type or fp32");
-    check_rows(c, rows, cols, "cols must be positive");
-    if (cols > kLayerNormMaxCols) c.fail(DION_E_UNSUPPORTED, "more than 65536 columns");
-    if (c.code != DION_OK) return c.done();
-    const int64_t es = esize(dtype), ws = esize(weight_dtype);
-    const View vdy{dy, lddy, rows, cols, es, "dy"}, vh{h, ldh, rows, cols, es, "h"},
-        vw{weight, cols, 1, cols, ws, "weight"}, vm{mean, 1, rows, 1, 4, "mean"}, vr{rstd, 1, rows, 1, 4, "rstd"},
-        vdh{dh, lddh, rows, cols, es, "dh"}, vdx{dx, lddx, rows, cols, es, "dx"},
-        vdw{dweight, cols, 1, cols, ws, "dweight"}, vdb{dbias, cols, 1, cols, ws, "dbias"};
-    for (const View& v : {vdy, vh, vw, vm, vr, vdx, vdw}) check_view(c, v);
-    if (dh) check_view(c, vdh);
-    if (dbias) check_view(c, vdb);
-    for (const View& in : {vdy, vdh}) check_apart(c, vdx, in, true);
-    for (const View& in : {vh, vw, vm, vr, vdw, vdb}) check_apart(c, vdx, in);
-    for (const View& out : {vdw, vdb})
-      for (const View& in : {vdy, vdh, vh, vw, vm, vr}) check_apart(c, out, in);
-    check_apart(c, vdw, vdb);
-    check_workspace(c, workspace, workspace_bytes, dion_layernorm_backward_workspace_size(rows, cols, dtype));
-    if (c.code == DION_OK) {
-      const View vws{workspace, (int64_t)workspace_bytes, 1, (int64_t)workspace_bytes, 1, "workspace"};
-      for (const View& in : {vdy, vdh, vh, vw, vm, vr, vdx, vdw, vdb}) check_apart(c, vws, in);
-    }
-    if (c.code != DION_OK) return c.done();
-    const hipStream_t st = (hipStream_t)stream;
-    const LayerNormBackArgs a{dy,   h,   weight, mean, rstd, dh,   dx,   dweight, dbias, (float*)workspace,
-                              lddy, ldh, lddh,   lddx, rows, cols, layernorm_back_parts(rows, cols, dtype)};
-    const double n = (double)rows * cols;
-    return run_phase("layernorm_backward", "dion::k_layernorm_backward", 14.0 * n, n * es * (3 + (dh ? 1 : 0)), st,
-                     [&]() { launch_layernorm_backward(dtype, weight_dtype, a, st); });
+    const LayerNormBackArgs a{dy,   h,   weight, mean, rstd, dh,   dx, dweight, dbias, (float*)workspace,
+                              lddy, ldh, lddh,   lddx, rows, cols, 0};
+    return layernorm_backward_call(a, true, dtype, weight_dtype, workspace_bytes, (hipStream_t)stream);
+  });
+}
+
+int dion_layernorm_backward_dx(const void* dy, int64_t lddy, const void* h, int64_t ldh, const void* weight,
+                               const float* mean, const float* rstd, const void* dh, int64_t lddh, void* dx,
+                               int64_t lddx, int64_t rows, int32_t cols, int32_t dtype, int32_t weight_dtype,
+                               void* stream) {
+  return guarded([&]() {
+    const LayerNormBackArgs a{dy,   h,   weight, mean, rstd, dh,   dx, nullptr, nullptr, nullptr,
+                              lddy, ldh, lddh,   lddx, rows, cols, 0};
+    return layernorm_backward_call(a, false, dtype, weight_dtype, 0, (hipStream_t)stream);
   });
 }
 

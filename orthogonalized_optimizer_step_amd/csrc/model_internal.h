@@ -33,8 +33,8 @@ struct LayerNormBackArgs {
   const float* rstd;
   const void* dh;         // may be NULL
   void* dx;
-  void* dweight;
-  void* dbias;            // may be NULL
+  void* dweight;          // NULL: dx alone, no partial sums
+  void* dbias;            // may be NULL, and is without dweight
   float* partial;         // [parts][cols] partial sums of dweight, then the same of dbias
   int64_t lddy, ldh, lddh, lddx;
   int64_t rows;

@@ -57,9 +57,9 @@ def layernorm(x, weight, bias=None, residual=None, eps=1e-5, stream=None):
     return y, (x if h is None else h), mean, rstd
 
 
-def layernorm_backward(dy, h, weight, mean, rstd, dh=None, bias=True, workspace=None, stream=None):
+def layernorm_backward(dy, h, weight, mean, rstd, dh=None, bias=True, workspace=None, stream=None, only_dx=False):
     """Gradients (dx, dweight, dbias) of ``layernorm`` from its ``h``, ``mean`` and ``rstd``; dbias is None without
-    ``bias``.
+    ``bias``, and so are both with ``only_dx``, which forms no sums and needs no workspace.
 
     ``dh`` is the gradient that reaches h itself along the residual stream; dx is the gradient of x and of the residual
     alike."""
@@ -72,6 +72,15 @@ def layernorm_backward(dy, h, weight, mean, rstd, dh=None, bias=True, workspace=
     _vector(weight, "weight", cols, (h.dtype, torch.float32), dev)
     _vector(mean, "mean", rows, _F32, dev)
     _vector(rstd, "rstd", rows, _F32, dev)
+    if only_dx:
+        dx = _new_like(h, h.dtype, stream)
+        rc = lib.dion_layernorm_backward_dx(dy.data_ptr(), lddy, h.data_ptr(), ldh, weight.data_ptr(), mean.data_ptr(),
+                                            rstd.data_ptr(), _ptr(dh), lddh, dx.data_ptr(), cols, rows, cols, code,
+                                            _CODE[weight.dtype], _handle(stream, dev))
+        if rc:
+            check(rc)
+        _used(stream, dy, h, weight, mean, rstd, dh)
+        return dx, None, None
     keep, ws, have = _workspace(lib.dion_layernorm_backward_workspace_size(rows, cols, code), h, workspace, stream)
     dx = _new_like(h, h.dtype, stream)
     dw = _new_like(weight, weight.dtype, stream)
@@ -254,14 +263,14 @@ class _LayerNorm(torch.autograd.Function):
         h, weight, mean, rstd = ctx.saved_tensors
         if dy is None:
             return dh, None, None, dh, None
+        w, b = ctx.needs_input_grad[1], ctx.bias and ctx.needs_input_grad[2]   # frozen ones have no sums formed
 
         def gradients(dy, h, weight, dh):
-            dx, dw, db = layernorm_backward(dy.contiguous(), h, weight, mean, rstd,
-                                            None if dh is None else dh.contiguous(), bias=ctx.bias)
-            return (dx, dw, db) if ctx.bias else (dx, dw)
+            return layernorm_backward(dy.contiguous(), h, weight, mean, rstd, None if dh is None else dh.contiguous(),
+                                      bias=b, only_dx=not (w or b))
 
-        dx, dw, *db = _once(gradients, dy, h, weight, dh)
-        return dx, dw, (db[0] if db else None), (dx if ctx.residual else None), None
+        dx, dw, db = _once(gradients, dy, h, weight, dh)
+        return dx, (dw if w else None), db, (dx if ctx.residual else None), None
 
 
 def layer_norm(x, weight, bias=None, residual=None, eps=1e-5):
