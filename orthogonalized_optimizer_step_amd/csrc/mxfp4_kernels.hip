@@ -538,13 +538,23 @@ __global__ __launch_bounds__(256) void k_mxfp4_align(AlignJobs jobs) {
 // Which kernel takes a product, by its sizes, and whether its operands lie as
 // the tiles need them (us on an MI355X, bf16 output).
 //  - Up to 16 tokens the rows kernel, which reads the weights once at any
-//    alignment (1 x 4096 x 4096: 5.0, 64 x 64 tiles 9.0; 16 x 4096 x 14336:
-//    10.8 against 13.8 with k in four splits), with k split over blocks where
-//    there are few channels (1 x 512 x 14336: 7.4 against 7.9).  Where the tiles
-//    of 64 channels fill the CUs and nothing has to be copied for them, they:
-//    their copies straight into LDS keep more of memory busy, and each of 16
-//    tokens costs the rows kernel reads of its own (1 x 14336 x 4096: 9.7
-//    against 10.6; 16 tokens: 9.7 against 13.5).
+//    alignment, in rounds of 16 channels for each of the 256 CUs, against the tiles
+//    of 64 channels, which fill the CUs in one round up to 16384 and whose copies
+//    straight into LDS keep more of memory busy, where nothing has to be copied for
+//    them.  The tiles from the fourth round on (1 token, k = 4096, rows and tiles: n =
+//    4096 4.7 and 8.7, 8192 7.1 and 9.3, 12288 9.7 and 9.6, 12352 11.0 and 9.7, 14336
+//    11.1 and 9.7, 32768 20 and 17, 131072 71 and 57; k = 14336: 12288 20.4 and 23.5,
+//    12352 24.3 and 23.5, 131072 177 and 165), and from the third on for more than
+//    8 tokens, of which each costs the rows kernel reads of its own (k = 4096: 16
+//    tokens at n = 8192 9.0 and 9.4; at 8256 4 tokens 9.5 and 9.5, 8 10.1 and 9.5, 16
+//    11.3 and 9.5; k = 14336, n = 9216: 4 tokens 21.0 and 23.0, 8 23.4 and 23.1, 12
+//    25.7 and 23.2).
+//    The rows kernel has k split over blocks where there are few channels and more
+//    than 32 stages of it, 14 at least to a block: the join costs 1 to 2 (1 token, one,
+//    two, four and eight splits: 512 x 4096 4.1, 5.3, 5.3, 6.2; 512 x 8192 6.0, 6.3,
+//    6.3, 6.7; 64 x 14336 7.2, 6.4, 5.6, 6.1; 1024 x 14336 7.9, 7.5, 6.8, 7.8; 2048 x
+//    14336 8.8, 8.4, 8.9, 11.0; 512 x 28672 14.4, 10.9, 8.6, 7.9; 512 x 65536 31, 20, 13,
+//    11).
 //  - Otherwise the tile and the split of k with the least of the sum of the
 //    rounds over the 256 CUs at a stage's time (256 k), a tile's fixed time, and
 //    the time of writing and joining the splits' sums.  A stage takes 2.0 for
@@ -562,9 +572,9 @@ struct MxPlan {
 MxPlan mx_plan(int64_t m, int64_t n, int kb, bool aligned) {
   const int stages = (kb + 127) / 128;
   if (m <= 16) {
-    if (aligned && n >= 64 * 208) return {MxPlan::TILE64, 1};
     const int64_t blocks = (n + 15) / 16;
-    return {MxPlan::ROWS, (int)std::max<int64_t>(1, std::min<int64_t>(256 / blocks, stages / 28))};
+    if (aligned && blocks > (m > 8 ? 2 : 3) * 256) return {MxPlan::TILE64, 1};
+    return {MxPlan::ROWS, stages <= 32 ? 1 : (int)std::max<int64_t>(1, std::min<int64_t>(256 / blocks, stages / 14))};
   }
   const auto tiles = [&](int64_t t) { return (m + t - 1) / t * ((n + t - 1) / t); };
   MxPlan best{MxPlan::TILE64, 1};
