@@ -542,9 +542,10 @@ int dion_mxfp4_dequantize(const uint8_t* q, int64_t ldq, const uint8_t* scale, i
  * a: m x k activations, b: n x k weights (output channels as rows), any codes
  * and scales; k even, up to 2^22 (codes of an odd number of columns count one
  * more).  The products are exact and summed in fp32, in an order fixed by m, n,
- * k and whether all rows lie at multiples of 16 bytes.  bias, out and the workspace as of dion_int8_linear; the workspace
- * also holds copies of rows that are not whole multiples of 16 bytes, the
- * scales' among them (k not a multiple of 512), when m > 16. */
+ * k and whether all rows lie at multiples of 16 bytes; one beyond fp32's range is
+ * infinite, one below it 0.  bias, out and the workspace as of dion_int8_linear;
+ * the workspace also holds copies of rows that are not whole multiples of 16
+ * bytes, the scales' among them (k not a multiple of 512), when m > 16. */
 size_t dion_mxfp4_linear_workspace_size(const uint8_t* a, int64_t lda, const uint8_t* a_scale, int64_t ldsa,
                                         const uint8_t* b, int64_t ldb, const uint8_t* b_scale, int64_t ldsb, int64_t m,
                                         int64_t n, int32_t k);
@@ -568,7 +569,10 @@ int dion_mxfp4_linear(const uint8_t* a, int64_t lda, const uint8_t* a_scale, int
  *                beyond them hold -infinity and -1
  *   top          0 .. 1024, with vocab up to 2^19 where it is not 0
  * A row that holds a NaN or +infinity has NaN statistics; a row of -infinity
- * alone has entropy 0 and log probability -infinity.  The workspace holds parts
+ * alone has entropy 0 and log probability -infinity.  No log probability is above
+ * 0 and no entropy below it.  The sums are fp32, in an order that the number of
+ * rows and alternatives decides on (a row's last bits may differ between batches),
+ * the same at every call.  The workspace holds parts
  * of a few rows that are shared out between blocks; sizes whose workspace size
  * is 256 use none (it may be NULL), the others' is 512 at least. */
 size_t dion_token_logprobs_workspace_size(int64_t rows, int32_t vocab, int32_t top, int32_t dtype);

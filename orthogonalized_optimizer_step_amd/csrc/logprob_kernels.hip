@@ -11,14 +11,15 @@
 // negative and no log probability above 0.  s holds what lies beside the largest
 // logit to half a unit of 1 for each addition that its 1 takes part in: a few
 // 2^-24, absolute, is what log s and the entropy of a nearly certain row are off
-// by.  Where a factor is u itself it is -200 (in powers of two) at
-// least: below that exp(u) is 0 in fp32, and so is the product (u = -inf of a
-// masked entry among them).
+// by.  Where a factor is u itself it is -200 (in powers of two) at least: below
+// that exp(u) is 0 in fp32, and so is the product (u = -inf of a masked entry
+// among them).  How many threads share a row depends on the number of rows and
+// of alternatives, and with it the order of the sums: a row's last bits do too.
 //
-// Reading bounds long batches: 8192 x 128256 bf16 take 355 us without
-// alternatives (5.9 TB/s; 5.8 is what a pass that only reads reaches in order),
-// 381 to 396 with 64 of them; the gradient of 4096 x 50257 164 to 174 (4.7 to
-// 5.0 TB/s read and written).
+// Reading bounds long batches: 8192 x 128256 bf16 take 355 to 375 us without
+// alternatives (5.6 to 5.9 TB/s; torch's sums and maxima of as long rows read at 5.8
+// to 6.2), 382 to 396 with 64 of them; the gradient of 4096 x 50257 164 to 175 (4.7
+// to 5.0 TB/s read and written).
 #include <algorithm>
 
 #include "model_internal.h"
@@ -670,8 +671,9 @@ void launch_rows(const LogprobArgs& a, int lg, hipStream_t s) {
   else hipLaunchKernelGGL((k_logprobs<Z, NT, TOP, false>), grid, dim3(NT), 0, s, a, lg);
 }
 
-// Threads of a row: 256, of which a CU holds eight rows, or 1024 where there is a
-// row to a CU at most and it is long, or the lists of 256 do not hold k (us,
+// Threads of a row: 256, of which a CU holds four rows (104 to 128 registers; five
+// of fp32 without alternatives, 88), or 1024 where there is a row to a CU at most
+// and it is long, or the lists of 256 do not hold k (us,
 // bf16, 256 and 1024 threads: 4096 x 50257 90 and 149, with 64 alternatives 116
 // and 254; 300 x 128256 22 and 26, 33 and 38; 64 x 128256 16.5 and 12.0, 26.1 and
 // 19.8; 64 x 65536 10.5 and 8.2, 18.4 and 15.6; 64 x 32001 7.1 and 7.1, 13.7 and
