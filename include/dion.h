@@ -497,7 +497,7 @@ int dion_distill_topk_step(const void* logits, int64_t ldz, const void* teacher,
  * The sums are fp32: a row whose squares overflow has rstd 0 and y = bias (NaN
  * where s - mean overflows too), one whose sum does is NaN.  One that holds an
  * infinity or a NaN has y and rstd NaN and a mean that is no number; with eps = 0
- * y of equal elements is NaN. */
+ * the y of equal elements is not defined. */
 int dion_layernorm(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight, const void* bias,
                    void* h, int64_t ldh, void* y, int64_t ldy, float* mean, float* rstd, int64_t rows, int32_t cols,
                    int32_t dtype, int32_t weight_dtype, float eps, void* stream);

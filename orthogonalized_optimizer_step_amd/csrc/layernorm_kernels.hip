@@ -178,8 +178,8 @@ __global__ __launch_bounds__(1024) void k_layernorm_long(LayerNormArgs a, bool w
 // chunks are asked for before this row's dx is written, and the terms of
 // dweight and dbias stay in registers until the end: one partial sum of each
 // for each block, in the order of its rows, joined over blocks by
-// k_layernorm_join (neither is written where no dweight is asked for).  64 threads with two chunks each hold more than 128
-// registers, and spill at the bound of the others.
+// k_layernorm_join (not where no dweight is asked for).  64 threads with two
+// chunks each hold more than 128 registers, and spill at the bound of the others.
 template <typename T, int NT, int CH>
 __global__ __launch_bounds__(block_of(NT), NT == 64 && CH == 2 ? 1 : 4) void k_layernorm_backward(LayerNormBackArgs a, bool w32) {
   typedef Chunk<T> C;

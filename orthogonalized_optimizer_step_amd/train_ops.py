@@ -11,7 +11,8 @@ Tensors are on the current GPU.  Matrices may have leading dimensions that
 flatten into rows and rows further apart than they are long (a padded
 vocabulary, a slice of columns); the elements of a row are contiguous.  With
 ``stream`` the work runs there, outputs and workspaces are allocated for it,
-and every tensor is recorded as used by it.
+and every tensor is recorded as used by it; the caller makes that stream wait
+for whatever else still writes them.
 """
 from __future__ import annotations
 
